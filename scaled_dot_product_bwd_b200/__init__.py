@@ -19,6 +19,8 @@ from .binding import (  # noqa: F401
     sdpa_bwd_noalloc,
     sdpa_bwd_varlen,
     sdpa_bwd_workspace_size,
+    sdpa_cache_append,
+    sdpa_cache_gather,
     sdpa_debug_wait_timeout,
     sdpa_exp2_fma,
     sdpa_fire_backward,
@@ -26,7 +28,12 @@ from .binding import (  # noqa: F401
     sdpa_fwd,
     sdpa_fwd_varlen,
     sdpa_read_device_status,
+    sdpa_rope,
+    sdpa_rope_frequencies,
     sdpa_set_wait_limit_ns,
+    sdpa_spec_verify,
     sdpa_status_string,
     sdpa_t5_bucket,
+    sdpa_tree_fwd,
+    sdpa_tree_fwd_workspace_size,
 )

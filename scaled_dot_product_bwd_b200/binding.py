@@ -31,7 +31,12 @@ EXPORTED = ("sdpa_fwd", "sdpa_fwd_varlen", "sdpa_bwd", "sdpa_bwd_phases", "sdpa_
             "sdpa_bwd_bias_grad", "sdpa_bwd_bias_grad_workspace_size", "sdpa_t5_bucket",
             "sdpa_exp2_fma", "sdpa_read_device_status", "sdpa_set_wait_limit_ns",
             "sdpa_debug_wait_timeout", "sdpa_status_string", "sdpa_fire_table",
-            "sdpa_fire_backward_workspace_size", "sdpa_fire_backward")
+            "sdpa_fire_backward_workspace_size", "sdpa_fire_backward", "sdpa_rope",
+            "sdpa_rope_frequencies", "sdpa_cache_append", "sdpa_cache_gather", "sdpa_tree_fwd",
+            "sdpa_tree_fwd_workspace_size", "sdpa_spec_verify")
+
+CACHE_BF16, CACHE_E4M3 = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class SdpaError(RuntimeError):
@@ -68,6 +73,39 @@ class Varlen(ctypes.Structure):
     _fields_ = [("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
                 ("max_seqlen_q", ctypes.c_int64), ("max_seqlen_k", ctypes.c_int64),
                 ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in
+                 ("B", "L", "Hq", "Hkv", "d", "q_b", "q_l", "q_h", "k_b", "k_l", "k_h",
+                  "qo_b", "qo_l", "qo_h", "ko_b", "ko_l", "ko_h")]
+                + [("positions", ctypes.c_void_p), ("pos_b", ctypes.c_int64),
+                   ("offset", ctypes.c_int64), ("freqs", ctypes.c_void_p),
+                   ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                   ("inverse", ctypes.c_int32), ("amplitude", ctypes.c_float)])
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [("format", ctypes.c_int32)]
+                + [(n, ctypes.c_int64) for n in
+                   ("num_pages", "page_size", "Hkv", "d", "stride_page", "stride_head",
+                    "stride_row", "scale_stride_page", "scale_stride_head")])
+
+
+class Tree(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "T", "max_nodes", "Hq", "q_t", "q_h", "o_t",
+                                               "o_h")]
+                + [(n, ctypes.c_void_p) for n in ("cu_nodes", "ctx_lens", "page_table")]
+                + [("table_width", ctypes.c_int64), ("table_b", ctypes.c_int64),
+                   ("tree_mask", ctypes.c_void_p), ("window_left", ctypes.c_int64)])
+
+
+class Verify(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "N", "V", "target_b", "target_n", "draft_b",
+                                               "draft_n")]
+                + [(n, ctypes.c_void_p) for n in ("target", "draft", "tokens", "parents",
+                                                  "u_accept", "u_sample")])
 
 
 _lib = None
@@ -124,6 +162,24 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sdpa_fire_backward_workspace_size.restype = sz
     lib.sdpa_fire_backward.argtypes = [fp, i64, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.sdpa_fire_backward.restype = i32
+    cp = ctypes.POINTER(KvCache)
+    f64 = ctypes.c_double
+    lib.sdpa_rope.argtypes = [ctypes.POINTER(RopeDesc), vp, vp, vp, vp, vp]
+    lib.sdpa_rope.restype = i32
+    lib.sdpa_rope_frequencies.argtypes = [i32, f64, i32, f64, i64, f64, f64,
+                                          ctypes.POINTER(f64), ctypes.POINTER(f32)]
+    lib.sdpa_rope_frequencies.restype = i32
+    lib.sdpa_cache_append.argtypes = [cp, vp, vp, i64, i64, i64, vp, vp]
+    lib.sdpa_cache_append.restype = i32
+    lib.sdpa_cache_gather.argtypes = [cp, i64, vp, i64, i64, vp, i64, vp, vp, i64, i64, vp]
+    lib.sdpa_cache_gather.restype = i32
+    tp = ctypes.POINTER(Tree)
+    lib.sdpa_tree_fwd.argtypes = [tp, cp, vp, bp, f32, vp, vp, vp, sz, vp]
+    lib.sdpa_tree_fwd.restype = i32
+    lib.sdpa_tree_fwd_workspace_size.argtypes = [tp, cp]
+    lib.sdpa_tree_fwd_workspace_size.restype = sz
+    lib.sdpa_spec_verify.argtypes = [ctypes.POINTER(Verify), vp, vp, vp, vp]
+    lib.sdpa_spec_verify.restype = i32
     lib.sdpa_status_string.argtypes = [i32]
     lib.sdpa_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -546,3 +602,267 @@ def sdpa_fire_backward(w1, b1, w2, b2, c, threshold, Lq, Lk, d_table):
 
 def sdpa_status_string(status: int) -> str:
     return load_library().sdpa_status_string(int(status)).decode()
+
+
+# ------------------------------------------------------------------- serving
+def _on_device(ref: torch.Tensor, **tensors):
+    """Every given tensor on ref's GPU, which is the current one."""
+    dev = ref.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, which is not the current CUDA device")
+    for n, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, not on {dev}")
+
+
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, *shape: int):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {str(dtype)[6:]} {list(shape)}")
+
+
+def _heads(t: torch.Tensor, name: str, dims: int):
+    if t.dtype != torch.bfloat16 or t.dim() != dims or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be bf16 with {dims} dimensions and a contiguous head_dim")
+
+
+def _stride8(t: torch.Tensor, i: int) -> int:
+    """Stride of dimension i; one that is never taken may be anything."""
+    return t.stride(i) if t.shape[i] > 1 else 8
+
+
+def sdpa_rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, original_length=0,
+                          beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """(freqs float64 [rot / 2] on ``device``, amplitude) for sdpa_rope: radians per position,
+    unscaled or scaled for longer contexts ("linear", "ntk", "yarn"; see include/sdpa.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = (ctypes.c_double * max(int(rot) // 2, 1))()
+    amplitude = ctypes.c_float()
+    _check(load_library().sdpa_rope_frequencies(int(rot), float(base), ROPE_SCALINGS[scaling],
+                                                float(factor), int(original_length),
+                                                float(beta_fast), float(beta_slow), out,
+                                                ctypes.byref(amplitude)), "sdpa_rope_frequencies")
+    return torch.tensor(list(out), dtype=torch.float64, device=device), amplitude.value
+
+
+def sdpa_rope(q, k, freqs, positions=None, *, offset=0, interleaved=False, inverse=False,
+              amplitude=1.0, out_q=None, out_k=None):
+    """q and k turned by their positions (see sdpa_rope in include/sdpa.h): (out_q, out_k).
+
+    q [B, L, Hq, d] and k [B, L, Hkv, d], or packed [T, Hq, d] and [T, Hkv, d]; k may be None.
+    ``positions`` int32 [B, L] (or [T]); without it row l has position ``offset`` + l.
+    ``inverse`` turns back: the gradient.  out_q=q, out_k=k works in place.
+    """
+    lib = load_library()
+    packed = q.dim() == 3
+    _heads(q, "q", 3 if packed else 4)
+    _on_device(q, k=k, freqs=freqs, positions=positions, out_q=out_q, out_k=out_k)
+    B, (L, Hq, d) = (1 if packed else q.shape[0]), q.shape[-3:]
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float64 vector")
+    pos_b = L
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.shape != q.shape[:-2]:
+            raise ValueError("positions must be int32 [B, L] (packed: [T])")
+        if L > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions must be contiguous along the sequence")
+        pos_b = L if packed or B == 1 else positions.stride(0)
+    out_q = torch.empty(q.shape, device=q.device, dtype=q.dtype) if out_q is None else out_q
+    if k is not None:
+        _heads(k, "k", q.dim())
+        if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d:
+            raise ValueError(f"k shape {tuple(k.shape)} does not match q {tuple(q.shape)}")
+        out_k = torch.empty(k.shape, device=k.device, dtype=k.dtype) if out_k is None else out_k
+    strides = []
+    for t, ref, n in ((q, q, "q"), (k, k, "k"), (out_q, q, "out_q"), (out_k if k is not None else None,
+                                                                     k, "out_k")):
+        if t is None:
+            strides += [0, 0, 0]
+            continue
+        _heads(t, n, q.dim())
+        if t.shape != ref.shape:
+            raise ValueError(f"{n} shape {tuple(t.shape)} is not {tuple(ref.shape)}")
+        strides += [8 if packed else _stride8(t, 0), _stride8(t, -3), _stride8(t, -2)]
+    if q.numel() == 0:
+        return out_q, (out_k if k is not None else None)
+    r = RopeDesc(B, L, Hq, 0 if k is None else k.shape[-2], d, *strides,
+                 positions.data_ptr() if positions is not None else None, pos_b, int(offset),
+                 freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0,
+                 1 if inverse else 0, float(amplitude))
+    _check(lib.sdpa_rope(ctypes.byref(r), _ptr(q), _ptr(k), _ptr(out_q), _ptr(out_k), _stream(q)),
+           "sdpa_rope")
+    return out_q, (out_k if k is not None else None)
+
+
+def make_cache(k_cache, v_cache, k_scale=None, v_scale=None) -> KvCache:
+    """Descriptor of a paged cache [num_pages, Hkv, page_size, d]: bf16, or float8_e4m3fn with
+    uint8 scale exponents [num_pages, Hkv, page_size]."""
+    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError("a cache is bf16 or float8_e4m3fn")
+    if (k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype
+            or v_cache.stride() != k_cache.stride() or k_cache.stride(-1) != 1):
+        raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] alike in "
+                         "type, shape and strides, with a contiguous head_dim")
+    _on_device(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    P, H, page, d = k_cache.shape
+    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+    ss = [0, 0]
+    if e4m3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        if (k_scale.dtype != torch.uint8 or tuple(k_scale.shape) != (P, H, page)
+                or k_scale.stride(-1) != 1 or v_scale.dtype != torch.uint8
+                or v_scale.shape != k_scale.shape or v_scale.stride() != k_scale.stride()):
+            raise ValueError("k_scale and v_scale must be uint8 [num_pages, Hkv, page_size] alike "
+                             "in strides, with contiguous rows")
+        ss = [k_scale.stride(i) if k_scale.shape[i] > 1 else 16 for i in (0, 1)]
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("a bf16 cache has no scales")
+    st = [k_cache.stride(i) if k_cache.shape[i] > 1 else 16 for i in (0, 1, 2)]
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+                   v_scale.data_ptr() if e4m3 else None, CACHE_E4M3 if e4m3 else CACHE_BF16,
+                   P, page, H, d, *st, *ss)
+
+
+def _table(page_table: torch.Tensor, B: int):
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError("page_table must be int32 [B, pages] with contiguous rows")
+    return page_table.shape[1], page_table.stride(0) if B > 1 else page_table.shape[1]
+
+
+def sdpa_cache_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
+    """Rows k, v [T, Hkv, d] into the cache at slots int64 [T] (page * page_size + row;
+    negative: skipped), quantised if the cache is e4m3 (see sdpa_cache_append)."""
+    lib = load_library()
+    c = make_cache(k_cache, v_cache, k_scale, v_scale)
+    _heads(k, "k", 3)
+    _same_layout(v, k, "v")
+    _on_device(k_cache, k=k, v=v, slots=slots)
+    if k.shape[1] != c.Hkv or k.shape[2] != c.d:
+        raise ValueError(f"k {tuple(k.shape)} does not fit the cache's heads")
+    _vector(slots, "slots", torch.int64, k.shape[0])
+    _check(lib.sdpa_cache_append(ctypes.byref(c), _ptr(k), _ptr(v), k.shape[0], _stride8(k, 0),
+                                 _stride8(k, 1), _ptr(slots), _stream(k)), "sdpa_cache_append")
+
+
+def sdpa_cache_gather(k_cache, v_cache, page_table, cu_seqlens, total, k_scale=None, v_scale=None,
+                      k=None, v=None):
+    """The cached sequences as packed bf16 (k, v) [total, Hkv, d], sequence b's first
+    cu_seqlens[b + 1] - cu_seqlens[b] positions at its rows (see sdpa_cache_gather)."""
+    lib = load_library()
+    c = make_cache(k_cache, v_cache, k_scale, v_scale)
+    _on_device(k_cache, page_table=page_table, cu_seqlens=cu_seqlens, k=k, v=v)
+    B = cu_seqlens.numel() - 1
+    _vector(cu_seqlens, "cu_seqlens", torch.int32, B + 1)
+    width, table_b = _table(page_table, B)
+    shape = (int(total), c.Hkv, c.d)
+    k = torch.empty(shape, device=k_cache.device, dtype=torch.bfloat16) if k is None else k
+    v = torch.empty(shape, device=k_cache.device, dtype=torch.bfloat16) if v is None else v
+    _heads(k, "k", 3)
+    if tuple(k.shape) != shape:
+        raise ValueError(f"k must be {list(shape)}")
+    _same_layout(v, k, "v")
+    _check(lib.sdpa_cache_gather(ctypes.byref(c), B, _ptr(page_table), width, table_b,
+                                 _ptr(cu_seqlens), int(total), _ptr(k), _ptr(v), _stride8(k, 0),
+                                 _stride8(k, 1), _stream(k_cache)), "sdpa_cache_gather")
+    return k, v
+
+
+def sdpa_tree_fwd(q, k_cache, v_cache, page_table, ctx_lens, cu_nodes, max_nodes, *,
+                  k_scale=None, v_scale=None, tree_mask=None, window_left=-1, t5_table=None,
+                  t5_num_buckets=32, t5_max_distance=128, t5_bidirectional=True,
+                  alibi_slopes=None, scale=None, out=None, lse=None, workspace=None):
+    """O [T, Hq, d], LSE [Hq, T]: each sequence's nodes over its cached context and over the
+    nodes that ``tree_mask`` (int64 [T], bit j: sees node j; None: a chain) shows them.  One node
+    per sequence is plain decoding.  The nodes' own keys are in the cache already, at positions
+    ctx_lens[b] and on (see sdpa_tree_fwd in include/sdpa.h)."""
+    lib = load_library()
+    c = make_cache(k_cache, v_cache, k_scale, v_scale)
+    _heads(q, "q", 3)
+    _on_device(k_cache, q=q, page_table=page_table, ctx_lens=ctx_lens, cu_nodes=cu_nodes,
+               tree_mask=tree_mask, t5_table=t5_table, alibi_slopes=alibi_slopes, out=out, lse=lse,
+               workspace=workspace)
+    T, Hq, d = q.shape
+    if d != c.d:
+        raise ValueError("q and the cache differ in head_dim")
+    B = ctx_lens.numel()
+    _vector(ctx_lens, "ctx_lens", torch.int32, B)
+    _vector(cu_nodes, "cu_nodes", torch.int32, B + 1)
+    if tree_mask is not None:
+        _vector(tree_mask, "tree_mask", torch.int64, T)
+    width, table_b = _table(page_table, B)
+    out = torch.empty(q.shape, device=q.device, dtype=q.dtype) if out is None else out
+    _heads(out, "out", 3)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = torch.empty(Hq, T, device=q.device, dtype=torch.float32)
+    _vector(lse, "lse", torch.float32, Hq, T)
+    t = Tree(B, T, int(max_nodes), Hq, _stride8(q, 0), _stride8(q, 1), _stride8(out, 0),
+             _stride8(out, 1), cu_nodes.data_ptr(), ctx_lens.data_ptr(), page_table.data_ptr(),
+             width, table_b, tree_mask.data_ptr() if tree_mask is not None else None,
+             int(window_left))
+    bd = make_bias(None, t5_table, t5_num_buckets, t5_max_distance, t5_bidirectional,
+                   (B, Hq, 0, 0), alibi_slopes)
+    if workspace is None:
+        need = int(lib.sdpa_tree_fwd_workspace_size(ctypes.byref(t), ctypes.byref(c)))
+        workspace = torch.empty(max(need, 256), device=q.device, dtype=torch.uint8)
+    sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    st = lib.sdpa_tree_fwd(ctypes.byref(t), ctypes.byref(c), _ptr(q), ctypes.byref(bd), sc,
+                           _ptr(out), _ptr(lse), _ptr(workspace),
+                           workspace.numel() * workspace.element_size(), _stream(q))
+    _check(st, "sdpa_tree_fwd")
+    return out, lse
+
+
+def sdpa_tree_fwd_workspace_size(q, k_cache, v_cache, page_table, ctx_lens, cu_nodes, max_nodes, *,
+                                 k_scale=None, v_scale=None) -> int:
+    """Bytes of the workspace of sdpa_tree_fwd for these tensors (0: they do not fit together)."""
+    c = make_cache(k_cache, v_cache, k_scale, v_scale)
+    width, table_b = _table(page_table, ctx_lens.numel())
+    st = (_stride8(q, 0), _stride8(q, 1))
+    t = Tree(ctx_lens.numel(), q.shape[0], int(max_nodes), q.shape[1], *st, *st,
+             cu_nodes.data_ptr(), ctx_lens.data_ptr(), page_table.data_ptr(), width, table_b, None,
+             -1)
+    return int(load_library().sdpa_tree_fwd_workspace_size(ctypes.byref(t), ctypes.byref(c)))
+
+
+def sdpa_spec_verify(target, draft, tokens, parents, u_accept, u_sample):
+    """(path int32 [B, N], accepted int32 [B], next_token int32 [B]) of drafted trees, by
+    rejection sampling with the given uniform numbers (see sdpa_spec_verify in include/sdpa.h).
+
+    target, draft float32 [B, N, V]: the distributions after each node (draft may be None when
+    N = 1); tokens int32 [B, N]; parents int32 [B, N] or None (a chain); u_accept float32 [B, N];
+    u_sample float32 [B].
+    """
+    lib = load_library()
+    if target.dtype != torch.float32 or target.dim() != 3 or target.stride(2) != 1:
+        raise ValueError("target must be float32 [B, N, V] with a contiguous vocabulary")
+    _on_device(target, draft=draft, tokens=tokens, parents=parents, u_accept=u_accept,
+               u_sample=u_sample)
+    B, N, V = target.shape
+    if draft is not None:
+        if draft.dtype != torch.float32 or draft.shape != target.shape or draft.stride(2) != 1:
+            raise ValueError("draft must be float32 [B, N, V] with a contiguous vocabulary")
+    if N > 1:
+        if draft is None:
+            raise ValueError("draft distributions are needed when there are drafted nodes")
+        _vector(tokens, "tokens", torch.int32, B, N)
+        _vector(u_accept, "u_accept", torch.float32, B, N)
+    if parents is not None:
+        _vector(parents, "parents", torch.int32, B, N)
+    _vector(u_sample, "u_sample", torch.float32, B)
+    i32 = dict(device=target.device, dtype=torch.int32)
+    path, accepted, token = torch.empty(B, N, **i32), torch.empty(B, **i32), torch.empty(B, **i32)
+    ds = (draft.stride(0), draft.stride(1)) if draft is not None else (0, 0)
+    s = Verify(B, N, V, target.stride(0), target.stride(1), *ds, target.data_ptr(),
+               draft.data_ptr() if draft is not None else None,
+               tokens.data_ptr() if tokens is not None else None,
+               parents.data_ptr() if parents is not None else None,
+               u_accept.data_ptr() if u_accept is not None else None, u_sample.data_ptr())
+    _check(lib.sdpa_spec_verify(ctypes.byref(s), _ptr(path), _ptr(accepted), _ptr(token),
+                                _stream(target)), "sdpa_spec_verify")
+    return path, accepted, token

@@ -1,0 +1,466 @@
+// serve_api.cuh -- host side of the serving entry points declared in
+// include/sdpa.h: rotary positions, the paged cache, tree attention over it
+// and the verification of drafted tokens.  Part of the library's one
+// translation unit (included by sdpa_api.cu, whose helpers it uses).
+#pragma once
+
+#include "kv_cache.cuh"
+#include "rope.cuh"
+#include "spec_verify.cuh"
+#include "tree_fwd.cuh"
+
+namespace {
+
+bool good_stride(int64_t v, int64_t multiple) {
+  return v > 0 && v % multiple == 0 && v < (1ll << 38);
+}
+
+// ------------------------------------------------------------------ rotary
+template <int D>
+cudaError_t launch_rope(const RopeArgs& a, int mode, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>((a.tokens + a.per_cta - 1) / a.per_cta);
+  switch (mode) {
+    case kRopeHalf: rope_kernel<D, kRopeHalf><<<grid, kRopeThreads, 0, st>>>(a); break;
+    case kRopeInterleaved: rope_kernel<D, kRopeInterleaved><<<grid, kRopeThreads, 0, st>>>(a); break;
+    default: rope_kernel<D, kRopeHalfAny><<<grid, kRopeThreads, 0, st>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------- cache
+sdpa_status_t check_cache(const sdpa_kv_cache* c, CacheView& v) {
+  if (!c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return SDPA_ERR_INVALID_ARG;
+  if (c->format != SDPA_CACHE_BF16 && c->format != SDPA_CACHE_E4M3) return SDPA_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->page_size < 1 || c->Hkv < 1) return SDPA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return SDPA_ERR_UNSUPPORTED;
+  const int64_t ps = c->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return SDPA_ERR_UNSUPPORTED;
+  if (c->Hkv > 65535 || c->num_pages >= (1ll << 31) - 1) return SDPA_ERR_UNSUPPORTED;
+  const bool e4m3 = c->format == SDPA_CACHE_E4M3;
+  const int64_t mult = e4m3 ? 16 : 8;
+  if (!good_stride(c->stride_page, mult) || !good_stride(c->stride_head, mult) ||
+      !good_stride(c->stride_row, mult))
+    return SDPA_ERR_INVALID_ARG;
+  if (e4m3) {
+    if (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+      return SDPA_ERR_INVALID_ARG;
+    if (!good_stride(c->scale_stride_page, 16) || !good_stride(c->scale_stride_head, 16))
+      return SDPA_ERR_INVALID_ARG;
+  }
+  v = CacheView{};
+  v.k = c->k;
+  v.v = c->v;
+  v.ks = e4m3 ? c->k_scale : nullptr;
+  v.vs = e4m3 ? c->v_scale : nullptr;
+  v.num_pages = c->num_pages;
+  v.page_size = static_cast<int>(ps);
+  for (v.page_shift = 0; (1 << v.page_shift) < ps;) ++v.page_shift;
+  v.Hkv = static_cast<int>(c->Hkv);
+  v.s_page = c->stride_page;
+  v.s_head = c->stride_head;
+  v.s_row = c->stride_row;
+  v.ss_page = c->scale_stride_page;
+  v.ss_head = c->scale_stride_head;
+  return SDPA_OK;
+}
+
+// 4-D map of a cache tensor along (head_dim, row, head, page): boxes of
+// box_rows rows of one head of one page, 128 bytes (or a whole 64-byte row)
+// wide, swizzled as wide as they are.  A page past the last reads as zeros.
+bool make_cache_map(CUtensorMap* m, const void* base, const sdpa_kv_cache* c, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const bool e4m3 = c->format == SDPA_CACHE_E4M3;
+  const int64_t cell = e4m3 ? 1 : 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->page_size),
+                        static_cast<cuuint64_t>(c->Hkv), static_cast<cuuint64_t>(c->num_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->stride_row * cell),
+                           static_cast<cuuint64_t>(c->stride_head * cell),
+                           static_cast<cuuint64_t>(c->stride_page * cell)};
+  const int64_t line = c->d * cell < 128 ? c->d * cell : 128;
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(line / cell), static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// -------------------------------------------------------------------- tree
+constexpr int kTreeRows = 16;
+
+struct TreePlan {
+  size_t prefix, ml, o, total;
+};
+
+sdpa_status_t check_tree(const sdpa_tree* t, const sdpa_kv_cache* c, CacheView& v, TreePlan& pl) {
+  sdpa_status_t st = check_cache(c, v);
+  if (st != SDPA_OK) return st;
+  if (!t || t->B < 1 || t->T < 1 || t->max_nodes < 1 || t->Hq < 1) return SDPA_ERR_INVALID_ARG;
+  if (t->Hq % c->Hkv != 0) return SDPA_ERR_INVALID_ARG;
+  if (t->max_nodes > kTreeMaxNodes || t->B > 65535 || t->Hq > 65535 || t->T >= (1ll << 30))
+    return SDPA_ERR_UNSUPPORTED;
+  if (!t->cu_nodes || !t->ctx_lens || !t->page_table || t->table_width < 1 ||
+      t->table_b < t->table_width)
+    return SDPA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(t->cu_nodes) & 3u) || (reinterpret_cast<uintptr_t>(t->ctx_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(t->page_table) & 3u) || (reinterpret_cast<uintptr_t>(t->tree_mask) & 7u))
+    return SDPA_ERR_INVALID_ARG;
+  // positions, and the tiles of one sequence, are counted in 32 bits
+  if (t->table_width > (1ll << 30) / c->page_size) return SDPA_ERR_UNSUPPORTED;
+  const int64_t tiles = (t->table_width * c->page_size + 63) / 64;
+  const int64_t blocks = (t->max_nodes * (t->Hq / c->Hkv) + kTreeRows - 1) / kTreeRows;
+  if (tiles * blocks >= (1ll << 31) / c->Hkv) return SDPA_ERR_UNSUPPORTED;
+  if (!good_stride(t->q_t, 8) || !good_stride(t->q_h, 8) || !good_stride(t->o_t, 8) ||
+      !good_stride(t->o_h, 8))
+    return SDPA_ERR_INVALID_ARG;
+  pl.prefix = 0;
+  pl.ml = round256(static_cast<size_t>(t->B + 1) * sizeof(int64_t));
+  pl.o = pl.ml + round256(static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeRows * sizeof(float2));
+  pl.total = pl.o + static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeRows * c->d * sizeof(float);
+  return SDPA_OK;
+}
+
+template <int D, int FMT, int BIAS>
+cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                        cudaStream_t st) {
+  using Tile = TreeTile<D, FMT>;
+  constexpr int kSmem = Tile::kStages * Tile::kStage + kTreeRows * (D + 4) * 4;
+  auto kern = tree_fwd_kernel<D, FMT, BIAS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int grid = std::min(2 * sms, kTreeMaxCtas);
+  kern<<<grid, kTreeThreads, kSmem, st>>>(a, mk, mv);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // no (sequence, head) longer than one tile can span CTAs
+  if (a.width * a.page_size <= Tile::kKeys) return cudaSuccess;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a.max_nodes * a.Hq + kTreeJoinWarps - 1) / kTreeJoinWarps, a.B);
+  cfg.blockDim = dim3(kTreeJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, FMT>, a, grid);
+}
+
+template <int D, int FMT>
+cudaError_t dispatch_tree_bias(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                               cudaStream_t st) {
+  return a.alibi_slopes || a.t5_table ? launch_tree<D, FMT, 1>(a, mk, mv, st)
+                                      : launch_tree<D, FMT, 0>(a, mk, mv, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+sdpa_status_t sdpa_rope(const sdpa_rope_desc* r, const void* q, const void* k, void* q_out,
+                        void* k_out, void* stream) {
+  if (!r || r->B < 1 || r->L < 1 || r->Hq < 1 || r->Hkv < 0) return SDPA_ERR_INVALID_ARG;
+  if (r->d != 64 && r->d != 128) return SDPA_ERR_UNSUPPORTED;
+  if (r->rot < 2 || r->rot > r->d || r->rot % 2 != 0) return SDPA_ERR_INVALID_ARG;
+  if (r->Hq > 65535 || r->Hkv > 65535 || r->B >= (1ll << 31) || r->L >= (1ll << 31) / r->B)
+    return SDPA_ERR_UNSUPPORTED;
+  if (!std::isfinite(r->amplitude)) return SDPA_ERR_INVALID_ARG;
+  if (!r->freqs || (reinterpret_cast<uintptr_t>(r->freqs) & 7u) ||
+      (reinterpret_cast<uintptr_t>(r->positions) & 3u) || (r->positions && r->B > 1 && r->pos_b < r->L))
+    return SDPA_ERR_INVALID_ARG;
+  if (!q || !q_out || !aligned16(q) || !aligned16(q_out)) return SDPA_ERR_INVALID_ARG;
+  const int64_t sq[] = {r->q_b, r->q_l, r->q_h, r->qo_b, r->qo_l, r->qo_h};
+  for (int64_t v : sq)
+    if (!good_stride(v, 8)) return SDPA_ERR_INVALID_ARG;
+  RopeArgs a{};
+  if (r->Hkv > 0) {
+    if (!k || !k_out || !aligned16(k) || !aligned16(k_out)) return SDPA_ERR_INVALID_ARG;
+    const int64_t sk[] = {r->k_b, r->k_l, r->k_h, r->ko_b, r->ko_l, r->ko_h};
+    for (int64_t v : sk)
+      if (!good_stride(v, 8)) return SDPA_ERR_INVALID_ARG;
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.ko = static_cast<__nv_bfloat16*>(k_out);
+    a.k_b = r->k_b;
+    a.k_l = r->k_l;
+    a.k_h = r->k_h;
+    a.ko_b = r->ko_b;
+    a.ko_l = r->ko_l;
+    a.ko_h = r->ko_h;
+  }
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.qo = static_cast<__nv_bfloat16*>(q_out);
+  a.q_b = r->q_b;
+  a.q_l = r->q_l;
+  a.q_h = r->q_h;
+  a.qo_b = r->qo_b;
+  a.qo_l = r->qo_l;
+  a.qo_h = r->qo_h;
+  a.positions = r->positions;
+  a.pos_b = r->pos_b;
+  a.offset = r->offset;
+  a.freqs = r->freqs;
+  a.L = static_cast<int>(r->L);
+  a.Hq = static_cast<int>(r->Hq);
+  a.H = static_cast<int>(r->Hq + r->Hkv);
+  a.tokens = r->B * r->L;
+  a.half = r->rot / 2;
+  a.amplitude = r->amplitude;
+  a.sign = r->inverse ? -1.f : 1.f;
+  const int sms = sm_count();
+  if (sms <= 0) return SDPA_ERR_CUDA;
+  // one token per CTA until every SM has its CTAs, then four share a CTA
+  a.per_cta = a.tokens <= 8ll * sms ? 1 : kRopeTokens;
+  const int mode = r->interleaved ? kRopeInterleaved : (a.half % 8 == 0 ? kRopeHalf : kRopeHalfAny);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = r->d == 128 ? launch_rope<128>(a, mode, cs) : launch_rope<64>(a, mode, cs);
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+sdpa_status_t sdpa_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor,
+                                    int64_t original_length, double beta_fast, double beta_slow,
+                                    double* freqs, float* amplitude) {
+  if (rot < 2 || rot % 2 != 0 || !std::isfinite(base) || base <= 1.0 || !freqs || !amplitude)
+    return SDPA_ERR_INVALID_ARG;
+  if (scaling < SDPA_ROPE_PLAIN || scaling > SDPA_ROPE_YARN) return SDPA_ERR_INVALID_ARG;
+  if (scaling != SDPA_ROPE_PLAIN && (!std::isfinite(factor) || factor < 1.0))
+    return SDPA_ERR_INVALID_ARG;
+  if (scaling == SDPA_ROPE_NTK && rot < 4) return SDPA_ERR_INVALID_ARG;
+  if (scaling == SDPA_ROPE_YARN &&
+      (original_length < 1 || !std::isfinite(beta_fast) || !(beta_slow > 0.0) ||
+       !(beta_fast > beta_slow)))
+    return SDPA_ERR_INVALID_ARG;
+  const double b = scaling == SDPA_ROPE_NTK ? base * std::pow(factor, rot / (rot - 2.0)) : base;
+  *amplitude = 1.f;
+  // YARN: the pair index at which `turns` turns fit into original_length positions
+  double lo = 0.0, hi = 0.0;
+  if (scaling == SDPA_ROPE_YARN) {
+    auto index_of = [&](double turns) {
+      return rot * std::log(static_cast<double>(original_length) / (turns * 2.0 * 3.14159265358979323846)) /
+             (2.0 * std::log(base));
+    };
+    lo = std::max(std::floor(index_of(beta_fast)), 0.0);
+    hi = std::min(std::ceil(index_of(beta_slow)), rot - 1.0);
+    if (hi <= lo) hi = lo + 0.001;
+    *amplitude = static_cast<float>(0.1 * std::log(factor) + 1.0);
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = std::pow(b, -2.0 * i / rot);
+    double g = f;
+    if (scaling == SDPA_ROPE_LINEAR) g = f / factor;
+    if (scaling == SDPA_ROPE_YARN) {
+      const double ramp = std::min(std::max((i - lo) / (hi - lo), 0.0), 1.0);  // 1: interpolated
+      g = f / factor * ramp + f * (1.0 - ramp);
+    }
+    freqs[i] = g;
+  }
+  return SDPA_OK;
+}
+
+sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const void* v,
+                                int64_t T, int64_t kv_t, int64_t kv_h, const int64_t* slots,
+                                void* stream) {
+  AppendArgs a{};
+  const sdpa_status_t st = check_cache(cache, a.c);
+  if (st != SDPA_OK) return st;
+  if (T < 0) return SDPA_ERR_INVALID_ARG;
+  if (T == 0) return SDPA_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !slots ||
+      (reinterpret_cast<uintptr_t>(slots) & 7u) || !good_stride(kv_t, 8) || !good_stride(kv_h, 8))
+    return SDPA_ERR_INVALID_ARG;
+  if (T >= (1ll << 31)) return SDPA_ERR_UNSUPPORTED;
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.T = T;
+  a.kv_t = kv_t;
+  a.kv_h = kv_h;
+  a.slots = slots;
+  const int64_t rows_per_cta = kAppendThreads / (cache->d / 8) * kAppendRows;
+  const int64_t grid = (T * a.c.Hkv + rows_per_cta - 1) / rows_per_cta;
+  if (grid >= (1ll << 31)) return SDPA_ERR_UNSUPPORTED;
+  const dim3 g(static_cast<unsigned>(grid), 2);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
+  if (cache->d == 128) {
+    if (e4m3) cache_append_kernel<128, kCacheE4m3><<<g, kAppendThreads, 0, cs>>>(a);
+    else cache_append_kernel<128, kCacheBf16><<<g, kAppendThreads, 0, cs>>>(a);
+  } else {
+    if (e4m3) cache_append_kernel<64, kCacheE4m3><<<g, kAppendThreads, 0, cs>>>(a);
+    else cache_append_kernel<64, kCacheBf16><<<g, kAppendThreads, 0, cs>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+sdpa_status_t sdpa_cache_gather(const sdpa_kv_cache* cache, int64_t B, const int32_t* page_table,
+                                int64_t table_width, int64_t table_b, const int32_t* cu_seqlens,
+                                int64_t total, void* k, void* v, int64_t kv_t, int64_t kv_h,
+                                void* stream) {
+  GatherArgs a{};
+  const sdpa_status_t st = check_cache(cache, a.c);
+  if (st != SDPA_OK) return st;
+  if (B < 1 || total < 0 || !page_table || table_width < 1 || table_b < table_width || !cu_seqlens ||
+      (reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+    return SDPA_ERR_INVALID_ARG;
+  if (B > 65535 || total >= (1ll << 30) || table_width >= (1ll << 31)) return SDPA_ERR_UNSUPPORTED;
+  if (total == 0) return SDPA_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !good_stride(kv_t, 8) || !good_stride(kv_h, 8))
+    return SDPA_ERR_INVALID_ARG;
+  a.B = static_cast<int>(B);
+  a.table = page_table;
+  a.width = table_width;
+  a.table_b = table_b;
+  a.cu = cu_seqlens;
+  a.total = total;
+  a.k = static_cast<__nv_bfloat16*>(k);
+  a.v = static_cast<__nv_bfloat16*>(v);
+  a.kv_t = kv_t;
+  a.kv_h = kv_h;
+  const dim3 g(static_cast<unsigned>((total + kGatherRows - 1) / kGatherRows), 2);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
+  if (cache->d == 128) {
+    if (e4m3) cache_gather_kernel<128, kCacheE4m3><<<g, kGatherThreads, 0, cs>>>(a);
+    else cache_gather_kernel<128, kCacheBf16><<<g, kGatherThreads, 0, cs>>>(a);
+  } else {
+    if (e4m3) cache_gather_kernel<64, kCacheE4m3><<<g, kGatherThreads, 0, cs>>>(a);
+    else cache_gather_kernel<64, kCacheBf16><<<g, kGatherThreads, 0, cs>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+size_t sdpa_tree_fwd_workspace_size(const sdpa_tree* tree, const sdpa_kv_cache* cache) {
+  CacheView v;
+  TreePlan pl;
+  return check_tree(tree, cache, v, pl) == SDPA_OK ? pl.total : 0;
+}
+
+sdpa_status_t sdpa_tree_fwd(const sdpa_tree* t, const sdpa_kv_cache* cache, const void* q,
+                            const sdpa_bias_desc* bias, float scale, void* o, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  CacheView v;
+  TreePlan pl;
+  const sdpa_status_t st = check_tree(t, cache, v, pl);
+  if (st != SDPA_OK) return st;
+  if (!std::isfinite(scale)) return SDPA_ERR_INVALID_ARG;
+  if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned16(lse))
+    return SDPA_ERR_INVALID_ARG;
+  TreeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (bias && bias->kind != SDPA_BIAS_NONE) {
+    if (bias->kind == SDPA_BIAS_ALIBI) {
+      if (!bias->ptr) return SDPA_ERR_INVALID_ARG;
+      a.alibi_slopes = bias->ptr;
+    } else if (bias->kind == SDPA_BIAS_T5) {
+      const int nb = bias->num_buckets;
+      if (!bias->ptr || nb < 2 || nb > 128 || (bias->bidirectional && nb % 2 != 0) ||
+          !fill_t5(a.t5, nb, bias->max_distance, bias->bidirectional))
+        return SDPA_ERR_INVALID_ARG;
+      a.t5_table = bias->ptr;
+    } else {
+      return bias->kind == SDPA_BIAS_DENSE || bias->kind == SDPA_BIAS_REL ? SDPA_ERR_UNSUPPORTED
+                                                                         : SDPA_ERR_INVALID_ARG;
+    }
+  }
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < pl.total)
+    return SDPA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.q_t = t->q_t;
+  a.q_h = t->q_h;
+  a.o_t = t->o_t;
+  a.o_h = t->o_h;
+  a.B = static_cast<int>(t->B);
+  a.T = static_cast<int>(t->T);
+  a.max_nodes = static_cast<int>(t->max_nodes);
+  a.Hq = static_cast<int>(t->Hq);
+  a.Hkv = v.Hkv;
+  a.G = a.Hq / a.Hkv;
+  a.cu = t->cu_nodes;
+  a.ctx = t->ctx_lens;
+  a.table = t->page_table;
+  a.width = t->table_width;
+  a.table_b = t->table_b;
+  a.mask = t->tree_mask;
+  a.wl = clamp_window(t->window_left, 1ll << 30);
+  a.page_size = v.page_size;
+  a.page_shift = v.page_shift;
+  a.num_pages = v.num_pages;
+  a.ks = v.ks;
+  a.vs = v.vs;
+  a.ss_page = v.ss_page;
+  a.ss_head = v.ss_head;
+  a.scale_log2 = scale * kLog2e;
+  a.prefix = reinterpret_cast<int64_t*>(ws + pl.prefix);
+  a.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
+  a.part_o = reinterpret_cast<float*>(ws + pl.o);
+  a.wait_limit_ns = g_wait_limit_ns;
+  const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
+  const int keys = cache->d == 128 && !e4m3 ? TreeTile<128, kCacheBf16>::kKeys : 128;
+  a.box_rows = std::min(v.page_size, keys);
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, cache->k, cache, a.box_rows) ||
+      !make_cache_map(&mv, cache->v, cache, a.box_rows))
+    return SDPA_ERR_CUDA;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (cache->d == 128)
+    e = e4m3 ? dispatch_tree_bias<128, kCacheE4m3>(a, mk, mv, cs)
+             : dispatch_tree_bias<128, kCacheBf16>(a, mk, mv, cs);
+  else
+    e = e4m3 ? dispatch_tree_bias<64, kCacheE4m3>(a, mk, mv, cs)
+             : dispatch_tree_bias<64, kCacheBf16>(a, mk, mv, cs);
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+sdpa_status_t sdpa_spec_verify(const sdpa_verify* s, int32_t* path, int32_t* accepted,
+                               int32_t* next_token, void* stream) {
+  if (!s || s->B < 1 || s->N < 1 || s->V < 1) return SDPA_ERR_INVALID_ARG;
+  if (s->N > kVerifyMaxNodes || s->V >= (1ll << 31) || s->B > (1ll << 24)) return SDPA_ERR_UNSUPPORTED;
+  if (!s->target || !s->u_sample || !path || !accepted || !next_token) return SDPA_ERR_INVALID_ARG;
+  if (s->N > 1 && (!s->draft || !s->tokens || !s->u_accept)) return SDPA_ERR_INVALID_ARG;
+  const void* ptrs[] = {s->target, s->draft, s->tokens, s->parents, s->u_accept, s->u_sample,
+                        path, accepted, next_token};
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return SDPA_ERR_INVALID_ARG;
+  const int64_t st[] = {s->target_b, s->target_n, s->draft_b, s->draft_n};
+  for (int64_t x : st)
+    if (x < 0 || x >= (1ll << 38)) return SDPA_ERR_INVALID_ARG;
+  VerifyArgs a{};
+  a.B = static_cast<int>(s->B);
+  a.N = static_cast<int>(s->N);
+  a.V = static_cast<int>(s->V);
+  a.t_b = s->target_b;
+  a.t_n = s->target_n;
+  a.d_b = s->draft_b;
+  a.d_n = s->draft_n;
+  a.target = s->target;
+  a.draft = s->draft;
+  a.tokens = s->tokens;
+  a.parents = s->parents;
+  a.u_accept = s->u_accept;
+  a.u_sample = s->u_sample;
+  a.path = path;
+  a.accepted = accepted;
+  a.next_token = next_token;
+  // a CTA of the cluster per 4096 entries of the vocabulary, up to eight
+  int cluster = 1;
+  while (cluster < kVerifyMaxCluster && cluster * 4096ll < s->V) cluster *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * cluster);
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, spec_verify_kernel, a) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+}  // extern "C"
