@@ -87,8 +87,6 @@ bool make_cache_map(CUtensorMap* m, const void* base, const sdpa_kv_cache* c, in
 }
 
 // -------------------------------------------------------------------- tree
-constexpr int kTreeRows = 16;
-
 struct TreePlan {
   size_t prefix, ml, o, total;
 };
@@ -108,35 +106,34 @@ sdpa_status_t check_tree(const sdpa_tree* t, const sdpa_kv_cache* c, CacheView& 
     return SDPA_ERR_INVALID_ARG;
   // positions, and the tiles of one sequence, are counted in 32 bits
   if (t->table_width > (1ll << 30) / c->page_size) return SDPA_ERR_UNSUPPORTED;
-  const int64_t tiles = (t->table_width * c->page_size + 63) / 64;
-  const int64_t blocks = (t->max_nodes * (t->Hq / c->Hkv) + kTreeRows - 1) / kTreeRows;
+  const int64_t tiles = (t->table_width * c->page_size + kTreeKeys - 1) / kTreeKeys;
+  const int64_t blocks = (t->max_nodes * (t->Hq / c->Hkv) + 15) / 16;
   if (tiles * blocks >= (1ll << 31) / c->Hkv) return SDPA_ERR_UNSUPPORTED;
   if (!good_stride(t->q_t, 8) || !good_stride(t->q_h, 8) || !good_stride(t->o_t, 8) ||
       !good_stride(t->o_h, 8))
     return SDPA_ERR_INVALID_ARG;
   pl.prefix = 0;
   pl.ml = round256(static_cast<size_t>(t->B + 1) * sizeof(int64_t));
-  pl.o = pl.ml + round256(static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeRows * sizeof(float2));
-  pl.total = pl.o + static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeRows * c->d * sizeof(float);
+  pl.o = pl.ml + round256(static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeMaxRows * sizeof(float2));
+  pl.total = pl.o + static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeMaxRows * c->d * sizeof(float);
   return SDPA_OK;
 }
 
-template <int D, int FMT, int BIAS>
+template <int D, int FMT, int R, int BIAS>
 cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                         cudaStream_t st) {
-  using Tile = TreeTile<D, FMT>;
-  constexpr int kSmem = Tile::kStages * Tile::kStage + kTreeRows * (D + 4) * 4;
-  auto kern = tree_fwd_kernel<D, FMT, BIAS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  using L = TreeLayout<D, FMT, R>;
+  auto kern = tree_fwd_kernel<D, FMT, R, BIAS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int grid = std::min(2 * sms, kTreeMaxCtas);
-  kern<<<grid, kTreeThreads, kSmem, st>>>(a, mk, mv);
+  const int grid = std::min(sms, kTreeMaxCtas);
+  kern<<<grid, kTreeThreads, L::kSmem, st>>>(a, mk, mv);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // no (sequence, head) longer than one tile can span CTAs
-  if (a.width * a.page_size <= Tile::kKeys) return cudaSuccess;
+  // a (sequence, head) of one tile cannot span CTAs
+  if (a.width * a.page_size <= kTreeKeys) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((a.max_nodes * a.Hq + kTreeJoinWarps - 1) / kTreeJoinWarps, a.B);
   cfg.blockDim = dim3(kTreeJoinWarps * 32);
@@ -146,14 +143,25 @@ cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const CUtensor
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, FMT>, a, grid);
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, R>, a, grid);
+}
+
+// Query rows of one product: the smallest of 16, 32 and 64 that holds a
+// sequence's, 64 (and several blocks) beyond.
+template <int D, int FMT, int BIAS>
+cudaError_t dispatch_tree_rows(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                               cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.max_nodes) * a.G;
+  if (rows <= 16) return launch_tree<D, FMT, 16, BIAS>(a, mk, mv, st);
+  if (rows <= 32) return launch_tree<D, FMT, 32, BIAS>(a, mk, mv, st);
+  return launch_tree<D, FMT, 64, BIAS>(a, mk, mv, st);
 }
 
 template <int D, int FMT>
 cudaError_t dispatch_tree_bias(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                                cudaStream_t st) {
-  return a.alibi_slopes || a.t5_table ? launch_tree<D, FMT, 1>(a, mk, mv, st)
-                                      : launch_tree<D, FMT, 0>(a, mk, mv, st);
+  return a.alibi_slopes || a.t5_table ? dispatch_tree_rows<D, FMT, 1>(a, mk, mv, st)
+                                      : dispatch_tree_rows<D, FMT, 0>(a, mk, mv, st);
 }
 
 }  // namespace
@@ -399,8 +407,7 @@ sdpa_status_t sdpa_tree_fwd(const sdpa_tree* t, const sdpa_kv_cache* cache, cons
   a.part_o = reinterpret_cast<float*>(ws + pl.o);
   a.wait_limit_ns = g_wait_limit_ns;
   const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
-  const int keys = cache->d == 128 && !e4m3 ? TreeTile<128, kCacheBf16>::kKeys : 128;
-  a.box_rows = std::min(v.page_size, keys);
+  a.box_rows = std::min(v.page_size, kTreeKeys);
   CUtensorMap mk, mv;
   if (!make_cache_map(&mk, cache->k, cache, a.box_rows) ||
       !make_cache_map(&mv, cache->v, cache, a.box_rows))

@@ -4,27 +4,39 @@
 // Mathematics.  The nodes of a sequence times the query heads of a KV head's
 // group are the rows of one score matrix against that head's keys, so every
 // cached byte is read once for all of them.  Per row an online softmax in
-// log2 units: running maximum m, sum l of 2^(s - m) and accumulator O.  An
-// e4m3 key's scale multiplies its score column.  A value row's scale 2^e
-// joins the exponent instead of the values: weights are 2^(s + e - m') with m'
-// the maximum of s + e, so they lie in [0, 1] whatever the scales are and
-// round to fp16 with 11 bits, and l adds weight * 2^-e.
+// log2 units: a reference r near the running maximum, the sum l of 2^(s - r)
+// and the accumulator O, rescaled when the maximum outgrows r.
 //
-// Bound by DRAM: at up to 16 rows per KV head a cached byte takes 8 to 32
-// FLOPs.  What costs is keeping enough loads in flight and every SM busy:
-//  * work is cut into tiles of one KV head's keys, laid out over all sequences
-//    and heads in one line, and the CTAs (two per SM) take equal pieces of the
-//    line, so ragged batches balance and one long sequence uses the whole GPU;
-//    a (sequence, head) that spans CTAs leaves partial (m, l, O) in the
-//    workspace and a second kernel joins them in order;
-//  * a producer warp copies tiles by TMA (one box per page piece) into a ring
-//    of 96 KB per CTA; four compute warps each take a quarter of a tile's keys
-//    with all rows, so a stored value is read from shared memory and converted
-//    by one warp only, and the warps meet only where a piece ends;
-//  * the products are mma.sync m16n8k16: with 16 rows a 128-row tcgen05 tile
-//    would be idle seven eighths of its rows.
+// The tensor core takes the products transposed: S^T = K Q^T and
+// O^T = V^T P^T, so that a tile's 128 keys, then the head's d, are the 128
+// rows of a tcgen05 tile and the few query rows are its columns.  A thread of
+// the softmax owns one key (one TMEM lane) with all query rows, which makes
+// masks, key scales and value scales values of the thread.
+//
+// An e4m3 cache is multiplied as it lies in memory (kind::f8f6f4), never
+// widened.  The other operand is split into two e4m3 parts x = x1 + x2 side
+// by side in the columns of one product: 4 + 4 significant bits hold a bf16
+// query exactly (down to 2^-21 of its row's largest element) and a weight to
+// 2^-9 (or 2^-23 of the largest).  Over a bf16 cache weights are split into
+// bf16 pairs the same way, so O carries the one rounding of its own type.  A
+// key's scale multiplies its scores; a value row's scale 2^e joins the
+// exponent, weights being 2^(s + e - r) with r near the maximum of s + e, so
+// they stay in range whatever the scales are, and l adds weight * 2^-e.
+//
+// Bound by DRAM: a cached byte takes 2 to 128 FLOPs (1 to 64 rows).  What
+// costs is keeping enough loads in flight and every SM busy:
+//  * work is cut into tiles of 128 keys of one KV head, laid out over all
+//    sequences and heads in one line, and the CTAs (one per SM) take equal
+//    pieces of the line, so ragged batches balance and one long sequence uses
+//    the whole GPU; a (sequence, head) that spans CTAs leaves partial
+//    (r, l, O) in the workspace and a second kernel joins them in order;
+//  * roles run on across pieces: a producer warp (TMA, one box per page
+//    piece, up to 190 KB in flight), a query warp that lays the next piece's
+//    rows out as an operand, one MMA-issuing thread that keeps S one tile
+//    ahead of P V, and two softmax warpgroups that share a tile by rows.
 #pragma once
 
+#include <cfloat>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,13 +45,16 @@
 #include "attn_common.cuh"
 #include "kv_cache.cuh"
 #include "sm100.cuh"
+#include "tmem_sync.cuh"
 
 namespace sdpa {
 
-constexpr int kTreeMaxCtas = 296;   // two per SM; the workspace is sized for it
+constexpr int kTreeMaxCtas = 148;   // one per SM; the workspace is sized for it
 constexpr int kTreeMaxNodes = 64;
-constexpr int kTreeKeyWarps = 4;
-constexpr int kTreeThreads = (kTreeKeyWarps + 1) * 32;
+constexpr int kTreeMaxRows = 64;    // query rows of one product
+constexpr int kTreeKeys = 128;      // keys per tile
+constexpr int kTreeProducer = 8, kTreeIssuer = 9, kTreeQuery = 10;  // warps after the 8 of the softmax
+constexpr int kTreeThreads = 11 * 32;
 
 struct TreeArgs {
   const __nv_bfloat16* q;
@@ -65,27 +80,62 @@ struct TreeArgs {
   T5Spec t5;
   // workspace
   int64_t* prefix;              // [B + 1] tiles before each sequence
-  float2* part_ml;              // [ctas][2][rows] (m, l)
+  float2* part_ml;              // [ctas][2][rows] (r, l)
   float* part_o;                // [ctas][2][rows][D]
   uint64_t wait_limit_ns;
 };
 
-// Shapes of a tile of keys in shared memory.
-template <int D, int FMT>
-struct TreeTile {
-  static constexpr int kCell = FMT == kCacheBf16 ? 2 : 1;
-  static constexpr int kRowBytes = D * kCell;                          // 64, 128 or 256
-  static constexpr int kHalves = kRowBytes == 256 ? 2 : 1;             // 128-byte columns
-  static constexpr int kLine = kRowBytes / kHalves;                    // bytes of a box row
-  static constexpr int kKeys = kRowBytes == 256 ? 64 : 128;            // keys per tile
-  static constexpr int kBytes = kKeys * kRowBytes;                     // of K, and of V
-  static constexpr int kStage = 2 * kBytes + 1024;                     // + scales of 128 keys each
-  static constexpr int kStages = kBytes == 16384 ? 3 : 6;
-  static constexpr int kWarpKeys = kKeys / kTreeKeyWarps;              // 16 or 32
-  // byte offset of 16-byte piece `c` of row `r`, as TMA's swizzle places it
-  static __device__ __forceinline__ uint32_t at(int r, int c) {
+// What a softmax thread needs to know of one query row.
+struct TreeRow {
+  uint64_t sees;  // nodes it sees
+  float scale;    // log2(e) * scale, and what undoes its operand's scaling
+  float bias;     // ALiBi: its slope; T5: the bias of every distance <= one_lo_max
+  int pos;        // its position
+  int head;       // its query head
+};
+
+struct TreeRows {
+  TreeRow row[kTreeMaxRows];
+  int depth[kTreeMaxNodes];  // of the sequence's nodes
+};
+
+template <int D, int FMT, int R>
+struct TreeLayout {
+  static constexpr bool kE4m3 = FMT == kCacheE4m3;
+  static constexpr int kCell = kE4m3 ? 1 : 2;
+  static constexpr int kRowBytes = D * kCell;               // 64, 128 or 256
+  static constexpr int kHalves = kRowBytes == 256 ? 2 : 1;  // 128-byte columns
+  static constexpr int kLine = kRowBytes / kHalves;         // bytes of a swizzled row
+  static constexpr int kTile = kTreeKeys * kRowBytes;       // bytes of K, and of V
+  static constexpr int kStage = 2 * kTile + (kE4m3 ? 1024 : 0);  // + 128 scales each
+  static constexpr int kSN = kE4m3 ? 2 * R : R;             // columns of S: query parts
+  static constexpr int kQBytes = kSN * kRowBytes;
+  static constexpr int kPBytes = 2 * R * kTreeKeys * kCell; // both parts of the weights
+  // two weight buffers, or one where two would leave a single stage
+  static constexpr int kPB = (!kE4m3 && R == 64) ? 1 : 2;
+  static constexpr int kRW = R / 2;                         // rows of a softmax warpgroup
+  static constexpr int kQOff = 0;
+  static constexpr int kPOff = kQOff + 2 * kQBytes;
+  static constexpr int kRowsOff = kPOff + kPB * kPBytes;
+  static constexpr int kRowsBytes = (static_cast<int>(sizeof(TreeRows)) + 15) / 16 * 16;
+  static constexpr int kMaxOff = kRowsOff + 2 * kRowsBytes;      // [2][R/2][4] floats
+  static constexpr int kMiscOff = kMaxOff + R * 4 * 4;
+  static constexpr int kMaxStages = 8;
+  static constexpr int kNumBars = 2 * kMaxStages + 13;
+  static constexpr int kMiscBytes = kNumBars * 8 + 128;
+  static constexpr int kRingOff = (kMiscOff + kMiscBytes + 1023) / 1024 * 1024;
+  static constexpr int kFit = (232448 - kRingOff) / kStage;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kSmem = kRingOff + kStages * kStage;
+  static constexpr int kOCol = 2 * kSN;                     // O^T, both parts, after two S buffers
+  static constexpr int kTmemCols = kOCol + 2 * R <= 128 ? 128 : kOCol + 2 * R <= 256 ? 256 : 512;
+  static_assert(kStages >= 2 && kSmem <= 232448, "shared memory budget");
+  static_assert(kOCol + 2 * R <= 512, "tensor memory budget");
+  static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "operand alignment");
+  // byte offset of 16-byte piece c of row r in a block of `rows` swizzled rows
+  static __device__ __forceinline__ uint32_t at(int r, int c, int rows) {
     if (kLine == 128)
-      return static_cast<uint32_t>((c >> 3) * kKeys * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+      return static_cast<uint32_t>((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
   }
 };
@@ -97,7 +147,7 @@ struct TreeSeq {
   __device__ __forceinline__ int units(int Hkv) const { return Hkv * rb * tiles; }
 };
 
-template <int KEYS, int ROWS>
+template <int R>
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
   TreeSeq s;
   s.row0 = a.cu[b];
@@ -110,224 +160,394 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
     s.row0 = s.n = s.ctx = 0;
   }
   s.keys = s.ctx + s.n;
-  s.tile0 = a.wl >= 0 ? max(0, s.ctx - a.wl) / KEYS : 0;
-  s.tiles = (s.keys + KEYS - 1) / KEYS - s.tile0;
-  s.rb = (s.n * a.G + ROWS - 1) / ROWS;
+  s.tile0 = a.wl >= 0 ? max(0, s.ctx - a.wl) / kTreeKeys : 0;
+  s.tiles = (s.keys + kTreeKeys - 1) / kTreeKeys - s.tile0;
+  s.rb = (s.n * a.G + R - 1) / R;
   if (s.n == 0) s.tiles = s.rb = 0;
   return s;
 }
 
-// One CTA's piece [u, end) of the line of tiles; next() gives it (sequence,
-// head, row block) by (sequence, head, row block).
-template <int KEYS, int ROWS>
+// One CTA's piece of the line of tiles; next() gives it (sequence, head, row
+// block) by (sequence, head, row block).
+template <int R>
 struct TreeWalk {
-  int64_t u, end;
-  int b, off, units;  // current sequence, tiles of it behind u, its tiles
+  int64_t left;       // tiles of the piece not walked yet
+  int b, off, units;  // current sequence, its tiles walked or before the piece, all its tiles
   TreeSeq s;
   int hkv, block, t0, nt;  // this step: head, row block, first tile, tiles
-  __device__ __forceinline__ void start(const TreeArgs& a, int64_t from, int64_t to, int b0,
-                                        int off0) {
-    u = from;
-    end = to;
-    b = b0;
-    off = off0;
-    if (u < end) {
-      s = tree_seq<KEYS, ROWS>(a, b);
-      units = s.units(a.Hkv);
-    }
-  }
   __device__ __forceinline__ bool next(const TreeArgs& a) {
-    if (u >= end) return false;
+    if (left <= 0) return false;
     while (off >= units) {
       off -= units;
-      s = tree_seq<KEYS, ROWS>(a, ++b);
+      s = tree_seq<R>(a, ++b);
       units = s.units(a.Hkv);
     }
     const int seg = off / s.tiles;
     t0 = off - seg * s.tiles;
     hkv = seg / s.rb;
     block = seg - hkv * s.rb;
-    nt = static_cast<int>(min(static_cast<int64_t>(s.tiles - t0), end - u));
-    u += nt;
+    nt = static_cast<int>(min(static_cast<int64_t>(s.tiles - t0), left));
+    left -= nt;
     off += nt;
     return true;
   }
 };
 
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+// Tiles per CTA of a line of `total`.
+__device__ __forceinline__ int64_t tree_share(int64_t total, int ctas) {
+  return (total + ctas - 1) / ctas;
 }
 
-// d += a * b, 16 x 8 x 16, bf16 or fp16 operands.
+// ------------------------------------------------- operands of the products
+// Shared-memory matrix descriptor of a layout: 0 plain, 2 128-byte swizzle,
+// 4 64-byte swizzle.  A K-major operand steps 8 rows by sbo; an MN-major one
+// steps 8 rows of K by sbo and a swizzle width along M by lbo when swizzled,
+// 8 rows of K by lbo and 16 bytes along N by sbo when plain.
+__device__ __forceinline__ uint64_t tree_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo,
+                                              uint32_t layout) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1) << 46 |
+         static_cast<uint64_t>(layout) << 61;
+}
+
 template <int FMT>
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  if (FMT == kCacheBf16)
+__device__ __forceinline__ void tree_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  if (FMT == kCacheBf16) {
+    mma_ss(d_tmem, adesc, bdesc, idesc, accumulate);
+  } else {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
 }
 
-// Two e4m3 codes (low 16 bits) as an fp16 pair: exact.
-__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t w) {
+// N fp32 columns of the warp's lanes, complete on return.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&x)[N]) {
+  if constexpr (N == 8) {
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+  } else if constexpr (N == 16) {
+    uint32_t r[16];
+    tmem_ld16_sync(taddr, r);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+  } else {
+    uint32_t r[32];
+    tmem_ld32_sync(taddr, r);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&x)[N]) {
+  if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(__float_as_uint(x[0])), "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])),
+        "r"(__float_as_uint(x[3])), "r"(__float_as_uint(x[4])), "r"(__float_as_uint(x[5])),
+        "r"(__float_as_uint(x[6])), "r"(__float_as_uint(x[7]))
+        : "memory");
+  } else if constexpr (N == 16) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+    tmem_st16_sync(taddr, r);
+  } else {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(x[i]);
+    tmem_st32_sync(taddr, r);
+  }
+}
+
+// Whether `x` holds for any thread of the named barrier's `count`.
+__device__ __forceinline__ bool barrier_or(uint32_t id, uint32_t count, bool x) {
   uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
-      : "r"(w));
+      : "r"(static_cast<uint32_t>(x)), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Two floats as e4m3 codes (x0 in the low byte), rounded to nearest even.
+__device__ __forceinline__ uint32_t e4m3x2(float x0, float x1) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
   return r;
 }
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&r));
 }
 
-// All bits of the codes / bf16 halves in w that are infinite or NaN.
-template <int FMT>
-__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
-  return FMT == kCacheBf16 ? __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u)
-                           : __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-}
+// What the second part of a split is multiplied by: with the first part
+// rounded to 4 bits, |rest| <= 8 for queries below 256 and <= 8 for weights up
+// to 256, so the products stay below 448 and as far above 2^-9 as they can.
+constexpr float kQueryRest = 16.f, kWeightRest = 32.f;
+// Weights are 2^(s - r): up to 2^8 (e4m3 holds 448), reached when r is set.
+constexpr float kWeightTop = 8.f;
 
 // b * log2(e) of a bias b, kept finite where b is: a bias of the type's lowest
 // value then still orders below every other score instead of hiding its key.
 __device__ __forceinline__ float bias_to_log2(float b) {
   const float x = b * kLog2e;
-  return isinf(x) && !isinf(b) ? copysignf(3.402823466e38f, b) : x;
+  return isinf(x) && !isinf(b) ? copysignf(FLT_MAX, b) : x;
 }
 
 __device__ __forceinline__ float t5_bias_log2(const TreeArgs& a, int rel, int h) {
   return bias_to_log2(a.t5_table[t5_bucket(rel, a.t5) * a.Hq + h]);
 }
 
-// The d index of accumulator element e (0, 1) of n-tile j for quad column c:
-// with e4m3 the two n-tiles of a 16-wide group hold its even and odd columns
-// (a transposed load moves pairs of codes).
-template <int FMT>
-__device__ __forceinline__ int acc_col(int j, int c, int e) {
-  return FMT == kCacheBf16 ? j * 8 + 2 * c + e : (j >> 1) * 16 + 4 * c + 2 * e + (j & 1);
+// ------------------------------------------------------------- query warp
+// One piece's query rows as the K-major operand `dst` (kSN rows; e4m3: first
+// parts in rows 0 .. R - 1, second parts from row R on) and their TreeRows.
+template <int D, int FMT, int R>
+__device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeWalk<R>& w, int lane,
+                                                  uint8_t* dst, TreeRows* info, bool bias) {
+  using L = TreeLayout<D, FMT, R>;
+  const TreeSeq& s = w.s;
+  const int n_rows = s.n * a.G - w.block * R;  // of this block, may exceed R
+  const uint64_t node_bits = s.n >= 64 ? ~0ull : (1ull << s.n) - 1ull;
+  auto sees_of = [&](int n) -> uint64_t {
+    const uint64_t m = a.mask ? static_cast<uint64_t>(a.mask[s.row0 + n]) : ~0ull >> (63 - n);
+    return m & node_bits;
+  };
+  for (int n = lane; n < s.n; n += 32) info->depth[n] = __popcll(sees_of(n) & ~(1ull << n));
+  for (int r = lane; r < R; r += 32) {
+    TreeRow t{0ull, a.scale_log2, 0.f, s.ctx, w.hkv * a.G};
+    if (r < n_rows) {
+      const int x = w.block * R + r;
+      const int n = x / a.G;
+      t.sees = sees_of(n);
+      t.pos = s.ctx + __popcll(t.sees & ~(1ull << n));
+      t.head = w.hkv * a.G + (x - n * a.G);
+      if (bias) {
+        if (a.alibi_slopes) t.bias = a.alibi_slopes[t.head];
+        else if (a.t5.one_lo_max != INT_MIN) t.bias = t5_bias_log2(a, a.t5.one_lo_max, t.head);
+      }
+    }
+    info->row[r] = t;
+  }
+  __syncwarp();
+  constexpr int kLanes = D / 8;        // lanes of a row, 8 elements each
+  constexpr int kPass = 32 / kLanes;   // rows per pass
+  constexpr int kFlight = R / kPass < 8 ? R / kPass : 8;
+  const int c = lane % kLanes, sub = lane / kLanes;
+  for (int r0 = 0; r0 < R; r0 += kPass * kFlight) {
+    uint4 x[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int r = r0 + f * kPass + sub;
+      x[f] = make_uint4(0, 0, 0, 0);
+      if (r < n_rows) {
+        const int at = w.block * R + r;
+        const int n = at / a.G;
+        x[f] = *reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(s.row0 + n) * a.q_t +
+                                               (w.hkv * a.G + at - n * a.G) * a.q_h + c * 8);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int r = r0 + f * kPass + sub;
+      if (FMT == kCacheBf16) {
+        *reinterpret_cast<uint4*>(dst + L::at(r, c, R)) = x[f];
+        continue;
+      }
+      // the row by a power of two that puts its largest element in [128, 256)
+      const uint32_t v[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, max(v[i] & 0x7fffu, (v[i] >> 16) & 0x7fffu));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
+      int e = static_cast<int>(m >> 7);          // biased exponent
+      e = e == 255 ? 134 : min(max(e, 16), 250);
+      // 2^(134 - e) in two factors, each a normal float
+      const int e1 = (134 - e) / 2, e2 = 134 - e - e1;
+      const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+      const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float y0 = __uint_as_float(v[i] << 16) * f1 * f2;
+        const float y1 = __uint_as_float(v[i] & 0xffff0000u) * f1 * f2;
+        hi[i] = e4m3x2(y0, y1);
+        const float2 h = e4m3x2_value(hi[i]);
+        lo[i] = e4m3x2((y0 - h.x) * kQueryRest, (y1 - h.y) * kQueryRest);
+      }
+      // a row that is not finite gives what float32 gives: NaN
+      if (m >= 0x7f80u) hi[0] = hi[1] = hi[2] = hi[3] = 0x7f7fu;
+      *reinterpret_cast<uint2*>(dst + L::at(r, c >> 1, 2 * R) + (c & 1) * 8) =
+          make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *reinterpret_cast<uint2*>(dst + L::at(R + r, c >> 1, 2 * R) + (c & 1) * 8) =
+          make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      if (c == 0) info->row[r].scale = a.scale_log2 / f1 / f2;
+    }
+  }
 }
 
-// Per-thread state of the two rows (lane / 4 and + 8) of a 16-row tile.
-struct TreeRow {
-  uint64_t sees;  // nodes it sees
-  int pos;        // its position
-  int head;       // its query head
-  float bias;     // ALiBi: its slope; T5: the bias of every distance <= one_lo_max
-};
-
-template <int D, int FMT, int BIAS>
-__global__ void __launch_bounds__(kTreeThreads, 2) tree_fwd_kernel(
-    const TreeArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using Tile = TreeTile<D, FMT>;
-  constexpr int ROWS = 16;
-  constexpr int KEYS = Tile::kKeys;
-  constexpr int WK = Tile::kWarpKeys;
-  constexpr int NT = WK / 8;    // score n-tiles per warp
-  constexpr int DT = D / 8;     // output n-tiles
-  constexpr int KS = D / 16;    // k-steps over d
-  constexpr int kPad = D + 4;   // merge buffer row, floats
+// ---------------------------------------------------------------- kernel
+template <int D, int FMT, int R, int BIAS>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
+    const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap mk,
+    const __grid_constant__ CUtensorMap mv) {
+  using L = TreeLayout<D, FMT, R>;
+  constexpr bool E4 = L::kE4m3;
+  constexpr int ST = L::kStages;
+  constexpr int PB = L::kPB;
+  constexpr int RW = L::kRW;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2 * Tile::kStages];
-  __shared__ int abort_flag;
-  __shared__ int start_b, start_off;
-  __shared__ int64_t total_sh;
-  __shared__ int64_t scan_sh[kTreeThreads / 32];
-  __shared__ float2 merge_ml[kTreeKeyWarps][ROWS];
   if (!smem_base_ok(smem)) {
     if (threadIdx.x == 0) atomicOr(&g_device_status, kStatusMisaligned);
     return;
   }
-  float* merge_o = reinterpret_cast<float*>(smem + Tile::kStages * Tile::kStage);
+  const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);
-  const uint32_t bar0 = smem_u32(bars);
-  auto full = [&](int s) { return bar0 + 8u * s; };
-  auto empty = [&](int s) { return bar0 + 8u * (Tile::kStages + s); };
-  if (tid == 0) {
-    abort_flag = 0;
-    start_b = -1;
-    for (int s = 0; s < Tile::kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), kTreeKeyWarps);
-    }
-    fence_mbar_init();
-    tma_prefetch_desc(&mk);
-    tma_prefetch_desc(&mv);
-  }
+  auto bar = [&](int i) -> uint32_t { return sb + L::kMiscOff + 8 * i; };
+  auto full = [&](int s) { return bar(s); };
+  auto empty = [&](int s) { return bar(L::kMaxStages + s); };
+  constexpr int kB = 2 * L::kMaxStages;
+  auto s_full = [&](int x) { return bar(kB + x); };       // S of a tile is in tensor memory
+  auto s_free = [&](int x) { return bar(kB + 2 + x); };   // ... and in registers
+  auto p_full = [&](int x) { return bar(kB + 4 + x); };   // weights are in shared memory
+  auto pv_done = [&](int x) { return bar(kB + 6 + x); };  // ... and added to O
+  auto q_full = [&](int x) { return bar(kB + 8 + x); };   // a piece's queries are laid out
+  auto q_free = [&](int x) { return bar(kB + 10 + x); };  // ... and the piece is done
+  const uint32_t drain = bar(kB + 12);
+  uint8_t* misc = smem + L::kMiscOff + L::kNumBars * 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  uint32_t* dirty = reinterpret_cast<uint32_t*>(misc + 16);   // [4] bits of keys
+  int64_t* start_left = reinterpret_cast<int64_t*>(misc + 32);
+  int* start_b = reinterpret_cast<int*>(misc + 40);
+  int* start_off = reinterpret_cast<int*>(misc + 44);
+  TreeSeq* start_seq = reinterpret_cast<TreeSeq*>(misc + 48);  // 28 bytes
 
-  // the line of tiles: its length, and where this CTA's piece begins
-  int64_t mine = 0;
-  for (int b = tid; b < a.B; b += kTreeThreads) mine += tree_seq<KEYS, ROWS>(a, b).units(a.Hkv);
+  if (warp == kTreeIssuer) {
+    if (lane == 0) {
+      *abort_flag = 0;
+      for (int s = 0; s < ST; ++s) {
+        mbar_init(full(s), 1);
+        mbar_init(empty(s), 1);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(s_full(x), 1);
+        mbar_init(s_free(x), 8);
+        mbar_init(p_full(x), 8);
+        mbar_init(pv_done(x), 1);
+        mbar_init(q_full(x), 1);
+        mbar_init(q_free(x), 8);
+      }
+      mbar_init(drain, 1);
+      fence_mbar_init();
+      tma_prefetch_desc(&mk);
+      tma_prefetch_desc(&mv);
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
+    tmem_relinquish();
+  } else if (warp == kTreeProducer) {
+    // the line of tiles: its length, and where this CTA's piece begins
+    TreeSeq s{};
+    int64_t units = 0, total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
+      units = 0;
+      if (b < a.B) {
+        s = tree_seq<R>(a, b);
+        units = s.units(a.Hkv);
+      }
+      total += units;
+    }
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) mine += __shfl_xor_sync(~0u, mine, s);
-  if (lane == 0) scan_sh[warp] = mine;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t total = 0;
-    for (int w = 0; w < kTreeThreads / 32; ++w) total += scan_sh[w];
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+    const int64_t per = tree_share(total, gridDim.x);
     const int64_t from = per * blockIdx.x;
+    if (lane == 0) {
+      *start_left = max(min(total - from, per), static_cast<int64_t>(0));
+      if (blockIdx.x == 0) a.prefix[a.B] = total;
+    }
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
-      const int64_t units = b < a.B ? tree_seq<KEYS, ROWS>(a, b).units(a.Hkv) : 0;
+      if (a.B > 32) {  // else the first pass's values are at hand
+        units = 0;
+        if (b < a.B) {
+          s = tree_seq<R>(a, b);
+          units = s.units(a.Hkv);
+        }
+      }
       int64_t upto = units;
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const int64_t y = __shfl_up_sync(~0u, upto, s);
-        if (lane >= s) upto += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += y;
       }
       const int64_t before = base + upto - units;
       if (blockIdx.x == 0 && b < a.B) a.prefix[b] = before;
       if (b < a.B && before <= from && from < before + units) {
-        start_b = b;
-        start_off = static_cast<int>(from - before);
+        *start_b = b;
+        *start_off = static_cast<int>(from - before);
+        *start_seq = s;
       }
       base += __shfl_sync(~0u, upto, 31);
-    }
-    if (lane == 0) {
-      total_sh = total;
-      if (blockIdx.x == 0) a.prefix[a.B] = total;
+      if (blockIdx.x != 0 && base > from) break;  // (CTA 0 writes all of `prefix`)
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t total = total_sh;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t from = per * blockIdx.x;
-  const int64_t to = min(total, from + per);
-  TreeWalk<KEYS, ROWS> walk;
-  walk.start(a, from, start_b < 0 ? from : to, max(start_b, 0), start_b < 0 ? 0 : start_off);
-  const WaitCtl ctl{&abort_flag, a.wait_limit_ns};
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{abort_flag, a.wait_limit_ns};
+  TreeWalk<R> walk;
+  walk.left = *start_left;
+  walk.b = *start_b;
+  walk.off = *start_off;
+  walk.s = *start_seq;
+  walk.units = walk.s.units(a.Hkv);
 
-  if (warp == kTreeKeyWarps) {
+  if (warp == kTreeProducer) {
     // ------------------------------------------------------------ producer
-    const int boxes = KEYS / a.box_rows;   // <= 8
-    const uint32_t box_bytes = static_cast<uint32_t>(a.box_rows) * Tile::kRowBytes;
+    const int boxes = kTreeKeys / a.box_rows;  // <= 8
+    const uint32_t box_bytes = static_cast<uint32_t>(a.box_rows) * L::kRowBytes;
     uint32_t it = 0;
     bool ok = true;
     while (ok && walk.next(a)) {
       const int* row = a.table + static_cast<int64_t>(walk.b) * a.table_b;
       auto page_of = [&](int t) {
-        const int pos = (walk.s.tile0 + t) * KEYS + lane * a.box_rows;
+        const int pos = (walk.s.tile0 + t) * kTreeKeys + lane * a.box_rows;
         int page = -1;
         if (lane < boxes && pos < walk.s.keys) {
           page = row[pos >> a.page_shift];
@@ -342,30 +562,30 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_fwd_kernel(
       for (int i = 0; i < walk.nt; ++i, ++it) {
         const int t = walk.t0 + i;
         const int next_page = i + 1 < walk.nt ? page_of(t + 1) : -1;
-        const int st = it % Tile::kStages;
-        if (it >= Tile::kStages) ok = mbar_wait(empty(st), ((it / Tile::kStages) - 1) & 1, ctl);
+        const int st = it % ST;
+        if (it >= ST) ok = mbar_wait(empty(st), ((it / ST) - 1) & 1, ctl);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         const bool copy = page >= 0;
-        const bool scales = FMT == kCacheE4m3 && copy && page < a.num_pages;
+        const bool scales = E4 && copy && page < a.num_pages;
         const int n_copy = __popc(__ballot_sync(~0u, copy));
         const int n_scale = __popc(__ballot_sync(~0u, scales));
-        const uint32_t base = smem_u32(smem) + st * Tile::kStage;
-        if (lane == 0)
-          mbar_expect_tx(full(st), 2u * (n_copy * box_bytes + n_scale * a.box_rows));
+        const uint32_t base = sb + L::kRingOff + st * L::kStage;
+        if (lane == 0) mbar_expect_tx(full(st), 2u * (n_copy * box_bytes + n_scale * a.box_rows));
         __syncwarp();
         if (copy) {
-          const int pos = (walk.s.tile0 + t) * KEYS + lane * a.box_rows;
+          const int pos = (walk.s.tile0 + t) * kTreeKeys + lane * a.box_rows;
           const int r = pos & (a.page_size - 1);
-          const uint32_t dst = base + static_cast<uint32_t>(lane) * a.box_rows * Tile::kLine;
+          const uint32_t dst = base + static_cast<uint32_t>(lane) * a.box_rows * L::kLine;
 #pragma unroll
-          for (int h = 0; h < Tile::kHalves; ++h) {
-            tma_load_4d(dst + h * KEYS * 128, &mk, full(st), h * 64, r, walk.hkv, page);
-            tma_load_4d(dst + Tile::kBytes + h * KEYS * 128, &mv, full(st), h * 64, r, walk.hkv, page);
-          }
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_load_4d(dst + h * kTreeKeys * 128, &mk, full(st), h * 64, r, walk.hkv, page);
+#pragma unroll
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_load_4d(dst + L::kTile + h * kTreeKeys * 128, &mv, full(st), h * 64, r, walk.hkv, page);
           if (scales) {
             const int64_t off = page * a.ss_page + walk.hkv * a.ss_head + r;
-            const uint32_t sdst = base + 2 * Tile::kBytes + lane * a.box_rows;
+            const uint32_t sdst = base + 2 * L::kTile + lane * a.box_rows;
             bulk_load(sdst, a.ks + off, a.box_rows, full(st));
             bulk_load(sdst + 512, a.vs + off, a.box_rows, full(st));
           }
@@ -373,434 +593,410 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_fwd_kernel(
         page = next_page;
       }
     }
-    // a wait that ran out ends the CTA: let the copies in flight land first
     if (!ok) {
-      const uint64_t t_end = globaltimer_ns() + a.wait_limit_ns;
-      const uint32_t first = it > Tile::kStages ? it - Tile::kStages : 0;
-      for (uint32_t j = first; j < it; ++j)
-        while (!mbar_try_wait(full(j % Tile::kStages), (j / Tile::kStages) & 1) &&
-               globaltimer_ns() < t_end) {
-        }
+      // a wait that ran out ends the CTA: let the copies in flight land first
+      volatile int never = 0;
+      const WaitCtl ign{&never, a.wait_limit_ns};
+      for (uint32_t j = it > ST ? it - ST : 0; j < it; ++j) mbar_wait(full(j % ST), (j / ST) & 1, ign);
     }
-    return;
-  }
-
-  // -------------------------------------------------------------- compute
-  const int quad = lane >> 2, c = lane & 3;
-  const int lm = lane >> 3, lr = lane & 7;  // ldmatrix: matrix and row this lane addresses
-  uint32_t it = 0;
-  bool alive = true;
-  // After a wait that ran out the warps go on through the rest of the walk
-  // without tiles, so that they still meet at every barrier.
-  while (walk.next(a)) {
-    const TreeSeq& s = walk.s;
-    const int n_rows = s.n * a.G;
-    const uint64_t node_bits = s.n >= 64 ? ~0ull : (1ull << s.n) - 1ull;
-    auto sees_of = [&](int n) -> uint64_t {
-      const uint64_t w = a.mask ? static_cast<uint64_t>(a.mask[s.row0 + n]) : ~0ull >> (63 - n);
-      return w & node_bits;
+  } else if (warp == kTreeQuery) {
+    // ------------------------------------------------------------- queries
+    uint32_t u = 0;
+    bool ok = true;
+    while (ok && walk.next(a)) {
+      const int x = u & 1;
+      if (u >= 2) ok = __all_sync(~0u, mbar_wait(q_free(x), ((u >> 1) - 1) & 1, ctl));
+      if (!ok) break;
+      tree_load_queries<D, FMT, R>(a, walk, lane, smem + L::kQOff + x * L::kQBytes,
+                                   reinterpret_cast<TreeRows*>(smem + L::kRowsOff + x * L::kRowsBytes),
+                                   BIAS != 0);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(x));
+      ++u;
+    }
+  } else if (warp == kTreeIssuer) {
+    // ----------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kNone = (1u << 4) | (static_cast<uint32_t>(128 >> 4) << 24);  // f32, M = 128
+      constexpr uint32_t kTypes = E4 ? 0u : (1u << 7) | (1u << 10);
+      constexpr uint32_t kIdS = kNone | kTypes | (static_cast<uint32_t>(L::kSN >> 3) << 17);
+      constexpr uint32_t kIdO = kNone | kTypes | (1u << 15) | (1u << 16) |
+                                (static_cast<uint32_t>(2 * R >> 3) << 17);
+      constexpr uint32_t kSwz = L::kLine == 128 ? 2u : 4u;
+      const uint64_t dk = tree_desc(sb, 16, 8 * L::kLine, kSwz);  // K and Q, K-major
+      // V, MN-major: 64-wide halves kTreeKeys rows apart; at d = 64 the
+      // tile's rows 64 .. 127 repeat its first 64 and are not read back
+      const uint64_t dv = tree_desc(sb, D == 128 && !E4 ? kTreeKeys * 128 : 0, 8 * L::kLine, kSwz);
+      const uint64_t dp = tree_desc(sb, 128, kTreeKeys * 16, 0);  // weights, MN-major, plain
+      uint32_t it = 0, u = 0;
+      bool ok = true;
+      auto add_values = [&](uint32_t j) -> bool {  // O^T += V^T P^T of tile j
+        const int pb = j % PB, st = j % ST;
+        if (!mbar_wait(p_full(pb), (j / PB) & 1, ctl)) return false;
+        tc_fence_after();
+        const uint64_t vd = dv + ((L::kRingOff + st * L::kStage + L::kTile) >> 4);
+        const uint64_t pd = dp + ((L::kPOff + pb * L::kPBytes) >> 4);
+        constexpr int kStep = E4 ? 32 : 16;  // keys per instruction
+#pragma unroll
+        for (int k = 0; k < kTreeKeys / kStep; ++k)
+          tree_mma<FMT>(tmem + L::kOCol, vd + (k * kStep * L::kLine >> 4), pd + (k * kStep * 16 >> 4), kIdO, 1u);
+        mma_commit(pv_done(pb));
+        mma_commit(empty(st));
+        return true;
+      };
+      while (ok && walk.next(a)) {
+        ok = mbar_wait(q_full(u & 1), (u >> 1) & 1, ctl);
+        for (int i = 0; ok && i < walk.nt; ++i, ++it) {
+          const int st = it % ST, x = it & 1;
+          if (!(ok = mbar_wait(full(st), (it / ST) & 1, ctl))) break;
+          if (it >= 2 && !(ok = mbar_wait(s_free(x), ((it >> 1) - 1) & 1, ctl))) break;
+          tc_fence_after();
+          const uint64_t kd = dk + ((L::kRingOff + st * L::kStage) >> 4);
+          const uint64_t qd = dk + ((L::kQOff + (u & 1) * L::kQBytes) >> 4);
+#pragma unroll
+          for (int k = 0; k < L::kRowBytes / 32; ++k)
+            tree_mma<FMT>(tmem + x * L::kSN, kd + (kmajor_koff(k, kTreeKeys) >> 4),
+                          qd + (kmajor_koff(k, L::kSN) >> 4), kIdS, k > 0 ? 1u : 0u);
+          mma_commit(s_full(x));
+          if (it > 0) ok = add_values(it - 1);
+        }
+        ++u;
+      }
+      if (ok && it > 0) add_values(it - 1);
+      // every MMA issued is done before tensor memory is freed
+      volatile int never = 0;
+      const WaitCtl ign{&never, a.wait_limit_ns};
+      mma_commit(drain);
+      mbar_wait(drain, 0, ign);
+    }
+    __syncwarp();
+  } else {
+    // -------- softmax: warpgroup wg has rows [RW wg, RW wg + RW), thread = key = row of O^T
+    const int wg = warp >> 2;
+    const int me = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_o = tmem + lanes + L::kOCol + wg * RW;
+    float* wmax = reinterpret_cast<float*>(smem + L::kMaxOff) + wg * RW * 4;  // [RW][4 warps]
+    // After a wait that ran out the warps go on without waiting, through the
+    // same barriers, so that no thread is left at one.
+    bool ok = true;
+    uint32_t it = 0, u = 0;
+    auto values_done = [&](uint32_t j) {  // P V of tile j has been added to O
+      if (ok) ok = mbar_wait(pv_done(j % PB), (j / PB) & 1, ctl);
+      ok = __all_sync(~0u, ok);
+      tc_fence_after();
     };
-    TreeRow row[2];
-    float row_scale[2];
-    uint32_t qa[KS][4];
+    while (walk.next(a)) {
+      const TreeSeq& s = walk.s;
+      const TreeRows* info = reinterpret_cast<const TreeRows*>(smem + L::kRowsOff + (u & 1) * L::kRowsBytes);
+      const TreeRow* rows = info->row + wg * RW;
+      if (ok) ok = mbar_wait(q_full(u & 1), (u >> 1) & 1, ctl);
+      ok = __all_sync(~0u, ok);
+      float ref[RW], l[RW];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = walk.block * ROWS + quad + 8 * i;
-      row[i].sees = 0;
-      row[i].pos = s.ctx;
-      row[i].head = walk.hkv * a.G;
-      row[i].bias = 0.f;
-      row_scale[i] = a.scale_log2;
+      for (int j = 0; j < RW; ++j) {
+        ref[j] = -FLT_MAX;
+        l[j] = 0.f;
+      }
+      for (int i = 0; i < walk.nt; ++i, ++it) {
+        const int st = it % ST, x = it & 1, pb = it % PB;
+        const int key0 = (s.tile0 + walk.t0 + i) * kTreeKeys;
+        const int key = key0 + me;
+        const uint8_t* stage = smem + L::kRingOff + st * L::kStage;
+        if (ok) ok = mbar_wait(s_full(x), (it >> 1) & 1, ctl);
+        ok = __all_sync(~0u, ok);
+        tc_fence_after();
+        float sc[RW];
+        tmem_ld_cols<RW>(tmem + lanes + x * L::kSN + wg * RW, sc);
+        if constexpr (E4) {
+          float rest[RW];
+          tmem_ld_cols<RW>(tmem + lanes + x * L::kSN + R + wg * RW, rest);
 #pragma unroll
-      for (int k = 0; k < KS; ++k) qa[k][i] = qa[k][2 + i] = 0u;
-      if (r < n_rows) {
-        const int n = r / a.G, h = walk.hkv * a.G + (r - n * a.G);
-        row[i].sees = sees_of(n);
-        row[i].pos = s.ctx + __popcll(row[i].sees & ~(1ull << n));
-        row[i].head = h;
-        if (BIAS && a.alibi_slopes)
-          row[i].bias = a.alibi_slopes[h];
-        else if (BIAS && a.t5.one_lo_max != INT_MIN)
-          row[i].bias = t5_bias_log2(a, a.t5.one_lo_max, h);
-        const __nv_bfloat16* src = a.q + static_cast<int64_t>(s.row0 + n) * a.q_t + h * a.q_h;
-        if (FMT == kCacheBf16) {
+          for (int j = 0; j < RW; ++j) sc[j] = fmaf(rest[j], 1.f / kQueryRest, sc[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free(x));
+
+        // scores in log2 units, plus the exponent of the key's value scale
+        float v_inv = 1.f;
+        if constexpr (E4) {
+          const float kf = e8m0_float(stage[2 * L::kTile + me]);
+          const int ve = stage[2 * L::kTile + 512 + me];
+          v_inv = e8m0_float(static_cast<uint32_t>(max(254 - ve, 0)));
+          const float vx = static_cast<float>(ve - 127);
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            qa[k][i] = *reinterpret_cast<const uint32_t*>(src + k * 16 + 2 * c);
-            qa[k][2 + i] = *reinterpret_cast<const uint32_t*>(src + k * 16 + 8 + 2 * c);
-          }
+          for (int j = 0; j < RW; ++j)
+            sc[j] = BIAS ? sc[j] * rows[j].scale * kf : fmaf(sc[j] * rows[j].scale, kf, vx);
         } else {
-          // k-slots 2c, 2c + 1, 2c + 8, 2c + 9 hold d = 4c .. 4c + 3, the four
-          // codes of one loaded word of K
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const uint2 w = *reinterpret_cast<const uint2*>(src + k * 16 + 4 * c);
-            qa[k][i] = w.x;
-            qa[k][2 + i] = w.y;
-          }
+          for (int j = 0; j < RW; ++j) sc[j] *= a.scale_log2;
         }
-      }
-      if (FMT == kCacheE4m3) {
-        // fp16 operands: the row by a power of two that puts its largest
-        // element in [2^14, 2^15), so that it neither overflows nor loses bits
-        uint32_t m = 0;
+        // all keys of the tile seen by every row: context keys inside every
+        // node's window (a node's position is below ctx + n)
+        const bool masked = key0 + kTreeKeys > s.ctx || (a.wl >= 0 && key0 < s.ctx + s.n - 1 - a.wl);
+        const int node = key - s.ctx;
+        const int key_pos = node >= 0 ? s.ctx + (node < s.n ? info->depth[node] : 0) : key;
+        if constexpr (BIAS != 0) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w = qa[k][2 * h + i];
-            m = max(m, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
-          }
-        m = max(m, __shfl_xor_sync(~0u, m, 1));
-        m = max(m, __shfl_xor_sync(~0u, m, 2));
-        int e = static_cast<int>(m >> 7);  // biased exponent
-        e = e == 255 ? 127 + 14 : min(max(e, 16), 250);
-        // times 2^(141 - e), in two steps where the factor is beyond a float
-        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (141 - e) / 2) << 23);
-        const float f2 = __uint_as_float(static_cast<uint32_t>(127 + (141 - e) - (141 - e) / 2) << 23);
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w = qa[k][2 * h + i];
-            qa[k][2 * h + i] = pack_half2(__uint_as_float(w << 16) * f1 * f2,
-                                          __uint_as_float(w & 0xffff0000u) * f1 * f2);
-          }
-        row_scale[i] = a.scale_log2 / f1 / f2;
-      }
-    }
-    // depths of nodes lane and lane + 32, for the tiles that hold nodes
-    int depth_lo = 0, depth_hi = 0;
-    if (lane < s.n) depth_lo = __popcll(sees_of(lane) & ~(1ull << lane));
-    if (lane + 32 < s.n) depth_hi = __popcll(sees_of(lane + 32) & ~(1ull << (lane + 32)));
-
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    float acc[DT][4];
-#pragma unroll
-    for (int j = 0; j < DT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-
-    for (int i = 0; alive && i < walk.nt; ++i, ++it) {
-      const int st = it % Tile::kStages;
-      alive = mbar_wait(full(st), (it / Tile::kStages) & 1, ctl);
-      alive = __all_sync(~0u, alive);
-      if (!alive) break;
-      const int key_tile = (s.tile0 + walk.t0 + i) * KEYS;
-      const int key0 = key_tile + warp * WK;      // this warp's first key
-      const uint32_t kbase = smem_u32(smem) + st * Tile::kStage;
-      const uint32_t vbase = kbase + Tile::kBytes;
-      const uint8_t* ksc = smem + st * Tile::kStage + 2 * Tile::kBytes + warp * WK;
-
-      float sc[NT][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
-      if (FMT == kCacheBf16) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int j = 0; j < NT; j += 2) {
-            uint32_t r[4];
-            ldsm_x4(kbase + Tile::at(warp * WK + j * 8 + (lm >> 1) * 8 + lr, 2 * k + (lm & 1)), r);
-            mma_16816<FMT>(sc[j], qa[k], r[0], r[1]);
-            mma_16816<FMT>(sc[j + 1], qa[k], r[2], r[3]);
-          }
-      } else {
-#pragma unroll
-        for (int k = 0; k < KS; k += 4)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint32_t r[4];
-            ldsm_x4(kbase + Tile::at(warp * WK + j * 8 + lr, k + lm), r);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_16816<FMT>(sc[j], qa[k + x], e4m3x2_half2(r[x] & 0xffffu),
-                             e4m3x2_half2(r[x] >> 16));
-          }
-      }
-
-      // all of this warp's keys seen by every row: context keys inside every
-      // node's window (a node's position is below ctx + 64)
-      const bool masked = key0 + WK > s.ctx || (a.wl >= 0 && key0 < s.ctx + s.n - 1 - a.wl);
-      float vexp[NT][2];   // e4m3: exponent of the value scale, and 2^-it
-      float vinv[NT][2];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float kf[2] = {1.f, 1.f};
-        if (FMT == kCacheE4m3) {
-          const uint32_t ke = *reinterpret_cast<const uint16_t*>(ksc + j * 8 + 2 * c);
-          const uint32_t ve = *reinterpret_cast<const uint16_t*>(ksc + 512 + j * 8 + 2 * c);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            kf[e] = e8m0_float((ke >> (8 * e)) & 0xffu);
-            const int v = static_cast<int>((ve >> (8 * e)) & 0xffu);
-            vexp[j][e] = static_cast<float>(v - 127);
-            vinv[j][e] = e8m0_float(static_cast<uint32_t>(max(254 - v, 0)));
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[j][e] *= row_scale[e >> 1];
-          if (FMT == kCacheE4m3) sc[j][e] *= kf[e & 1];
-        }
-      }
-      if (BIAS) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            int pos = key0 + j * 8 + 2 * c + (e & 1);
-            if (masked) {
-              const int n = pos - s.ctx;
-              const int lo = __shfl_sync(~0u, depth_lo, n & 31), hi = __shfl_sync(~0u, depth_hi, n & 31);
-              if (n >= 0) pos = s.ctx + (n < 32 ? lo : hi);
-            }
-            const TreeRow& rw = row[e >> 1];
-            const int rel = pos - rw.pos;
+          for (int j = 0; j < RW; ++j) {
+            const int rel = key_pos - rows[j].pos;
             if (a.alibi_slopes)
-              sc[j][e] += bias_to_log2(-rw.bias * fabsf(static_cast<float>(rel)));
+              sc[j] += bias_to_log2(-rows[j].bias * fabsf(static_cast<float>(rel)));
             else
-              sc[j][e] += rel <= a.t5.one_lo_max ? rw.bias : t5_bias_log2(a, rel, rw.head);
+              sc[j] += rel <= a.t5.one_lo_max ? rows[j].bias : t5_bias_log2(a, rel, rows[j].head);
           }
-      }
-      if (masked) {
+          if constexpr (E4) {
+            const float vx = static_cast<float>(static_cast<int>(stage[2 * L::kTile + 512 + me]) - 127);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = key0 + j * 8 + 2 * c + (e & 1);
-            const int n = key - s.ctx;
-            const TreeRow& rw = row[e >> 1];
-            int pos = key;
-            if (a.wl >= 0) {
-              const int lo = __shfl_sync(~0u, depth_lo, n & 31), hi = __shfl_sync(~0u, depth_hi, n & 31);
-              if (n >= 0) pos = s.ctx + (n < 32 ? lo : hi);
-            }
-            bool seen = n < 0 || (n < 64 && ((rw.sees >> n) & 1ull));
-            if (a.wl >= 0) seen = seen && rw.pos - pos <= a.wl;
-            if (!seen) sc[j][e] = -INFINITY;
+            for (int j = 0; j < RW; ++j) sc[j] += vx;
           }
-      }
-      if (FMT == kCacheE4m3) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[j][e] += vexp[j][e & 1];
-      }
-
-      float m_new[2];
-#pragma unroll
-      for (int i2 = 0; i2 < 2; ++i2) {
-        float m = m_run[i2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) m = fmax3(m, sc[j][2 * i2], sc[j][2 * i2 + 1]);
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-        m_new[i2] = m;
-      }
-      if (__any_sync(~0u, m_new[0] != m_run[0] || m_new[1] != m_run[1])) {
-#pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          const float f = m_run[i2] == m_new[i2] ? 1.f : fast_exp2(m_run[i2] - m_new[i2]);
-          l_run[i2] *= f;
-#pragma unroll
-          for (int j = 0; j < DT; ++j) {
-            acc[j][2 * i2] *= f;
-            acc[j][2 * i2 + 1] *= f;
-          }
-          m_run[i2] = m_new[i2];
         }
-      }
-      const float off0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
-      const float off1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
+        if (masked) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = fast_exp2(sc[j][e] - (e < 2 ? off0 : off1));
-          sc[j][e] = p;
-          l_run[e >> 1] += FMT == kCacheE4m3 ? p * vinv[j][e & 1] : p;
+          for (int j = 0; j < RW; ++j) {
+            bool seen = node < 0 || (node < 64 && ((rows[j].sees >> node) & 1ull));
+            if (a.wl >= 0) seen = seen && rows[j].pos - key_pos <= a.wl;
+            if (!seen) sc[j] = -INFINITY;
+          }
         }
 
-      // O += P V over 16 keys at a time
-      auto values = [&](auto flag) {
-        constexpr bool kClean = decltype(flag)::value;
+        // a new reference where a score has outgrown the old one
+        float over = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          uint32_t pa[4];
-          if (FMT == kCacheBf16) {
-            pa[0] = pack_bf16x2(sc[j][0], sc[j][1]);
-            pa[1] = pack_bf16x2(sc[j][2], sc[j][3]);
-            pa[2] = pack_bf16x2(sc[j + 1][0], sc[j + 1][1]);
-            pa[3] = pack_bf16x2(sc[j + 1][2], sc[j + 1][3]);
-          } else {
-            pa[0] = pack_half2(sc[j][0], sc[j][1]);
-            pa[1] = pack_half2(sc[j][2], sc[j][3]);
-            pa[2] = pack_half2(sc[j + 1][0], sc[j + 1][1]);
-            pa[3] = pack_half2(sc[j + 1][2], sc[j + 1][3]);
+        for (int j = 0; j < RW; j += 2) over = fmax3(over, sc[j] - ref[j], sc[j + 1] - ref[j + 1]);
+        if (barrier_or(1 + wg, 128, over > kWeightTop || i == 0)) {
+          float keep = 0.f;
+#pragma unroll
+          for (int j = 0; j < RW; ++j) {
+            const float m = warp_max(sc[j]);
+            if (lane == j) keep = m;
           }
-          uint32_t dirty = 0;
+          if (lane < RW) wmax[lane * 4 + (warp & 3)] = keep;
+          named_barrier(1 + wg, 128);
+          float f[RW];
 #pragma unroll
-          for (int x = 0; x < Tile::kRowBytes / 16; x += 2) {
-            uint32_t r[4];
-            ldsm_x4_t(vbase + Tile::at(warp * WK + j * 8 + (lm & 1) * 8 + lr, x + (lm >> 1)), r);
-            if (kClean) {
-              // 0 * NaN is NaN: a value no row may see is taken out here, and
-              // put back below for the rows that do see it
+          for (int j = 0; j < RW; ++j) {
+            const float4 w4 = *reinterpret_cast<const float4*>(wmax + j * 4);
+            float m = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w));
+            m = fmaxf(m - (E4 ? kWeightTop : 0.f), ref[j]);
+            f[j] = fast_exp2(ref[j] - m);
+            ref[j] = m;
+            l[j] *= f[j];
+          }
+          if (i > 0) values_done(it - 1);
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const uint32_t bits = nonfinite_bits<FMT>(r[y]);
-                dirty |= bits;
-                r[y] &= ~bits;
-              }
-            }
-            if (FMT == kCacheBf16) {
-              mma_16816<FMT>(acc[x], pa, r[0], r[1]);
-              mma_16816<FMT>(acc[x + 1], pa, r[2], r[3]);
+          for (int part = 0; part < 2; ++part) {
+            float o[RW];
+            if (i > 0) {
+              tmem_ld_cols<RW>(t_o + part * R, o);
+#pragma unroll
+              for (int j = 0; j < RW; ++j) o[j] *= f[j];
             } else {
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t w0 = __byte_perm(r[2 * y], 0, 0x3120);
-                const uint32_t w1 = __byte_perm(r[2 * y + 1], 0, 0x3120);
-                mma_16816<FMT>(acc[2 * (x + y)], pa, e4m3x2_half2(w0 & 0xffffu),
-                               e4m3x2_half2(w1 & 0xffffu));
-                mma_16816<FMT>(acc[2 * (x + y) + 1], pa, e4m3x2_half2(w0 >> 16),
-                               e4m3x2_half2(w1 >> 16));
+              for (int j = 0; j < RW; ++j) o[j] = 0.f;
+            }
+            tmem_st_cols<RW>(t_o + part * R, o);
+          }
+          named_barrier(1 + wg, 128);  // wmax is read
+        }
+
+        if (it >= PB) values_done(it - PB);  // the weight buffer is free
+        uint8_t* pbuf = smem + L::kPOff + pb * L::kPBytes + me * 16;
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+          sc[j] = fast_exp2(sc[j] - ref[j]);
+          l[j] = E4 ? fmaf(sc[j], v_inv, l[j]) : l[j] + sc[j];
+        }
+        // both parts of the weights: 16 bytes of one key's rows at a time
+        if constexpr (E4) {
+          uint32_t hi[RW / 4], lo[RW / 4];
+#pragma unroll
+          for (int j = 0; j < RW; j += 4) {
+            const uint32_t h0 = e4m3x2(sc[j], sc[j + 1]), h1 = e4m3x2(sc[j + 2], sc[j + 3]);
+            const float2 a0 = e4m3x2_value(h0), a1 = e4m3x2_value(h1);
+            hi[j / 4] = h0 | h1 << 16;
+            lo[j / 4] = e4m3x2((sc[j] - a0.x) * kWeightRest, (sc[j + 1] - a0.y) * kWeightRest) |
+                        e4m3x2((sc[j + 2] - a1.x) * kWeightRest, (sc[j + 3] - a1.y) * kWeightRest) << 16;
+          }
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint32_t* w = part ? lo : hi;
+            const int row0 = part * R + wg * RW;
+            uint8_t* dst = pbuf + (row0 / 16) * (kTreeKeys * 16) + row0 % 16;
+            if constexpr (RW == 8) {
+              *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < RW / 4; j += 4)
+                *reinterpret_cast<uint4*>(dst + (j / 4) * (kTreeKeys * 16)) =
+                    make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < RW; j += 8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p0 = sc[j + 2 * e], p1 = sc[j + 2 * e + 1];
+              hi[e] = pack_bf16x2(p0, p1);
+              lo[e] = pack_bf16x2(p0 - __uint_as_float(hi[e] << 16),
+                                  p1 - __uint_as_float(hi[e] & 0xffff0000u));
+            }
+            uint8_t* dst = pbuf + ((wg * RW + j) / 8) * (kTreeKeys * 16);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + R / 8 * (kTreeKeys * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        if (masked) {
+          // 0 * NaN is NaN: an infinite or NaN value that some row must not see
+          // (stale rows of a page among them) is taken out of the tile, and
+          // added to the rows that do see it here
+          constexpr int kPieces = L::kRowBytes / 16;
+          uint8_t* vrows = smem + L::kRingOff + st * L::kStage + L::kTile;
+          uint32_t odd = 0;
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vrows + L::at(me, c, kTreeKeys));
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              odd |= E4 ? __vcmpeq4(v[e] & 0x7f7f7f7fu, 0x7f7f7f7fu)
+                        : __vcmpeq2(v[e] & 0x7f807f80u, 0x7f807f80u);
+          }
+          if (barrier_or(3, 256, odd != 0)) {
+            const uint32_t bits = __ballot_sync(~0u, odd != 0);
+            if (wg == 0 && lane == 0) dirty[warp & 3] = bits;
+            named_barrier(3, 256);
+            if (it > 0) values_done(it - 1);
+            float add[RW];
+#pragma unroll
+            for (int j = 0; j < RW; ++j) add[j] = 0.f;
+            for (int k4 = 0; k4 < 4; ++k4)
+              for (uint32_t left = dirty[k4]; left; left &= left - 1) {
+                const int k = k4 * 32 + __ffs(left) - 1;
+                float v = 0.f;
+                if (me < D) {
+                  const int byte = me * L::kCell;
+                  const uint8_t* src = vrows + L::at(k, byte >> 4, kTreeKeys) + (byte & 15);
+                  if (E4) v = (*src & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : 0.f;
+                  else v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(src));
+                }
+                if (!isinf(v) && !isnan(v)) continue;
+                const uint8_t* pk = smem + L::kPOff + pb * L::kPBytes + k * 16;
+#pragma unroll
+                for (int j = 0; j < RW; ++j) {
+                  const int byte = (wg * RW + j) * L::kCell;
+                  const uint8_t* src = pk + (byte >> 4) * (kTreeKeys * 16) + (byte & 15);
+                  const bool seen = E4 ? *src != 0 : *reinterpret_cast<const uint16_t*>(src) != 0;
+                  if (seen) add[j] += v;
+                }
+              }
+            __syncwarp();
+            float o[RW];
+            tmem_ld_cols<RW>(t_o, o);
+#pragma unroll
+            for (int j = 0; j < RW; ++j) o[j] += add[j];
+            tmem_st_cols<RW>(t_o, o);
+            named_barrier(3, 256);
+            if (wg == 0 && odd != 0) {
+#pragma unroll 1
+              for (int c = 0; c < kPieces; ++c) {
+                uint4* p = reinterpret_cast<uint4*>(vrows + L::at(me, c, kTreeKeys));
+                uint4 w = *p;
+                uint32_t* v = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  v[e] &= ~(E4 ? __vcmpeq4(v[e] & 0x7f7f7f7fu, 0x7f7f7f7fu)
+                               : __vcmpeq2(v[e] & 0x7f807f80u, 0x7f807f80u));
+                *p = w;
               }
             }
           }
-          if (kClean && __any_sync(~0u, dirty != 0)) {
+        }
+        fence_async_shared();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(pb));
+      }
+
+      // ---- the piece's result: row sums over the warpgroup's keys, then O
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj)
+      for (int n = RW, o = 16; n > 1; n >>= 1, o >>= 1) {
+        const bool up = (lane & o) != 0;  // keeps the upper half of the rows
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-#pragma unroll 1
-                for (int cc = 0; cc < 4; ++cc) {
-                  const float p0 = __shfl_sync(~0u, sc[j + jj][e], (lane & ~3) | cc);
-                  const float p1 = __shfl_sync(~0u, sc[j + jj][2 + e], (lane & ~3) | cc);
-                  const int r = warp * WK + (j + jj) * 8 + 2 * cc + e;
+        for (int j = 0; j < n / 2; ++j) {
+          const float send = up ? l[j] : l[j + n / 2];
+          l[j] = (up ? l[j + n / 2] : l[j]) + __shfl_xor_sync(~0u, send, o);
+        }
+      }
 #pragma unroll
-                  for (int n = 0; n < DT; ++n)
+      for (int o = 16 / RW; o > 0; o >>= 1) l[0] += __shfl_xor_sync(~0u, l[0], o);
+      // lane's bits from 16 down select the row, halves first
+      if ((lane & (32 / RW - 1)) == 0) wmax[(lane / (32 / RW)) * 4 + (warp & 3)] = l[0];
+      named_barrier(1 + wg, 128);
+      values_done(it - 1);
+      float o[RW];
+      {
+        float rest[RW];
+        tmem_ld_cols<RW>(t_o, o);
+        tmem_ld_cols<RW>(t_o + R, rest);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                      const int byte = acc_col<FMT>(n, c, y) * Tile::kCell;
-                      const uint8_t* src = smem + st * Tile::kStage + Tile::kBytes +
-                                           Tile::at(r, byte >> 4) + (byte & 15);
-                      float v;
-                      bool odd;
-                      if (FMT == kCacheBf16) {
-                        v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(src));
-                        odd = isinf(v) || isnan(v);
-                      } else {
-                        odd = (*src & 0x7fu) == 0x7fu;
-                        v = __uint_as_float(0x7fc00000u);
-                      }
-                      if (odd && p0 > 0.f) acc[n][y] += p0 * v;
-                      if (odd && p1 > 0.f) acc[n][2 + y] += p1 * v;
-                    }
-                }
+        for (int j = 0; j < RW; ++j) o[j] = E4 ? fmaf(rest[j], 1.f / kWeightRest, o[j]) : o[j] + rest[j];
+      }
+      const bool whole = walk.t0 == 0 && walk.nt == s.tiles;
+      const int slot = walk.t0 == 0 ? 1 : 0;  // 0: began in an earlier CTA
+      const int n_rows = s.n * a.G - walk.block * R - wg * RW;  // of this warpgroup, may exceed RW
+      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + wg * RW;
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        const float4 l4 = *reinterpret_cast<const float4*>(wmax + j * 4);
+        const float sum = (l4.x + l4.y) + (l4.z + l4.w);
+        if (whole) o[j] *= sum > 0.f || isnan(sum) ? 1.f / sum : 0.f;
+        if (me == j && j < n_rows) {
+          if (whole) {
+            const int node = (walk.block * R + wg * RW + j) / a.G;
+            a.lse[static_cast<int64_t>(rows[j].head) * a.T + s.row0 + node] = (ref[j] + log2f(sum)) * kLn2;
+          } else {
+            a.part_ml[part + j] = make_float2(ref[j], sum);
           }
         }
-      };
-      if (masked) values(Flag<true>{});
-      else values(Flag<false>{});
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(st));
-    }
-    // join the four warps' (m, l, O) in order: everyone scales to the common
-    // maximum, warp 0 adds the others' accumulators one after another
-#pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) {
-      l_run[i2] += __shfl_xor_sync(~0u, l_run[i2], 1);
-      l_run[i2] += __shfl_xor_sync(~0u, l_run[i2], 2);
-      if (c == 0) merge_ml[warp][quad + 8 * i2] = make_float2(m_run[i2], l_run[i2]);
-    }
-    named_barrier(1, kTreeKeyWarps * 32);
-    float m_all[2], l_all[2];
-#pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kTreeKeyWarps; ++w) m = fmaxf(m, merge_ml[w][quad + 8 * i2].x);
-      float l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kTreeKeyWarps; ++w) {
-        const float2 ml = merge_ml[w][quad + 8 * i2];
-        // a piece without a visible key has m = -inf, l = 0 (or NaN, which stays)
-        l += ml.x == -INFINITY ? ml.y : ml.y * fast_exp2(ml.x - m);
       }
-      m_all[i2] = m;
-      l_all[i2] = l;
-      const float f = m_run[i2] == -INFINITY ? 1.f : fast_exp2(m_run[i2] - m);
+      if (me < D) {
 #pragma unroll
-      for (int j = 0; j < DT; ++j) {
-        acc[j][2 * i2] *= f;
-        acc[j][2 * i2 + 1] *= f;
-      }
-    }
-#pragma unroll 1
-    for (int w = 1; w < kTreeKeyWarps; ++w) {
-      if (warp == w) {
-#pragma unroll
-        for (int j = 0; j < DT; ++j)
-#pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2)
-            *reinterpret_cast<float2*>(merge_o + (quad + 8 * i2) * kPad + j * 8 + 2 * c) =
-                make_float2(acc[j][2 * i2], acc[j][2 * i2 + 1]);
-      }
-      named_barrier(1, kTreeKeyWarps * 32);
-      if (warp == 0) {
-#pragma unroll
-        for (int j = 0; j < DT; ++j)
-#pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2) {
-            const float2 o = *reinterpret_cast<const float2*>(merge_o + (quad + 8 * i2) * kPad +
-                                                              j * 8 + 2 * c);
-            acc[j][2 * i2] += o.x;
-            acc[j][2 * i2 + 1] += o.y;
+        for (int j = 0; j < RW; j += 2) {
+          if (j >= n_rows) break;
+          if (whole) {
+            // lane pairs trade: the even lane stores two columns of row j, the
+            // odd lane of row j + 1
+            const bool up = lane & 1;
+            const float got = __shfl_xor_sync(~0u, up ? o[j] : o[j + 1], 1);
+            const int r = j + (up ? 1 : 0);
+            if (r < n_rows) {
+              const int node = (walk.block * R + wg * RW + r) / a.G;
+              __nv_bfloat16* dst = a.o + static_cast<int64_t>(s.row0 + node) * a.o_t +
+                                   static_cast<int64_t>(up ? rows[j + 1].head : rows[j].head) * a.o_h + (me & ~1);
+              *reinterpret_cast<uint32_t*>(dst) = up ? pack_bf16x2(got, o[j + 1]) : pack_bf16x2(o[j], got);
+            }
+          } else {
+            a.part_o[(part + j) * D + me] = o[j];
+            if (j + 1 < n_rows) a.part_o[(part + j + 1) * D + me] = o[j + 1];
           }
-      }
-      named_barrier(1, kTreeKeyWarps * 32);
-    }
-    if (warp != 0) continue;
-    const bool whole = walk.t0 == 0 && walk.nt == s.tiles;
-    const int slot = walk.t0 == 0 ? 1 : 0;  // 0: began in an earlier CTA
-#pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) {
-      const int lr2 = quad + 8 * i2;
-      const int r = walk.block * ROWS + lr2;
-      if (r >= n_rows) continue;
-      const int n = r / a.G;
-      if (whole) {
-        const float inv = l_all[i2] > 0.f || isnan(l_all[i2]) ? 1.f / l_all[i2] : 0.f;
-        __nv_bfloat16* dst = a.o + static_cast<int64_t>(s.row0 + n) * a.o_t + row[i2].head * a.o_h;
-        if (FMT == kCacheBf16) {
-#pragma unroll
-          for (int j = 0; j < DT; ++j)
-            *reinterpret_cast<uint32_t*>(dst + j * 8 + 2 * c) =
-                pack_bf16x2(acc[j][2 * i2] * inv, acc[j][2 * i2 + 1] * inv);
-        } else {
-#pragma unroll
-          for (int j = 0; j < DT; j += 2)
-            *reinterpret_cast<uint2*>(dst + j * 8 + 4 * c) =
-                make_uint2(pack_bf16x2(acc[j][2 * i2] * inv, acc[j + 1][2 * i2] * inv),
-                           pack_bf16x2(acc[j][2 * i2 + 1] * inv, acc[j + 1][2 * i2 + 1] * inv));
         }
-        if (c == 0)
-          a.lse[static_cast<int64_t>(row[i2].head) * a.T + s.row0 + n] =
-              (m_all[i2] + log2f(l_all[i2])) * kLn2;
-      } else {
-        const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * ROWS + lr2;
-        float* dst = a.part_o + at * D;
-#pragma unroll
-        for (int j = 0; j < DT; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) dst[acc_col<FMT>(j, c, e)] = acc[j][2 * i2 + e];
-        if (c == 0) a.part_ml[at] = make_float2(m_all[i2], l_all[i2]);
       }
+      tc_fence_before();
+      named_barrier(1 + wg, 128);  // wmax is read
+      if (lane == 0) mbar_arrive(q_free(u & 1));
+      ++u;
     }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTreeIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
   }
 }
 
@@ -809,47 +1005,41 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_fwd_kernel(
 // then add them, D / 32 columns each.
 constexpr int kTreeJoinWarps = 4;
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const TreeArgs a, int ctas) {
-  constexpr int ROWS = 16;
-  constexpr int KEYS = TreeTile<D, FMT>::kKeys;
+template <int D, int R>
+__global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a,
+                                                                       int ctas) {
   constexpr int W = D / 32;
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 31;
-  const int x = blockIdx.x * kTreeJoinWarps + (threadIdx.x >> 5);   // node * Hq + head
+  const int x = blockIdx.x * kTreeJoinWarps + (threadIdx.x >> 5);  // node * Hq + head
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const TreeSeq s = tree_seq<KEYS, ROWS>(a, b);
+  const TreeSeq s = tree_seq<R>(a, b);
   const int n = x / a.Hq, h = x - n * a.Hq;
   if (n >= s.n) return;
   const int hkv = h / a.G;
   const int r = n * a.G + (h - hkv * a.G);
-  const int block = r / ROWS;
-  const int64_t total = a.prefix[a.B];
-  const int64_t per = (total + ctas - 1) / ctas;
+  const int block = r / R, in = r - block * R;
+  const int64_t per = tree_share(a.prefix[a.B], ctas);
   const int64_t first = a.prefix[b] + (static_cast<int64_t>(hkv) * s.rb + block) * s.tiles;
   const int c0 = static_cast<int>(first / per);
   const int c1 = static_cast<int>((first + s.tiles - 1) / per);
   if (c0 == c1) return;
-  float m = -INFINITY, l = 0.f, acc[W];
+  float ref = -FLT_MAX, l = 0.f, acc[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) acc[i] = 0.f;
   for (int base = c0; base <= c1; base += 32) {
     const int cta = base + lane;
     // the first CTA's piece began in it, every later one's before it
-    const int64_t at = (static_cast<int64_t>(cta) * 2 + (cta == c0 ? 1 : 0)) * ROWS + (r & (ROWS - 1));
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (cta <= c1) ml = a.part_ml[at];
-    float top = ml.x;
-#pragma unroll
-    for (int sft = 16; sft > 0; sft >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, sft));
-    top = fmaxf(top, m);
-    const float f_old = m == -INFINITY ? 1.f : fast_exp2(m - top);
-    const float f = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - top);
+    float2 ml = make_float2(-FLT_MAX, 0.f);
+    if (cta <= c1) ml = a.part_ml[(static_cast<int64_t>(cta) * 2 + (cta == c0 ? 1 : 0)) * R + in];
+    const float top = fmaxf(warp_max(ml.x), ref);
+    const float f_old = fast_exp2(ref - top);
+    const float f = fast_exp2(ml.x - top);
     float add = ml.y * f;
 #pragma unroll
-    for (int sft = 16; sft > 0; sft >>= 1) add += __shfl_xor_sync(~0u, add, sft);
+    for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(~0u, add, o);
     l = l * f_old + add;
-    m = top;
+    ref = top;
 #pragma unroll
     for (int i = 0; i < W; ++i) acc[i] *= f_old;
     const int count = min(32, c1 - base + 1);
@@ -857,14 +1047,13 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const Tr
     for (int j = 0; j < count; ++j) {
       const int cj = base + j;
       const float w = __shfl_sync(~0u, f, j);
-      const float* src = a.part_o + ((static_cast<int64_t>(cj) * 2 + (cj == c0 ? 1 : 0)) * ROWS +
-                                     (r & (ROWS - 1))) * D + lane * W;
-      if (W == 4) {
+      const float* src = a.part_o + ((static_cast<int64_t>(cj) * 2 + (cj == c0 ? 1 : 0)) * R + in) * D + lane * W;
+      if constexpr (W == 4) {
         const float4 v = *reinterpret_cast<const float4*>(src);
         acc[0] += w * v.x;
         acc[1] += w * v.y;
-        acc[2 % W] += w * v.z;
-        acc[3 % W] += w * v.w;
+        acc[2] += w * v.z;
+        acc[3] += w * v.w;
       } else {
         const float2 v = *reinterpret_cast<const float2*>(src);
         acc[0] += w * v.x;
@@ -873,14 +1062,13 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const Tr
     }
   }
   const float inv = l > 0.f || isnan(l) ? 1.f / l : 0.f;
-  __nv_bfloat16* dst = a.o + static_cast<int64_t>(s.row0 + n) * a.o_t + h * a.o_h + lane * W;
-  if (W == 4)
+  __nv_bfloat16* dst = a.o + static_cast<int64_t>(s.row0 + n) * a.o_t + static_cast<int64_t>(h) * a.o_h + lane * W;
+  if constexpr (W == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                pack_bf16x2(acc[2 % W] * inv, acc[3 % W] * inv));
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0)
-    a.lse[static_cast<int64_t>(h) * a.T + s.row0 + n] = (m + log2f(l)) * kLn2;
+  if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + s.row0 + n] = (ref + log2f(l)) * kLn2;
 }
 
 }  // namespace sdpa

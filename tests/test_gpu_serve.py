@@ -4,12 +4,16 @@ Tolerances (half a step of bf16 is 2^-8 of the value, of fp16 2^-11):
   rope   the sines and cosines and two products in float32 (2^-20 of the
          magnitudes covers them), then one rounding to bf16.
   cache  exact: codes, scales and values are compared bit for bit.
-  tree   O: one rounding to bf16 (2^-8 |O|); each weight rounded for the
-         product with V, to bf16 (2^-8) over a bf16 cache and to fp16 (2^-11)
-         over e4m3, so at most that times sum(w |v|); a score's error e_s of
-         float32 accumulation, at most (d + 8) steps of 2^-23 of sum |q k|
-         scale, moves a weight by 2 e_s (numerator and denominator).  2^-18
-         covers exp2 and the sums.  LSE: e_s, and 2^-20 for the rest.
+  tree   O: one rounding to bf16 (2^-8 |O|).  Each weight enters the product
+         with V as two parts, bf16 (2^-8 each, 2^-16 together) over a bf16
+         cache and e4m3 (2^-4 each, 2^-8 together) over e4m3, so at most that
+         times sum(w |v|); e4m3 parts also drop below 2^-23 of the largest
+         weight, at most that for each of the n keys' |v|.  A score's error e_s
+         of float32 accumulation, at most (d + 8) steps of 2^-23 of sum |q k|
+         scale, moves a weight by 2 e_s (numerator and denominator); over e4m3
+         a query element is off by at most 2^-21 of its row's largest, which
+         adds 2^-21 max |q| sum |k| scale to e_s.  2^-18 covers exp2 and the
+         sums.  LSE: e_s, and 2^-20 for the rest.
 """
 import numpy as np
 import pytest
@@ -223,17 +227,26 @@ def test_bad_slots_and_pages_are_reported():
 
 
 # --------------------------------------------------------------------- tree
+def tree_tolerance(q, k, v, ro, spread, size, kv, scale=None):
+    """The module docstring's bounds for O and LSE."""
+    d = q.shape[-1]
+    e_s = (d + 8) * 2.0 ** -23 * size
+    if kv == "bf16":
+        return 2.0 ** -8 * np.abs(ro) + (2.0 ** -16 + 2 * e_s[..., None] + 2.0 ** -18) * spread, e_s
+    scale = d ** -0.5 if scale is None else abs(scale)
+    e_s = e_s + 2.0 ** -21 * np.abs(q).max(-1) * np.abs(k).sum(-1).max() * scale
+    lost = 2.0 ** -23 * len(v) * np.abs(v).max()
+    return 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * e_s[..., None] + 2.0 ** -18) * spread + lost, e_s
+
+
 def check_tree(o, lse, q, seqs, cu, kv, masks=None, **kw):
     """seqs: (k, v, ctx) per sequence in float64; every output against the definition."""
-    d = q.shape[-1]
-    p_step = 2.0 ** -8 if kv == "bf16" else 2.0 ** -11
     for b, (k, v, ctx) in enumerate(seqs):
         lo, hi = cu[b], cu[b + 1]
         if hi == lo:
             continue
         ro, rl, spread, size = so.tree_attention(f64(q[lo:hi]), k, v, ctx, None if masks is None else masks[lo:hi], **kw)
-        e_s = (d + 8) * 2.0 ** -23 * size
-        tol = 2.0 ** -8 * np.abs(ro) + (p_step + 2 * e_s[..., None] + 2.0 ** -18) * spread
+        tol, e_s = tree_tolerance(f64(q[lo:hi]), k, v, ro, spread, size, kv, kw.get("scale"))
         err = np.abs(f64(o[lo:hi]) - ro)
         assert (err <= tol).all(), (b, float(err.max()), float((err / np.maximum(tol, 1e-30)).max()))
         gl = f64(lse[:, lo:hi]).T
@@ -350,8 +363,7 @@ def test_tree_masks_that_leave_nothing_and_nan_in_hidden_nodes(kv):
         assert torch.isnan(o[bad]).all() and torch.isnan(lse[:, bad]).all()
         keep = [i for i in range(6) if i != bad]
         err = np.abs(f64(o)[keep] - ro[keep])
-        e_s = (128 + 8) * 2.0 ** -23 * size
-        tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * e_s[..., None] + 2.0 ** -18) * spread
+        tol, _ = tree_tolerance(f64(q), k, v, ro, spread, size, kv)
         assert (err <= tol[keep]).all()
         if ctx == 0:
             for i in (0, 5):
