@@ -17,11 +17,11 @@
 // widened.  The other operand is split into two e4m3 parts x = x1 + x2 side
 // by side in the columns of one product: 4 + 4 significant bits hold a bf16
 // query exactly (down to 2^-21 of its row's largest element) and a weight to
-// 2^-9 (or 2^-23 of the largest).  Over a bf16 cache weights are split into
-// bf16 pairs the same way, so O carries the one rounding of its own type.  A
-// key's scale multiplies its scores; a value row's scale 2^e joins the
-// exponent, weights being 2^(s + e - r) with r near the maximum of s + e, so
-// they stay in range whatever the scales are, and l adds weight * 2^-e.
+// 2^-8 (or 2^-21 of the largest).  Over a bf16 cache a weight is rounded to
+// bf16 (2^-8), as in the framework's forward.  A key's scale multiplies its
+// scores; a value row's scale 2^e joins the exponent, weights being
+// 2^(s + e - r) with r near the maximum of s + e, so they stay in range
+// whatever the scales are, and l adds weight * 2^-e.
 //
 // Bound by DRAM: a cached byte takes 2 to 128 FLOPs (1 to 64 rows).  What
 // costs is keeping enough loads in flight and every SM busy:
@@ -31,9 +31,12 @@
 //    the whole GPU; a (sequence, head) that spans CTAs leaves partial
 //    (r, l, O) in the workspace and a second kernel joins them in order;
 //  * roles run on across pieces: a producer warp (TMA, one box per page
-//    piece, up to 190 KB in flight), a query warp that lays the next piece's
-//    rows out as an operand, one MMA-issuing thread that keeps S one tile
-//    ahead of P V, and two softmax warpgroups that share a tile by rows.
+//    piece, K and V in slots of their own so that K's is free as soon as S is
+//    there), a query warp that lays the next piece's rows out as an operand,
+//    an issuing thread each for S and for P V, and two softmax warpgroups.
+//    The softmax's chain of waits per tile (~700 cycles) is what a short row
+//    block would pay, so up to 32 rows the warpgroups take turns by tile, each
+//    with its own O; at 64 rows they share a tile by rows.
 #pragma once
 
 #include <cfloat>
@@ -53,8 +56,10 @@ constexpr int kTreeMaxCtas = 148;   // one per SM; the workspace is sized for it
 constexpr int kTreeMaxNodes = 64;
 constexpr int kTreeMaxRows = 64;    // query rows of one product
 constexpr int kTreeKeys = 128;      // keys per tile
-constexpr int kTreeProducer = 8, kTreeIssuer = 9, kTreeQuery = 10;  // warps after the 8 of the softmax
-constexpr int kTreeThreads = 11 * 32;
+// warps after the 8 of the softmax
+constexpr int kTreeProducer = 8, kTreeIssueS = 9, kTreeIssueO = 10, kTreeQuery = 11;
+constexpr int kTreeThreads = 12 * 32;
+constexpr int kTreeScaleRing = 8;   // tiles whose e4m3 scales are kept
 
 struct TreeArgs {
   const __nv_bfloat16* q;
@@ -85,18 +90,17 @@ struct TreeArgs {
   uint64_t wait_limit_ns;
 };
 
-// What a softmax thread needs to know of one query row.
-struct TreeRow {
-  uint64_t sees;  // nodes it sees
-  float scale;    // log2(e) * scale, and what undoes its operand's scaling
-  float bias;     // ALiBi: its slope; T5: the bias of every distance <= one_lo_max
-  int pos;        // its position
-  int head;       // its query head
-};
-
+// What the softmax needs to know of a piece's query rows.
 struct TreeRows {
-  TreeRow row[kTreeMaxRows];
-  int depth[kTreeMaxNodes];  // of the sequence's nodes
+  float scale[kTreeMaxRows];    // log2(e) * scale, and what undoes the operand's scaling (e4m3)
+  float bias[kTreeMaxRows];     // ALiBi: its slope; T5: the bias of every distance <= one_lo_max
+  uint64_t sees[kTreeMaxRows];  // nodes a row sees
+  uint64_t seen[kTreeMaxNodes]; // rows that see a node
+  int64_t out[kTreeMaxRows];    // its element offset in o
+  int64_t lse[kTreeMaxRows];    // its index in lse
+  int pos[kTreeMaxRows];        // its position
+  int head[kTreeMaxRows];       // its query head
+  int depth[kTreeMaxNodes];     // of the sequence's nodes
 };
 
 template <int D, int FMT, int R>
@@ -106,32 +110,40 @@ struct TreeLayout {
   static constexpr int kRowBytes = D * kCell;               // 64, 128 or 256
   static constexpr int kHalves = kRowBytes == 256 ? 2 : 1;  // 128-byte columns
   static constexpr int kLine = kRowBytes / kHalves;         // bytes of a swizzled row
-  static constexpr int kTile = kTreeKeys * kRowBytes;       // bytes of K, and of V
-  static constexpr int kStage = 2 * kTile + (kE4m3 ? 1024 : 0);  // + 128 scales each
-  static constexpr int kSN = kE4m3 ? 2 * R : R;             // columns of S: query parts
-  static constexpr int kQBytes = kSN * kRowBytes;
-  static constexpr int kPBytes = 2 * R * kTreeKeys * kCell; // both parts of the weights
-  // two weight buffers, or one where two would leave a single stage
-  static constexpr int kPB = (!kE4m3 && R == 64) ? 1 : 2;
-  static constexpr int kRW = R / 2;                         // rows of a softmax warpgroup
+  static constexpr int kTile = kTreeKeys * kRowBytes;       // bytes of a slot: a tile of K or of V
+  static constexpr int kParts = kE4m3 ? 2 : 1;              // of queries and weights
+  static constexpr int kN = kParts * R;                     // columns of S and of O^T
+  static constexpr int kQBytes = kN * kRowBytes;
+  static constexpr int kPBytes = kN * kTreeKeys * kCell;
+  // Up to 32 rows the softmax warpgroups take turns by tile, each with all
+  // rows and an O of its own; 64 rows of state do not fit a thread, and they
+  // take half the rows each.
+  static constexpr bool kTurns = R <= 32;
+  static constexpr int kRT = kTurns ? R : R / 2;            // rows of a softmax thread
+  static constexpr int kRO = R / 2;                         // rows it writes out
+  static constexpr int kSoftWarps = kTurns ? 4 : 8;         // that work on one tile
   static constexpr int kQOff = 0;
   static constexpr int kPOff = kQOff + 2 * kQBytes;
-  static constexpr int kRowsOff = kPOff + kPB * kPBytes;
+  static constexpr int kScaleOff = kPOff + 2 * kPBytes;     // [kTreeScaleRing][K, V][128]
+  static constexpr int kRowsOff = kScaleOff + (kE4m3 ? kTreeScaleRing * 256 : 0);
   static constexpr int kRowsBytes = (static_cast<int>(sizeof(TreeRows)) + 15) / 16 * 16;
-  static constexpr int kMaxOff = kRowsOff + 2 * kRowsBytes;      // [2][R/2][4] floats
-  static constexpr int kMiscOff = kMaxOff + R * 4 * 4;
-  static constexpr int kMaxStages = 8;
-  static constexpr int kNumBars = 2 * kMaxStages + 13;
+  static constexpr int kMaxOff = kRowsOff + 2 * kRowsBytes;      // [2][kRT][4] floats
+  static constexpr int kRefOff = kMaxOff + 2 * kRT * 16;         // [2][kRT] floats
+  static constexpr int kMiscOff = kRefOff + 2 * kRT * 4;
+  static constexpr int kMaxSlots = 12;                      // scales outlive their tile's slots
+  static constexpr int kNumBars = 2 * kMaxSlots + 14;
   static constexpr int kMiscBytes = kNumBars * 8 + 128;
   static constexpr int kRingOff = (kMiscOff + kMiscBytes + 1023) / 1024 * 1024;
-  static constexpr int kFit = (232448 - kRingOff) / kStage;
-  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-  static constexpr int kSmem = kRingOff + kStages * kStage;
-  static constexpr int kOCol = 2 * kSN;                     // O^T, both parts, after two S buffers
-  static constexpr int kTmemCols = kOCol + 2 * R <= 128 ? 128 : kOCol + 2 * R <= 256 ? 256 : 512;
-  static_assert(kStages >= 2 && kSmem <= 232448, "shared memory budget");
-  static_assert(kOCol + 2 * R <= 512, "tensor memory budget");
+  static constexpr int kFit = (232448 - kRingOff) / kTile / 2 * 2;
+  static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;  // K and V in turn: even
+  static constexpr int kSmem = kRingOff + kSlots * kTile;
+  static constexpr int kOCol = 2 * kN;                      // O^T after two S buffers
+  static constexpr int kCols = kOCol + (kTurns ? 2 : 1) * kN;
+  static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kSlots >= 4 && kSmem <= 232448, "shared memory budget");
+  static_assert(kCols <= 512, "tensor memory budget");
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "operand alignment");
+  static_assert(kMiscOff % 16 == 0, "barrier alignment");
   // byte offset of 16-byte piece c of row r in a block of `rows` swizzled rows
   static __device__ __forceinline__ uint32_t at(int r, int c, int rows) {
     if (kLine == 128)
@@ -274,6 +286,15 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&x)[N]
   }
 }
 
+// y += x * f.
+template <int N>
+__device__ __forceinline__ void fma_rows(const float (&x)[N], float f, float* y) {
+  const uint64_t f2 = f2_pack(f, f);
+#pragma unroll
+  for (int j = 0; j < N; j += 2)
+    f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), f2, f2_pack(y[j], y[j + 1])), y[j], y[j + 1]);
+}
+
 // Whether `x` holds for any thread of the named barrier's `count`.
 __device__ __forceinline__ bool barrier_or(uint32_t id, uint32_t count, bool x) {
   uint32_t r;
@@ -311,11 +332,32 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t w) {
 }
 
 // What the second part of a split is multiplied by: with the first part
-// rounded to 4 bits, |rest| <= 8 for queries below 256 and <= 8 for weights up
-// to 256, so the products stay below 448 and as far above 2^-9 as they can.
-constexpr float kQueryRest = 16.f, kWeightRest = 32.f;
-// Weights are 2^(s - r): up to 2^8 (e4m3 holds 448), reached when r is set.
-constexpr float kWeightTop = 8.f;
+// rounded to 4 bits, |rest| <= 8 for queries below 256 and <= 16 for weights
+// up to 416, so the products stay below 448 and far above 2^-9.
+constexpr float kQueryRest = 16.f, kWeightRest = 16.f;
+// Weights are 2^(s - r).  Over a bf16 cache r is a maximum that a later score
+// may outgrow by 2^8 before O is rescaled; over e4m3, whose largest value is
+// 448, r is set 7 below the maximum and outgrown at 2^8.7 = 416.
+constexpr float kTopBf16 = 0.f, kOverBf16 = 8.f, kTopE4m3 = 7.f, kOverE4m3 = 8.7f;
+
+// All bits of the codes / bf16 halves in w that are infinite or NaN.
+template <int FMT>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
+  return FMT == kCacheBf16 ? __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u)
+                           : __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// The codes of what the codes `w` leave of two weights, times kWeightRest.
+__device__ __forceinline__ uint32_t e4m3x2_rest(float x0, float x1, uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+  // at most 448 * 16 in fp16: exact
+  const __half2 n = __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(-kWeightRest));
+  const float2 nf = __half22float2(n);
+  float r0, r1;
+  f2_unpack(f2_fma(f2_pack(x0, x1), f2_pack(kWeightRest, kWeightRest), f2_pack(nf.x, nf.y)), r0, r1);
+  return e4m3x2(r0, r1);
+}
 
 // b * log2(e) of a bias b, kept finite where b is: a bias of the type's lowest
 // value then still orders below every other score instead of hiding its key.
@@ -329,7 +371,7 @@ __device__ __forceinline__ float t5_bias_log2(const TreeArgs& a, int rel, int h)
 }
 
 // ------------------------------------------------------------- query warp
-// One piece's query rows as the K-major operand `dst` (kSN rows; e4m3: first
+// One piece's query rows as the K-major operand `dst` (kN rows; e4m3: first
 // parts in rows 0 .. R - 1, second parts from row R on) and their TreeRows.
 template <int D, int FMT, int R>
 __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeWalk<R>& w, int lane,
@@ -344,19 +386,30 @@ __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeW
   };
   for (int n = lane; n < s.n; n += 32) info->depth[n] = __popcll(sees_of(n) & ~(1ull << n));
   for (int r = lane; r < R; r += 32) {
-    TreeRow t{0ull, a.scale_log2, 0.f, s.ctx, w.hkv * a.G};
+    uint64_t sees = 0;
+    float slope = 0.f;
+    int pos = s.ctx, head = w.hkv * a.G;
+    int64_t out = 0, lse = 0;
     if (r < n_rows) {
       const int x = w.block * R + r;
       const int n = x / a.G;
-      t.sees = sees_of(n);
-      t.pos = s.ctx + __popcll(t.sees & ~(1ull << n));
-      t.head = w.hkv * a.G + (x - n * a.G);
+      sees = sees_of(n);
+      pos += __popcll(sees & ~(1ull << n));
+      head += x - n * a.G;
+      out = static_cast<int64_t>(s.row0 + n) * a.o_t + static_cast<int64_t>(head) * a.o_h;
+      lse = static_cast<int64_t>(head) * a.T + s.row0 + n;
       if (bias) {
-        if (a.alibi_slopes) t.bias = a.alibi_slopes[t.head];
-        else if (a.t5.one_lo_max != INT_MIN) t.bias = t5_bias_log2(a, a.t5.one_lo_max, t.head);
+        if (a.alibi_slopes) slope = a.alibi_slopes[head];
+        else if (a.t5.one_lo_max != INT_MIN) slope = t5_bias_log2(a, a.t5.one_lo_max, head);
       }
     }
-    info->row[r] = t;
+    info->scale[r] = a.scale_log2;
+    info->bias[r] = slope;
+    info->sees[r] = sees;
+    info->pos[r] = pos;
+    info->head[r] = head;
+    info->out[r] = out;
+    info->lse[r] = lse;
   }
   __syncwarp();
   constexpr int kLanes = D / 8;        // lanes of a row, 8 elements each
@@ -411,8 +464,14 @@ __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeW
           make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
       *reinterpret_cast<uint2*>(dst + L::at(R + r, c >> 1, 2 * R) + (c & 1) * 8) =
           make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      if (c == 0) info->row[r].scale = a.scale_log2 / f1 / f2;
+      if (c == 0) info->scale[r] = a.scale_log2 / f1 / f2;
     }
+  }
+  for (int n = lane; n < s.n; n += 32) {
+    uint64_t m = 0;
+#pragma unroll 8
+    for (int r = 0; r < R; ++r) m |= ((info->sees[r] >> n) & 1ull) << r;
+    info->seen[n] = m;
   }
 }
 
@@ -423,9 +482,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     const __grid_constant__ CUtensorMap mv) {
   using L = TreeLayout<D, FMT, R>;
   constexpr bool E4 = L::kE4m3;
-  constexpr int ST = L::kStages;
-  constexpr int PB = L::kPB;
-  constexpr int RW = L::kRW;
+  constexpr int NS = L::kSlots;
+  constexpr int RT = L::kRT;
+  constexpr int RO = L::kRO;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!smem_base_ok(smem)) {
     if (threadIdx.x == 0) atomicOr(&g_device_status, kStatusMisaligned);
@@ -436,40 +495,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   const int warp = __shfl_sync(~0u, tid >> 5, 0);
   auto bar = [&](int i) -> uint32_t { return sb + L::kMiscOff + 8 * i; };
   auto full = [&](int s) { return bar(s); };
-  auto empty = [&](int s) { return bar(L::kMaxStages + s); };
-  constexpr int kB = 2 * L::kMaxStages;
+  auto empty = [&](int s) { return bar(L::kMaxSlots + s); };
+  constexpr int kB = 2 * L::kMaxSlots;
   auto s_full = [&](int x) { return bar(kB + x); };       // S of a tile is in tensor memory
   auto s_free = [&](int x) { return bar(kB + 2 + x); };   // ... and in registers
   auto p_full = [&](int x) { return bar(kB + 4 + x); };   // weights are in shared memory
   auto pv_done = [&](int x) { return bar(kB + 6 + x); };  // ... and added to O
   auto q_full = [&](int x) { return bar(kB + 8 + x); };   // a piece's queries are laid out
   auto q_free = [&](int x) { return bar(kB + 10 + x); };  // ... and the piece is done
-  const uint32_t drain = bar(kB + 12);
+  auto drain = [&](int x) { return bar(kB + 12 + x); };
+  // K of the CTA's tile `it` is item 2 it of the ring, its V item 2 it + 1
+  auto slot_off = [&](uint32_t item) { return L::kRingOff + (item % NS) * L::kTile; };
   uint8_t* misc = smem + L::kMiscOff + L::kNumBars * 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
-  uint32_t* dirty = reinterpret_cast<uint32_t*>(misc + 16);   // [4] bits of keys
+  uint32_t* dirty = reinterpret_cast<uint32_t*>(misc + 96);   // [2][4] bits of keys
   int64_t* start_left = reinterpret_cast<int64_t*>(misc + 32);
   int* start_b = reinterpret_cast<int*>(misc + 40);
   int* start_off = reinterpret_cast<int*>(misc + 44);
   TreeSeq* start_seq = reinterpret_cast<TreeSeq*>(misc + 48);  // 28 bytes
 
-  if (warp == kTreeIssuer) {
+  if (warp == kTreeIssueS) {
     if (lane == 0) {
       *abort_flag = 0;
-      for (int s = 0; s < ST; ++s) {
+      for (int s = 0; s < NS; ++s) {
         mbar_init(full(s), 1);
         mbar_init(empty(s), 1);
       }
       for (int x = 0; x < 2; ++x) {
         mbar_init(s_full(x), 1);
-        mbar_init(s_free(x), 8);
-        mbar_init(p_full(x), 8);
+        mbar_init(s_free(x), L::kSoftWarps);
+        mbar_init(p_full(x), L::kSoftWarps);
         mbar_init(pv_done(x), 1);
         mbar_init(q_full(x), 1);
         mbar_init(q_free(x), 8);
+        mbar_init(drain(x), 1);
       }
-      mbar_init(drain, 1);
       fence_mbar_init();
       tma_prefetch_desc(&mk);
       tma_prefetch_desc(&mv);
@@ -542,7 +603,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     // ------------------------------------------------------------ producer
     const int boxes = kTreeKeys / a.box_rows;  // <= 8
     const uint32_t box_bytes = static_cast<uint32_t>(a.box_rows) * L::kRowBytes;
-    uint32_t it = 0;
+    uint32_t it = 0, item = 0;
     bool ok = true;
     while (ok && walk.next(a)) {
       const int* row = a.table + static_cast<int64_t>(walk.b) * a.table_b;
@@ -559,35 +620,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         return page;
       };
       int page = page_of(walk.t0);
-      for (int i = 0; i < walk.nt; ++i, ++it) {
+      for (int i = 0; ok && i < walk.nt; ++i, ++it) {
         const int t = walk.t0 + i;
         const int next_page = i + 1 < walk.nt ? page_of(t + 1) : -1;
-        const int st = it % ST;
-        if (it >= ST) ok = mbar_wait(empty(st), ((it / ST) - 1) & 1, ctl);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
         const bool copy = page >= 0;
         const bool scales = E4 && copy && page < a.num_pages;
         const int n_copy = __popc(__ballot_sync(~0u, copy));
         const int n_scale = __popc(__ballot_sync(~0u, scales));
-        const uint32_t base = sb + L::kRingOff + st * L::kStage;
-        if (lane == 0) mbar_expect_tx(full(st), 2u * (n_copy * box_bytes + n_scale * a.box_rows));
-        __syncwarp();
-        if (copy) {
-          const int pos = (walk.s.tile0 + t) * kTreeKeys + lane * a.box_rows;
-          const int r = pos & (a.page_size - 1);
-          const uint32_t dst = base + static_cast<uint32_t>(lane) * a.box_rows * L::kLine;
+        const int r = ((walk.s.tile0 + t) * kTreeKeys + lane * a.box_rows) & (a.page_size - 1);
 #pragma unroll
-          for (int h = 0; h < L::kHalves; ++h)
-            tma_load_4d(dst + h * kTreeKeys * 128, &mk, full(st), h * 64, r, walk.hkv, page);
+        for (int kv = 0; kv < 2; ++kv, ++item) {
+          const uint32_t f = full(item % NS);
+          if (item >= NS) ok = mbar_wait(empty(item % NS), ((item / NS) - 1) & 1, ctl);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          // the scales of both come with K.  Their place was tile it - 8's, whose
+          // P V is done: V's slot of tile it - 1 was free for that tile's copy, and
+          // the tile before it there is at most 7 tiles back.
+          if (lane == 0) mbar_expect_tx(f, n_copy * box_bytes + (kv == 0 ? 2u * n_scale * a.box_rows : 0u));
+          __syncwarp();
+          if (copy) {
+            const uint32_t dst = sb + slot_off(item) + static_cast<uint32_t>(lane) * a.box_rows * L::kLine;
 #pragma unroll
-          for (int h = 0; h < L::kHalves; ++h)
-            tma_load_4d(dst + L::kTile + h * kTreeKeys * 128, &mv, full(st), h * 64, r, walk.hkv, page);
-          if (scales) {
+            for (int h = 0; h < L::kHalves; ++h)
+              tma_load_4d(dst + h * kTreeKeys * 128, kv ? &mv : &mk, f, h * 64, r, walk.hkv, page);
+          }
+          if (kv == 0 && scales) {
             const int64_t off = page * a.ss_page + walk.hkv * a.ss_head + r;
-            const uint32_t sdst = base + 2 * L::kTile + lane * a.box_rows;
-            bulk_load(sdst, a.ks + off, a.box_rows, full(st));
-            bulk_load(sdst + 512, a.vs + off, a.box_rows, full(st));
+            const uint32_t dst = sb + L::kScaleOff + (it % kTreeScaleRing) * 256 + lane * a.box_rows;
+            bulk_load(dst, a.ks + off, a.box_rows, f);
+            bulk_load(dst + 128, a.vs + off, a.box_rows, f);
           }
         }
         page = next_page;
@@ -597,7 +659,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       // a wait that ran out ends the CTA: let the copies in flight land first
       volatile int never = 0;
       const WaitCtl ign{&never, a.wait_limit_ns};
-      for (uint32_t j = it > ST ? it - ST : 0; j < it; ++j) mbar_wait(full(j % ST), (j / ST) & 1, ign);
+      for (uint32_t j = item > NS ? item - NS : 0; j < item; ++j) mbar_wait(full(j % NS), (j / NS) & 1, ign);
     }
   } else if (warp == kTreeQuery) {
     // ------------------------------------------------------------- queries
@@ -615,15 +677,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       if (lane == 0) mbar_arrive(q_full(x));
       ++u;
     }
-  } else if (warp == kTreeIssuer) {
-    // ----------------------------------------------------------- MMA issuer
+  } else if (warp == kTreeIssueS || warp == kTreeIssueO) {
+    // ----------------------------------------------------------- MMA issuers
+    const bool is_s = warp == kTreeIssueS;
     if (lane == 0) {
-      constexpr uint32_t kNone = (1u << 4) | (static_cast<uint32_t>(128 >> 4) << 24);  // f32, M = 128
-      constexpr uint32_t kTypes = E4 ? 0u : (1u << 7) | (1u << 10);
-      constexpr uint32_t kIdS = kNone | kTypes | (static_cast<uint32_t>(L::kSN >> 3) << 17);
-      constexpr uint32_t kIdO = kNone | kTypes | (1u << 15) | (1u << 16) |
-                                (static_cast<uint32_t>(2 * R >> 3) << 17);
+      constexpr uint32_t kShape = (1u << 4) | (E4 ? 0u : (1u << 7) | (1u << 10)) |
+                                  (static_cast<uint32_t>(L::kN >> 3) << 17) |
+                                  (static_cast<uint32_t>(128 >> 4) << 24);  // f32, M = 128
+      constexpr uint32_t kIdS = kShape, kIdO = kShape | (1u << 15) | (1u << 16);
       constexpr uint32_t kSwz = L::kLine == 128 ? 2u : 4u;
+      constexpr int kStep = E4 ? 32 : 16;  // keys per instruction of P V
       const uint64_t dk = tree_desc(sb, 16, 8 * L::kLine, kSwz);  // K and Q, K-major
       // V, MN-major: 64-wide halves kTreeKeys rows apart; at d = 64 the
       // tile's rows 64 .. 127 repeat its first 64 and are not read back
@@ -631,89 +694,94 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       const uint64_t dp = tree_desc(sb, 128, kTreeKeys * 16, 0);  // weights, MN-major, plain
       uint32_t it = 0, u = 0;
       bool ok = true;
-      auto add_values = [&](uint32_t j) -> bool {  // O^T += V^T P^T of tile j
-        const int pb = j % PB, st = j % ST;
-        if (!mbar_wait(p_full(pb), (j / PB) & 1, ctl)) return false;
-        tc_fence_after();
-        const uint64_t vd = dv + ((L::kRingOff + st * L::kStage + L::kTile) >> 4);
-        const uint64_t pd = dp + ((L::kPOff + pb * L::kPBytes) >> 4);
-        constexpr int kStep = E4 ? 32 : 16;  // keys per instruction
-#pragma unroll
-        for (int k = 0; k < kTreeKeys / kStep; ++k)
-          tree_mma<FMT>(tmem + L::kOCol, vd + (k * kStep * L::kLine >> 4), pd + (k * kStep * 16 >> 4), kIdO, 1u);
-        mma_commit(pv_done(pb));
-        mma_commit(empty(st));
-        return true;
-      };
       while (ok && walk.next(a)) {
-        ok = mbar_wait(q_full(u & 1), (u >> 1) & 1, ctl);
+        if (is_s) ok = mbar_wait(q_full(u & 1), (u >> 1) & 1, ctl);
+        const uint64_t qd = dk + ((L::kQOff + (u & 1) * L::kQBytes) >> 4);
         for (int i = 0; ok && i < walk.nt; ++i, ++it) {
-          const int st = it % ST, x = it & 1;
-          if (!(ok = mbar_wait(full(st), (it / ST) & 1, ctl))) break;
-          if (it >= 2 && !(ok = mbar_wait(s_free(x), ((it >> 1) - 1) & 1, ctl))) break;
-          tc_fence_after();
-          const uint64_t kd = dk + ((L::kRingOff + st * L::kStage) >> 4);
-          const uint64_t qd = dk + ((L::kQOff + (u & 1) * L::kQBytes) >> 4);
+          const uint32_t x = it & 1, item = 2 * it + (is_s ? 0 : 1);
+          if (!(ok = mbar_wait(full(item % NS), (item / NS) & 1, ctl))) break;
+          if (is_s) {  // S^T = K Q^T
+            if (it >= 2 && !(ok = mbar_wait(s_free(x), ((it >> 1) - 1) & 1, ctl))) break;
+            tc_fence_after();
+            const uint64_t kd = dk + (slot_off(item) >> 4);
 #pragma unroll
-          for (int k = 0; k < L::kRowBytes / 32; ++k)
-            tree_mma<FMT>(tmem + x * L::kSN, kd + (kmajor_koff(k, kTreeKeys) >> 4),
-                          qd + (kmajor_koff(k, L::kSN) >> 4), kIdS, k > 0 ? 1u : 0u);
-          mma_commit(s_full(x));
-          if (it > 0) ok = add_values(it - 1);
+            for (int k = 0; k < L::kRowBytes / 32; ++k)
+              tree_mma<FMT>(tmem + x * L::kN, kd + (kmajor_koff(k, kTreeKeys) >> 4),
+                            qd + (kmajor_koff(k, L::kN) >> 4), kIdS, k > 0 ? 1u : 0u);
+            mma_commit(s_full(x));
+          } else {  // O^T += V^T P^T; a piece's first tile in an O overwrites it
+            if (!(ok = mbar_wait(p_full(x), (it >> 1) & 1, ctl))) break;
+            tc_fence_after();
+            const uint64_t vd = dv + (slot_off(item) >> 4);
+            const uint64_t pd = dp + ((L::kPOff + x * L::kPBytes) >> 4);
+            const uint32_t o = tmem + L::kOCol + (L::kTurns ? x * L::kN : 0);
+            const bool add = i >= (L::kTurns ? 2 : 1);
+#pragma unroll
+            for (int k = 0; k < kTreeKeys / kStep; ++k)
+              tree_mma<FMT>(o, vd + (k * kStep * L::kLine >> 4), pd + (k * kStep * 16 >> 4), kIdO,
+                            add || k > 0 ? 1u : 0u);
+            mma_commit(pv_done(x));
+          }
+          mma_commit(empty(item % NS));
         }
         ++u;
       }
-      if (ok && it > 0) add_values(it - 1);
       // every MMA issued is done before tensor memory is freed
       volatile int never = 0;
       const WaitCtl ign{&never, a.wait_limit_ns};
-      mma_commit(drain);
-      mbar_wait(drain, 0, ign);
+      mma_commit(drain(is_s ? 0 : 1));
+      mbar_wait(drain(is_s ? 0 : 1), 0, ign);
     }
     __syncwarp();
   } else {
-    // -------- softmax: warpgroup wg has rows [RW wg, RW wg + RW), thread = key = row of O^T
+    // ------------- softmax: thread = key of the tile, and row of O^T at the end
     const int wg = warp >> 2;
     const int me = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_o = tmem + lanes + L::kOCol + wg * RW;
-    float* wmax = reinterpret_cast<float*>(smem + L::kMaxOff) + wg * RW * 4;  // [RW][4 warps]
+    const int row0 = L::kTurns ? 0 : wg * RT;                     // first row of this thread's scores
+    const uint32_t t_o = tmem + lanes + L::kOCol + (L::kTurns ? wg * L::kN : row0);
+    float* wmax = reinterpret_cast<float*>(smem + L::kMaxOff);    // [2][RT][4 warps]
+    float* mine = wmax + wg * RT * 4;
+    float* refs = reinterpret_cast<float*>(smem + L::kRefOff);    // [2][RT]
     // After a wait that ran out the warps go on without waiting, through the
     // same barriers, so that no thread is left at one.
     bool ok = true;
     uint32_t it = 0, u = 0;
-    auto values_done = [&](uint32_t j) {  // P V of tile j has been added to O
-      if (ok) ok = mbar_wait(pv_done(j % PB), (j / PB) & 1, ctl);
+    auto wait = [&](uint32_t b, uint32_t phase) {
+      if (ok) ok = mbar_wait(b, phase, ctl);
       ok = __all_sync(~0u, ok);
+    };
+    auto values_done = [&](uint32_t j) {  // P V of tile j has been added to O
+      wait(pv_done(j & 1), (j >> 1) & 1);
       tc_fence_after();
     };
     while (walk.next(a)) {
       const TreeSeq& s = walk.s;
       const TreeRows* info = reinterpret_cast<const TreeRows*>(smem + L::kRowsOff + (u & 1) * L::kRowsBytes);
-      const TreeRow* rows = info->row + wg * RW;
-      if (ok) ok = mbar_wait(q_full(u & 1), (u >> 1) & 1, ctl);
-      ok = __all_sync(~0u, ok);
-      float ref[RW], l[RW];
+      wait(q_full(u & 1), (u >> 1) & 1);
+      float ref[RT], l[RT];
 #pragma unroll
-      for (int j = 0; j < RW; ++j) {
+      for (int j = 0; j < RT; ++j) {
         ref[j] = -FLT_MAX;
         l[j] = 0.f;
       }
+      bool fresh = true;  // no tile of the piece in this warpgroup's O yet
       for (int i = 0; i < walk.nt; ++i, ++it) {
-        const int st = it % ST, x = it & 1, pb = it % PB;
+        if (L::kTurns && (it & 1) != static_cast<uint32_t>(wg)) continue;
+        const uint32_t x = it & 1;
         const int key0 = (s.tile0 + walk.t0 + i) * kTreeKeys;
         const int key = key0 + me;
-        const uint8_t* stage = smem + L::kRingOff + st * L::kStage;
-        if (ok) ok = mbar_wait(s_full(x), (it >> 1) & 1, ctl);
-        ok = __all_sync(~0u, ok);
+        wait(s_full(x), (it >> 1) & 1);
         tc_fence_after();
-        float sc[RW];
-        tmem_ld_cols<RW>(tmem + lanes + x * L::kSN + wg * RW, sc);
+        float sc[RT];
+        tmem_ld_cols<RT>(tmem + lanes + x * L::kN + row0, sc);
         if constexpr (E4) {
-          float rest[RW];
-          tmem_ld_cols<RW>(tmem + lanes + x * L::kSN + R + wg * RW, rest);
 #pragma unroll
-          for (int j = 0; j < RW; ++j) sc[j] = fmaf(rest[j], 1.f / kQueryRest, sc[j]);
+          for (int j0 = 0; j0 < RT; j0 += 16) {
+            float rest[16];
+            tmem_ld_cols<16>(tmem + lanes + x * L::kN + R + row0 + j0, rest);
+            fma_rows<16>(rest, 1.f / kQueryRest, sc + j0);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -722,16 +790,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         // scores in log2 units, plus the exponent of the key's value scale
         float v_inv = 1.f;
         if constexpr (E4) {
-          const float kf = e8m0_float(stage[2 * L::kTile + me]);
-          const int ve = stage[2 * L::kTile + 512 + me];
+          const uint8_t* sc8 = smem + L::kScaleOff + (it % kTreeScaleRing) * 256 + me;
+          const float kf = e8m0_float(sc8[0]);
+          const int ve = sc8[128];
           v_inv = e8m0_float(static_cast<uint32_t>(max(254 - ve, 0)));
+          const uint64_t kf2 = f2_pack(kf, kf);
           const float vx = static_cast<float>(ve - 127);
+          const uint64_t vx2 = f2_pack(vx, vx);
 #pragma unroll
-          for (int j = 0; j < RW; ++j)
-            sc[j] = BIAS ? sc[j] * rows[j].scale * kf : fmaf(sc[j] * rows[j].scale, kf, vx);
+          for (int j = 0; j < RT; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(info->scale + row0 + j);
+            f2_unpack(f2_fma(f2_mul(f2_pack(sc[j], sc[j + 1]), kf2), f2_pack(f.x, f.y), vx2), sc[j], sc[j + 1]);
+            f2_unpack(f2_fma(f2_mul(f2_pack(sc[j + 2], sc[j + 3]), kf2), f2_pack(f.z, f.w), vx2), sc[j + 2],
+                      sc[j + 3]);
+          }
         } else {
+          const uint64_t f2 = f2_pack(a.scale_log2, a.scale_log2);
 #pragma unroll
-          for (int j = 0; j < RW; ++j) sc[j] *= a.scale_log2;
+          for (int j = 0; j < RT; j += 2) f2_unpack(f2_mul(f2_pack(sc[j], sc[j + 1]), f2), sc[j], sc[j + 1]);
         }
         // all keys of the tile seen by every row: context keys inside every
         // node's window (a node's position is below ctx + n)
@@ -739,143 +815,151 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         const int node = key - s.ctx;
         const int key_pos = node >= 0 ? s.ctx + (node < s.n ? info->depth[node] : 0) : key;
         if constexpr (BIAS != 0) {
+          if (a.alibi_slopes) {
 #pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            const int rel = key_pos - rows[j].pos;
-            if (a.alibi_slopes)
-              sc[j] += bias_to_log2(-rows[j].bias * fabsf(static_cast<float>(rel)));
-            else
-              sc[j] += rel <= a.t5.one_lo_max ? rows[j].bias : t5_bias_log2(a, rel, rows[j].head);
-          }
-          if constexpr (E4) {
-            const float vx = static_cast<float>(static_cast<int>(stage[2 * L::kTile + 512 + me]) - 127);
+            for (int j = 0; j < RT; ++j)
+              sc[j] += bias_to_log2(-info->bias[row0 + j] *
+                                    fabsf(static_cast<float>(key_pos - info->pos[row0 + j])));
+          } else if (key0 + kTreeKeys - 1 - s.ctx <= a.t5.one_lo_max) {
+            // every distance of the tile in the last bucket
 #pragma unroll
-            for (int j = 0; j < RW; ++j) sc[j] += vx;
+            for (int j = 0; j < RT; ++j) sc[j] += info->bias[row0 + j];
+          } else {
+            // the buckets first, then the loads, eight at a time in flight
+#pragma unroll
+            for (int j0 = 0; j0 < RT; j0 += 8) {
+              int at[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                at[j] = t5_bucket(key_pos - info->pos[row0 + j0 + j], a.t5) * a.Hq + info->head[row0 + j0 + j];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) sc[j0 + j] += bias_to_log2(a.t5_table[at[j]]);
+            }
           }
         }
         if (masked) {
+          const uint32_t seen = node < 0 ? ~0u : node < s.n ? static_cast<uint32_t>(info->seen[node] >> row0) : 0u;
 #pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            bool seen = node < 0 || (node < 64 && ((rows[j].sees >> node) & 1ull));
-            if (a.wl >= 0) seen = seen && rows[j].pos - key_pos <= a.wl;
-            if (!seen) sc[j] = -INFINITY;
+          for (int j = 0; j < RT; ++j)
+            if (!((seen >> j) & 1u)) sc[j] = -INFINITY;
+          if (a.wl >= 0) {
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+              if (info->pos[row0 + j] - key_pos > a.wl) sc[j] = -INFINITY;
           }
         }
 
+        // the weight buffer is free, and with turns this warpgroup's O at rest
+        if (it >= 2) values_done(it - 2);
         // a new reference where a score has outgrown the old one
         float over = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < RW; j += 2) over = fmax3(over, sc[j] - ref[j], sc[j + 1] - ref[j + 1]);
-        if (barrier_or(1 + wg, 128, over > kWeightTop || i == 0)) {
+        for (int j = 0; j < RT; j += 2) {
+          float d0, d1;
+          f2_unpack(f2_sub(f2_pack(sc[j], sc[j + 1]), f2_pack(ref[j], ref[j + 1])), d0, d1);
+          over = fmax3(over, d0, d1);
+        }
+        if (barrier_or(1 + wg, 128, over > (E4 ? kOverE4m3 : kOverBf16) || fresh)) {
           float keep = 0.f;
 #pragma unroll
-          for (int j = 0; j < RW; ++j) {
+          for (int j = 0; j < RT; ++j) {
             const float m = warp_max(sc[j]);
             if (lane == j) keep = m;
           }
-          if (lane < RW) wmax[lane * 4 + (warp & 3)] = keep;
+          if (lane < RT) mine[lane * 4 + (warp & 3)] = keep;
           named_barrier(1 + wg, 128);
-          float f[RW];
+          if (!L::kTurns && !fresh) values_done(it - 1);
 #pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            const float4 w4 = *reinterpret_cast<const float4*>(wmax + j * 4);
-            float m = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w));
-            m = fmaxf(m - (E4 ? kWeightTop : 0.f), ref[j]);
-            f[j] = fast_exp2(ref[j] - m);
-            ref[j] = m;
-            l[j] *= f[j];
-          }
-          if (i > 0) values_done(it - 1);
+          for (int j0 = 0; j0 < RT; j0 += 8) {
+            float f[8];
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            float o[RW];
-            if (i > 0) {
-              tmem_ld_cols<RW>(t_o + part * R, o);
-#pragma unroll
-              for (int j = 0; j < RW; ++j) o[j] *= f[j];
-            } else {
-#pragma unroll
-              for (int j = 0; j < RW; ++j) o[j] = 0.f;
+            for (int j = 0; j < 8; ++j) {
+              const float4 w4 = *reinterpret_cast<const float4*>(mine + (j0 + j) * 4);
+              float m = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w));
+              m = fmaxf(m - (E4 ? kTopE4m3 : kTopBf16), ref[j0 + j]);
+              f[j] = fast_exp2(ref[j0 + j] - m);
+              ref[j0 + j] = m;
+              l[j0 + j] *= f[j];
             }
-            tmem_st_cols<RW>(t_o + part * R, o);
+            if (!fresh) {
+#pragma unroll
+              for (int part = 0; part < L::kParts; ++part) {
+                float o[8];
+                tmem_ld_cols<8>(t_o + part * R + j0, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] *= f[j];
+                tmem_st_cols<8>(t_o + part * R + j0, o);
+              }
+            }
           }
-          named_barrier(1 + wg, 128);  // wmax is read
+          named_barrier(1 + wg, 128);  // `mine` is read
         }
 
-        if (it >= PB) values_done(it - PB);  // the weight buffer is free
-        uint8_t* pbuf = smem + L::kPOff + pb * L::kPBytes + me * 16;
+        uint8_t* pbuf = smem + L::kPOff + x * L::kPBytes + me * 16;
+        const uint64_t v_inv2 = f2_pack(v_inv, v_inv);
 #pragma unroll
-        for (int j = 0; j < RW; ++j) {
-          sc[j] = fast_exp2(sc[j] - ref[j]);
-          l[j] = E4 ? fmaf(sc[j], v_inv, l[j]) : l[j] + sc[j];
+        for (int j = 0; j < RT; j += 2) {
+          f2_unpack(f2_sub(f2_pack(sc[j], sc[j + 1]), f2_pack(ref[j], ref[j + 1])), sc[j], sc[j + 1]);
+          sc[j] = fast_exp2(sc[j]);
+          sc[j + 1] = fast_exp2(sc[j + 1]);
+          const uint64_t p2 = f2_pack(sc[j], sc[j + 1]), l2 = f2_pack(l[j], l[j + 1]);
+          f2_unpack(E4 ? f2_fma(p2, v_inv2, l2) : f2_add(p2, l2), l[j], l[j + 1]);
         }
-        // both parts of the weights: 16 bytes of one key's rows at a time
+        // the weights: 16 bytes of one key's rows at a time
         if constexpr (E4) {
-          uint32_t hi[RW / 4], lo[RW / 4];
+          uint32_t hi[RT / 4], lo[RT / 4];
 #pragma unroll
-          for (int j = 0; j < RW; j += 4) {
+          for (int j = 0; j < RT; j += 4) {
             const uint32_t h0 = e4m3x2(sc[j], sc[j + 1]), h1 = e4m3x2(sc[j + 2], sc[j + 3]);
-            const float2 a0 = e4m3x2_value(h0), a1 = e4m3x2_value(h1);
             hi[j / 4] = h0 | h1 << 16;
-            lo[j / 4] = e4m3x2((sc[j] - a0.x) * kWeightRest, (sc[j + 1] - a0.y) * kWeightRest) |
-                        e4m3x2((sc[j + 2] - a1.x) * kWeightRest, (sc[j + 3] - a1.y) * kWeightRest) << 16;
+            lo[j / 4] = e4m3x2_rest(sc[j], sc[j + 1], h0) | e4m3x2_rest(sc[j + 2], sc[j + 3], h1) << 16;
           }
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
             const uint32_t* w = part ? lo : hi;
-            const int row0 = part * R + wg * RW;
-            uint8_t* dst = pbuf + (row0 / 16) * (kTreeKeys * 16) + row0 % 16;
-            if constexpr (RW == 8) {
-              *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-            } else {
 #pragma unroll
-              for (int j = 0; j < RW / 4; j += 4)
-                *reinterpret_cast<uint4*>(dst + (j / 4) * (kTreeKeys * 16)) =
-                    make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
-            }
+            for (int j = 0; j < RT / 4; j += 4)
+              *reinterpret_cast<uint4*>(pbuf + ((part * R + row0) / 16 + j / 4) * (kTreeKeys * 16)) =
+                  make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < RW; j += 8) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float p0 = sc[j + 2 * e], p1 = sc[j + 2 * e + 1];
-              hi[e] = pack_bf16x2(p0, p1);
-              lo[e] = pack_bf16x2(p0 - __uint_as_float(hi[e] << 16),
-                                  p1 - __uint_as_float(hi[e] & 0xffff0000u));
-            }
-            uint8_t* dst = pbuf + ((wg * RW + j) / 8) * (kTreeKeys * 16);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + R / 8 * (kTreeKeys * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
+          for (int j = 0; j < RT; j += 8)
+            *reinterpret_cast<uint4*>(pbuf + ((row0 + j) / 8) * (kTreeKeys * 16)) =
+                make_uint4(pack_bf16x2(sc[j], sc[j + 1]), pack_bf16x2(sc[j + 2], sc[j + 3]),
+                           pack_bf16x2(sc[j + 4], sc[j + 5]), pack_bf16x2(sc[j + 6], sc[j + 7]));
         }
+        bool mend = false;
         if (masked) {
           // 0 * NaN is NaN: an infinite or NaN value that some row must not see
           // (stale rows of a page among them) is taken out of the tile, and
-          // added to the rows that do see it here
+          // added to the rows that do see it once P V of the tile is in O
           constexpr int kPieces = L::kRowBytes / 16;
-          uint8_t* vrows = smem + L::kRingOff + st * L::kStage + L::kTile;
+          const uint32_t item = 2 * it + 1;
+          uint8_t* vrows = smem + slot_off(item);
+          wait(full(item % NS), (item / NS) & 1);
           uint32_t odd = 0;
 #pragma unroll
           for (int c = 0; c < kPieces; ++c) {
             const uint4 w = *reinterpret_cast<const uint4*>(vrows + L::at(me, c, kTreeKeys));
-            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              odd |= E4 ? __vcmpeq4(v[e] & 0x7f7f7f7fu, 0x7f7f7f7fu)
-                        : __vcmpeq2(v[e] & 0x7f807f80u, 0x7f807f80u);
+            odd |= nonfinite_bits<FMT>(w.x) | nonfinite_bits<FMT>(w.y) | nonfinite_bits<FMT>(w.z) |
+                   nonfinite_bits<FMT>(w.w);
           }
-          if (barrier_or(3, 256, odd != 0)) {
-            const uint32_t bits = __ballot_sync(~0u, odd != 0);
-            if (wg == 0 && lane == 0) dirty[warp & 3] = bits;
-            named_barrier(3, 256);
-            if (it > 0) values_done(it - 1);
-            float add[RW];
+          constexpr uint32_t kAll = L::kTurns ? 128 : 256;  // threads of the tile
+          const uint32_t b_all = L::kTurns ? 1 + wg : 3;
+          mend = barrier_or(b_all, kAll, odd != 0);
+          if (mend) {
+            uint32_t* bits = dirty + (L::kTurns ? wg * 4 : 0);
+            const uint32_t some = __ballot_sync(~0u, odd != 0);
+            if (lane == 0) bits[warp & 3] = some;  // (both warpgroups write the same)
+            named_barrier(b_all, kAll);
+            // sc becomes what the rows of this thread miss in its column of O
 #pragma unroll
-            for (int j = 0; j < RW; ++j) add[j] = 0.f;
+            for (int j = 0; j < RT; ++j) sc[j] = 0.f;
+#pragma unroll 1
             for (int k4 = 0; k4 < 4; ++k4)
-              for (uint32_t left = dirty[k4]; left; left &= left - 1) {
+#pragma unroll 1
+              for (uint32_t left = bits[k4]; left; left &= left - 1) {
                 const int k = k4 * 32 + __ffs(left) - 1;
                 float v = 0.f;
                 if (me < D) {
@@ -885,32 +969,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
                   else v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(src));
                 }
                 if (!isinf(v) && !isnan(v)) continue;
-                const uint8_t* pk = smem + L::kPOff + pb * L::kPBytes + k * 16;
+                const uint8_t* pk = smem + L::kPOff + x * L::kPBytes + k * 16;
 #pragma unroll
-                for (int j = 0; j < RW; ++j) {
-                  const int byte = (wg * RW + j) * L::kCell;
+                for (int j = 0; j < RT; ++j) {
+                  const int byte = (row0 + j) * L::kCell;
                   const uint8_t* src = pk + (byte >> 4) * (kTreeKeys * 16) + (byte & 15);
-                  const bool seen = E4 ? *src != 0 : *reinterpret_cast<const uint16_t*>(src) != 0;
-                  if (seen) add[j] += v;
+                  if (E4 ? *src != 0 : *reinterpret_cast<const uint16_t*>(src) != 0) sc[j] += v;
                 }
               }
-            __syncwarp();
-            float o[RW];
-            tmem_ld_cols<RW>(t_o, o);
-#pragma unroll
-            for (int j = 0; j < RW; ++j) o[j] += add[j];
-            tmem_st_cols<RW>(t_o, o);
-            named_barrier(3, 256);
-            if (wg == 0 && odd != 0) {
+            named_barrier(b_all, kAll);
+            if ((L::kTurns || wg == 0) && odd != 0) {
 #pragma unroll 1
               for (int c = 0; c < kPieces; ++c) {
                 uint4* p = reinterpret_cast<uint4*>(vrows + L::at(me, c, kTreeKeys));
                 uint4 w = *p;
-                uint32_t* v = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  v[e] &= ~(E4 ? __vcmpeq4(v[e] & 0x7f7f7f7fu, 0x7f7f7f7fu)
-                               : __vcmpeq2(v[e] & 0x7f807f80u, 0x7f807f80u));
+                w.x &= ~nonfinite_bits<FMT>(w.x);
+                w.y &= ~nonfinite_bits<FMT>(w.y);
+                w.z &= ~nonfinite_bits<FMT>(w.z);
+                w.w &= ~nonfinite_bits<FMT>(w.w);
                 *p = w;
               }
             }
@@ -919,13 +995,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         fence_async_shared();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(pb));
+        if (lane == 0) mbar_arrive(p_full(x));
+        fresh = false;
+        if (mend) {
+          values_done(it);
+#pragma unroll
+          for (int j0 = 0; j0 < RT; j0 += 8) {
+            float o[8];
+            tmem_ld_cols<8>(t_o + j0, o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] += sc[j0 + j];
+            tmem_st_cols<8>(t_o + j0, o);
+          }
+          tc_fence_before();
+        }
       }
 
-      // ---- the piece's result: row sums over the warpgroup's keys, then O
+      // ---- the piece's result.  Row sums over the warpgroup's keys: lanes
+      // trade halves of their rows, upper lanes keeping the upper half
 #pragma unroll
-      for (int n = RW, o = 16; n > 1; n >>= 1, o >>= 1) {
-        const bool up = (lane & o) != 0;  // keeps the upper half of the rows
+      for (int n = RT, o = 16; n > 1; n >>= 1, o >>= 1) {
+        const bool up = (lane & o) != 0;
 #pragma unroll
         for (int j = 0; j < n / 2; ++j) {
           const float send = up ? l[j] : l[j + n / 2];
@@ -933,68 +1023,101 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
       }
 #pragma unroll
-      for (int o = 16 / RW; o > 0; o >>= 1) l[0] += __shfl_xor_sync(~0u, l[0], o);
-      // lane's bits from 16 down select the row, halves first
-      if ((lane & (32 / RW - 1)) == 0) wmax[(lane / (32 / RW)) * 4 + (warp & 3)] = l[0];
-      named_barrier(1 + wg, 128);
-      values_done(it - 1);
-      float o[RW];
-      {
-        float rest[RW];
-        tmem_ld_cols<RW>(t_o, o);
-        tmem_ld_cols<RW>(t_o + R, rest);
+      for (int o = 16 / RT; o > 0; o >>= 1) l[0] += __shfl_xor_sync(~0u, l[0], o);
+      if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = l[0];
 #pragma unroll
-        for (int j = 0; j < RW; ++j) o[j] = E4 ? fmaf(rest[j], 1.f / kWeightRest, o[j]) : o[j] + rest[j];
-      }
+      for (int j = 0; j < RT; ++j)
+        if (me == j) refs[wg * RT + j] = ref[j];
+      // the last P V of this warpgroup's O
+      const uint32_t last = it - 1;
+      if (!L::kTurns) values_done(last);
+      else if (!fresh) values_done((last & 1) == static_cast<uint32_t>(wg) ? last : last - 1);
+      constexpr uint32_t kAll = L::kTurns ? 256 : 128;  // threads whose results meet
+      const uint32_t b_all = L::kTurns ? 3 : 1 + wg;
+      tc_fence_before();
+      named_barrier(b_all, kAll);
+      tc_fence_after();
+
       const bool whole = walk.t0 == 0 && walk.nt == s.tiles;
       const int slot = walk.t0 == 0 ? 1 : 0;  // 0: began in an earlier CTA
-      const int n_rows = s.n * a.G - walk.block * R - wg * RW;  // of this warpgroup, may exceed RW
-      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + wg * RW;
+      const int out0 = wg * RO;               // first row that this thread writes
+      const int n_rows = s.n * a.G - walk.block * R - out0;  // from there on, may exceed RO
+      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + out0;
+      const bool second = L::kTurns && walk.nt > 1;  // both warpgroups had tiles
+      const int w0 = L::kTurns ? static_cast<int>((it - walk.nt) & 1) : wg;  // that of the first tile
 #pragma unroll
-      for (int j = 0; j < RW; ++j) {
-        const float4 l4 = *reinterpret_cast<const float4*>(wmax + j * 4);
-        const float sum = (l4.x + l4.y) + (l4.z + l4.w);
-        if (whole) o[j] *= sum > 0.f || isnan(sum) ? 1.f / sum : 0.f;
-        if (me == j && j < n_rows) {
-          if (whole) {
-            const int node = (walk.block * R + wg * RW + j) / a.G;
-            a.lse[static_cast<int64_t>(rows[j].head) * a.T + s.row0 + node] = (ref[j] + log2f(sum)) * kLn2;
-          } else {
-            a.part_ml[part + j] = make_float2(ref[j], sum);
+      for (int j0 = 0; j0 < RO; j0 += 8) {
+        if (j0 >= n_rows) break;
+        float o[8], sum[8], rr[8];
+        // one accumulator's 8 columns, its parts joined
+        auto columns = [&](uint32_t t, float (&y)[8]) {
+          tmem_ld_cols<8>(t, y);
+          if constexpr (E4) {
+            float rest[8];
+            tmem_ld_cols<8>(t + R, rest);
+            fma_rows<8>(rest, 1.f / kWeightRest, y);
+          }
+        };
+        auto sum_of = [&](int w, int row) {
+          const float4 l4 = *reinterpret_cast<const float4*>(wmax + (w * RT + row) * 4);
+          return (l4.x + l4.y) + (l4.z + l4.w);
+        };
+        const uint32_t t = tmem + lanes + L::kOCol + out0 + j0;
+        const int row = L::kTurns ? out0 + j0 : j0;   // in the warpgroups' arrays
+        columns(t + (L::kTurns ? w0 * L::kN : 0), o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          rr[j] = refs[w0 * RT + row + j];
+          sum[j] = sum_of(w0, row + j);
+        }
+        if (second) {
+          float o2[8];
+          columns(t + (1 - w0) * L::kN, o2);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float r2 = refs[(1 - w0) * RT + row + j];
+            const float top = fmaxf(rr[j], r2);
+            const float f1 = fast_exp2(rr[j] - top), f2 = fast_exp2(r2 - top);
+            o[j] = o[j] * f1 + o2[j] * f2;
+            sum[j] = sum[j] * f1 + sum_of(1 - w0, row + j) * f2;
+            rr[j] = top;
           }
         }
-      }
-      if (me < D) {
 #pragma unroll
-        for (int j = 0; j < RW; j += 2) {
-          if (j >= n_rows) break;
-          if (whole) {
-            // lane pairs trade: the even lane stores two columns of row j, the
-            // odd lane of row j + 1
-            const bool up = lane & 1;
-            const float got = __shfl_xor_sync(~0u, up ? o[j] : o[j + 1], 1);
-            const int r = j + (up ? 1 : 0);
-            if (r < n_rows) {
-              const int node = (walk.block * R + wg * RW + r) / a.G;
-              __nv_bfloat16* dst = a.o + static_cast<int64_t>(s.row0 + node) * a.o_t +
-                                   static_cast<int64_t>(up ? rows[j + 1].head : rows[j].head) * a.o_h + (me & ~1);
-              *reinterpret_cast<uint32_t*>(dst) = up ? pack_bf16x2(got, o[j + 1]) : pack_bf16x2(o[j], got);
+        for (int j = 0; j < 8; ++j) {
+          if (whole) o[j] *= sum[j] > 0.f || isnan(sum[j]) ? 1.f / sum[j] : 0.f;
+          if (me == j0 + j && j0 + j < n_rows) {
+            if (whole) a.lse[info->lse[out0 + j0 + j]] = (rr[j] + log2f(sum[j])) * kLn2;
+            else a.part_ml[part + j0 + j] = make_float2(rr[j], sum[j]);
+          }
+        }
+        if (me < D) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            if (whole) {
+              // lane pairs trade: the even lane stores two columns of row j,
+              // the odd lane of row j + 1
+              const bool up = lane & 1;
+              const float got = __shfl_xor_sync(~0u, up ? o[j] : o[j + 1], 1);
+              if (j0 + j + (up ? 1 : 0) < n_rows)
+                *reinterpret_cast<uint32_t*>(a.o + info->out[out0 + j0 + j + (up ? 1 : 0)] + (me & ~1)) =
+                    up ? pack_bf16x2(got, o[j + 1]) : pack_bf16x2(o[j], got);
+            } else {
+              if (j0 + j < n_rows) a.part_o[(part + j0 + j) * D + me] = o[j];
+              if (j0 + j + 1 < n_rows) a.part_o[(part + j0 + j + 1) * D + me] = o[j + 1];
             }
-          } else {
-            a.part_o[(part + j) * D + me] = o[j];
-            if (j + 1 < n_rows) a.part_o[(part + j + 1) * D + me] = o[j + 1];
           }
         }
       }
       tc_fence_before();
-      named_barrier(1 + wg, 128);  // wmax is read
+      named_barrier(b_all, kAll);  // O, the sums and the references are read
       if (lane == 0) mbar_arrive(q_free(u & 1));
       ++u;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kTreeIssuer) {
+  if (warp == kTreeIssueS) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }

@@ -5,10 +5,11 @@ Tolerances (half a step of bf16 is 2^-8 of the value, of fp16 2^-11):
          magnitudes covers them), then one rounding to bf16.
   cache  exact: codes, scales and values are compared bit for bit.
   tree   O: one rounding to bf16 (2^-8 |O|).  Each weight enters the product
-         with V as two parts, bf16 (2^-8 each, 2^-16 together) over a bf16
-         cache and e4m3 (2^-4 each, 2^-8 together) over e4m3, so at most that
-         times sum(w |v|); e4m3 parts also drop below 2^-23 of the largest
-         weight, at most that for each of the n keys' |v|.  A score's error e_s
+         with V rounded to bf16 (2^-8) over a bf16 cache, as two e4m3 parts
+         (2^-4 each, 2^-8 together) over e4m3, so at most 2^-8 sum(w |v|);
+         e4m3 parts also drop what is below 2^-21 of the largest weight (half
+         a step of 2^-9, over 16 for the second part and 2^7 for the largest
+         weight), at most that for each of the n keys' |v|.  A score's error e_s
          of float32 accumulation, at most (d + 8) steps of 2^-23 of sum |q k|
          scale, moves a weight by 2 e_s (numerator and denominator); over e4m3
          a query element is off by at most 2^-21 of its row's largest, which
@@ -232,10 +233,10 @@ def tree_tolerance(q, k, v, ro, spread, size, kv, scale=None):
     d = q.shape[-1]
     e_s = (d + 8) * 2.0 ** -23 * size
     if kv == "bf16":
-        return 2.0 ** -8 * np.abs(ro) + (2.0 ** -16 + 2 * e_s[..., None] + 2.0 ** -18) * spread, e_s
+        return 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * e_s[..., None] + 2.0 ** -18) * spread, e_s
     scale = d ** -0.5 if scale is None else abs(scale)
     e_s = e_s + 2.0 ** -21 * np.abs(q).max(-1) * np.abs(k).sum(-1).max() * scale
-    lost = 2.0 ** -23 * len(v) * np.abs(v).max()
+    lost = 2.0 ** -21 * len(v) * np.abs(v).max()
     return 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * e_s[..., None] + 2.0 ** -18) * spread + lost, e_s
 
 
