@@ -88,7 +88,7 @@ bool make_cache_map(CUtensorMap* m, const void* base, const sdpa_kv_cache* c, in
 
 // -------------------------------------------------------------------- tree
 struct TreePlan {
-  size_t prefix, ml, o, total;
+  size_t ml, o, total;
 };
 
 sdpa_status_t check_tree(const sdpa_tree* t, const sdpa_kv_cache* c, CacheView& v, TreePlan& pl) {
@@ -112,9 +112,8 @@ sdpa_status_t check_tree(const sdpa_tree* t, const sdpa_kv_cache* c, CacheView& 
   if (!good_stride(t->q_t, 8) || !good_stride(t->q_h, 8) || !good_stride(t->o_t, 8) ||
       !good_stride(t->o_h, 8))
     return SDPA_ERR_INVALID_ARG;
-  pl.prefix = 0;
-  pl.ml = round256(static_cast<size_t>(t->B + 1) * sizeof(int64_t));
-  pl.o = pl.ml + round256(static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeMaxRows * sizeof(float2));
+  pl.ml = 0;
+  pl.o = round256(static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeMaxRows * sizeof(float2));
   pl.total = pl.o + static_cast<size_t>(kTreeMaxCtas) * 2 * kTreeMaxRows * c->d * sizeof(float);
   return SDPA_OK;
 }
@@ -366,6 +365,7 @@ sdpa_status_t sdpa_tree_fwd(const sdpa_tree* t, const sdpa_kv_cache* cache, cons
           !fill_t5(a.t5, nb, bias->max_distance, bias->bidirectional))
         return SDPA_ERR_INVALID_ARG;
       a.t5_table = bias->ptr;
+      a.t5_buckets = nb;
     } else {
       return bias->kind == SDPA_BIAS_DENSE || bias->kind == SDPA_BIAS_REL ? SDPA_ERR_UNSUPPORTED
                                                                          : SDPA_ERR_INVALID_ARG;
@@ -402,7 +402,6 @@ sdpa_status_t sdpa_tree_fwd(const sdpa_tree* t, const sdpa_kv_cache* cache, cons
   a.ss_page = v.ss_page;
   a.ss_head = v.ss_head;
   a.scale_log2 = scale * kLog2e;
-  a.prefix = reinterpret_cast<int64_t*>(ws + pl.prefix);
   a.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
   a.part_o = reinterpret_cast<float*>(ws + pl.o);
   a.wait_limit_ns = g_wait_limit_ns;

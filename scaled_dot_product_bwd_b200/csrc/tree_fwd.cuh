@@ -60,6 +60,9 @@ constexpr int kTreeKeys = 128;      // keys per tile
 constexpr int kTreeProducer = 8, kTreeIssueS = 9, kTreeIssueO = 10, kTreeQuery = 11;
 constexpr int kTreeThreads = 12 * 32;
 constexpr int kTreeScaleRing = 8;   // tiles whose e4m3 scales are kept
+// T5: buckets of the distances -kTreeNear .. 63 are tabulated per CTA, and the
+// table's entries of a KV head's query heads per piece where they fit.
+constexpr int kTreeNear = 960, kTreeBuckets = kTreeNear + 64, kTreeT5Slice = 1024;
 
 struct TreeArgs {
   const __nv_bfloat16* q;
@@ -83,8 +86,8 @@ struct TreeArgs {
   const float* alibi_slopes;
   const float* t5_table;
   T5Spec t5;
+  int t5_buckets;
   // workspace
-  int64_t* prefix;              // [B + 1] tiles before each sequence
   float2* part_ml;              // [ctas][2][rows] (r, l)
   float* part_o;                // [ctas][2][rows][D]
   uint64_t wait_limit_ns;
@@ -129,7 +132,10 @@ struct TreeLayout {
   static constexpr int kRowsBytes = (static_cast<int>(sizeof(TreeRows)) + 15) / 16 * 16;
   static constexpr int kMaxOff = kRowsOff + 2 * kRowsBytes;      // [2][kRT][4] floats
   static constexpr int kRefOff = kMaxOff + 2 * kRT * 16;         // [2][kRT] floats
-  static constexpr int kMiscOff = kRefOff + 2 * kRT * 4;
+  static constexpr int kFacOff = kRefOff + 2 * kRT * 4;          // [2][kRT] floats
+  static constexpr int kBucketOff = kFacOff + 2 * kRT * 4;       // [kTreeBuckets] bytes
+  static constexpr int kT5Off = kBucketOff + kTreeBuckets;       // [2][kTreeT5Slice] floats
+  static constexpr int kMiscOff = kT5Off + 2 * kTreeT5Slice * 4;
   static constexpr int kMaxSlots = 12;                      // scales outlive their tile's slots
   static constexpr int kNumBars = 2 * kMaxSlots + 14;
   static constexpr int kMiscBytes = kNumBars * 8 + 128;
@@ -375,7 +381,8 @@ __device__ __forceinline__ float t5_bias_log2(const TreeArgs& a, int rel, int h)
 // parts in rows 0 .. R - 1, second parts from row R on) and their TreeRows.
 template <int D, int FMT, int R>
 __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeWalk<R>& w, int lane,
-                                                  uint8_t* dst, TreeRows* info, bool bias) {
+                                                  uint8_t* dst, TreeRows* info, float* t5_slice,
+                                                  bool bias) {
   using L = TreeLayout<D, FMT, R>;
   const TreeSeq& s = w.s;
   const int n_rows = s.n * a.G - w.block * R;  // of this block, may exceed R
@@ -467,6 +474,13 @@ __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeW
       if (c == 0) info->scale[r] = a.scale_log2 / f1 / f2;
     }
   }
+  if (bias && a.t5_table && a.t5_buckets * a.G <= kTreeT5Slice) {
+#pragma unroll 4
+    for (int i = lane; i < a.t5_buckets * a.G; i += 32) {
+      const int k = i / a.G;
+      t5_slice[i] = bias_to_log2(a.t5_table[k * a.Hq + w.hkv * a.G + (i - k * a.G)]);
+    }
+  }
   for (int n = lane; n < s.n; n += 32) {
     uint64_t m = 0;
 #pragma unroll 8
@@ -555,10 +569,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
     const int64_t per = tree_share(total, gridDim.x);
     const int64_t from = per * blockIdx.x;
-    if (lane == 0) {
-      *start_left = max(min(total - from, per), static_cast<int64_t>(0));
-      if (blockIdx.x == 0) a.prefix[a.B] = total;
-    }
+    if (lane == 0) *start_left = max(min(total - from, per), static_cast<int64_t>(0));
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
@@ -576,15 +587,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         if (lane >= o) upto += y;
       }
       const int64_t before = base + upto - units;
-      if (blockIdx.x == 0 && b < a.B) a.prefix[b] = before;
       if (b < a.B && before <= from && from < before + units) {
         *start_b = b;
         *start_off = static_cast<int>(from - before);
         *start_seq = s;
       }
       base += __shfl_sync(~0u, upto, 31);
-      if (blockIdx.x != 0 && base > from) break;  // (CTA 0 writes all of `prefix`)
+      if (base > from) break;
     }
+  } else if (BIAS != 0 && warp < 8 && a.t5_table) {
+    for (int i = tid; i < kTreeBuckets; i += 256)
+      smem[L::kBucketOff + i] = static_cast<uint8_t>(t5_bucket(i - kTreeNear, a.t5));
   }
   tc_fence_before();
   __syncthreads();
@@ -671,7 +684,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       if (!ok) break;
       tree_load_queries<D, FMT, R>(a, walk, lane, smem + L::kQOff + x * L::kQBytes,
                                    reinterpret_cast<TreeRows*>(smem + L::kRowsOff + x * L::kRowsBytes),
-                                   BIAS != 0);
+                                   reinterpret_cast<float*>(smem + L::kT5Off) + x * kTreeT5Slice, BIAS != 0);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(x));
@@ -743,6 +756,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     float* wmax = reinterpret_cast<float*>(smem + L::kMaxOff);    // [2][RT][4 warps]
     float* mine = wmax + wg * RT * 4;
     float* refs = reinterpret_cast<float*>(smem + L::kRefOff);    // [2][RT]
+    float* facs = reinterpret_cast<float*>(smem + L::kFacOff);    // [2][RT]: what the last rescaling took
     // After a wait that ran out the warps go on without waiting, through the
     // same barriers, so that no thread is left at one.
     bool ok = true;
@@ -825,15 +839,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
 #pragma unroll
             for (int j = 0; j < RT; ++j) sc[j] += info->bias[row0 + j];
           } else {
-            // the buckets first, then the loads, eight at a time in flight
+            const uint8_t* buckets = smem + L::kBucketOff;
+            const float* slice = reinterpret_cast<const float*>(smem + L::kT5Off) + (u & 1) * kTreeT5Slice;
+            const bool in_slice = a.t5_buckets * a.G <= kTreeT5Slice;
+            const bool deep = a.t5.one_lo_max < -kTreeNear;  // buckets beyond the tabulated distances
+            const int head0 = walk.hkv * a.G;
 #pragma unroll
-            for (int j0 = 0; j0 < RT; j0 += 8) {
-              int at[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                at[j] = t5_bucket(key_pos - info->pos[row0 + j0 + j], a.t5) * a.Hq + info->head[row0 + j0 + j];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) sc[j0 + j] += bias_to_log2(a.t5_table[at[j]]);
+            for (int j = 0; j < RT; ++j) {
+              const int rel = key_pos - info->pos[row0 + j], head = info->head[row0 + j];
+              int k = buckets[max(rel, -kTreeNear) + kTreeNear];
+              if (deep && rel < -kTreeNear) k = t5_bucket(rel, a.t5);
+              sc[j] += in_slice ? slice[k * a.G + head - head0] : bias_to_log2(a.t5_table[k * a.Hq + head]);
             }
           }
         }
@@ -868,31 +884,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           }
           if (lane < RT) mine[lane * 4 + (warp & 3)] = keep;
           named_barrier(1 + wg, 128);
+          if ((warp & 3) == 0 && lane < RT) {
+            const float4 w4 = *reinterpret_cast<const float4*>(mine + lane * 4);
+            const float old = fresh ? -FLT_MAX : refs[wg * RT + lane];
+            const float m = fmaxf(fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) - (E4 ? kTopE4m3 : kTopBf16), old);
+            refs[wg * RT + lane] = m;
+            facs[wg * RT + lane] = fast_exp2(old - m);
+          }
           if (!L::kTurns && !fresh) values_done(it - 1);
+          named_barrier(1 + wg, 128);
 #pragma unroll
-          for (int j0 = 0; j0 < RT; j0 += 8) {
-            float f[8];
+          for (int j = 0; j < RT; j += 4) {
+            const float4 r4 = *reinterpret_cast<const float4*>(refs + wg * RT + j);
+            const float4 f4 = *reinterpret_cast<const float4*>(facs + wg * RT + j);
+            ref[j] = r4.x;
+            ref[j + 1] = r4.y;
+            ref[j + 2] = r4.z;
+            ref[j + 3] = r4.w;
+            f2_unpack(f2_mul(f2_pack(l[j], l[j + 1]), f2_pack(f4.x, f4.y)), l[j], l[j + 1]);
+            f2_unpack(f2_mul(f2_pack(l[j + 2], l[j + 3]), f2_pack(f4.z, f4.w)), l[j + 2], l[j + 3]);
+          }
+          if (!fresh) {
+#pragma unroll 1
+            for (int j0 = 0; j0 < RT * L::kParts; j0 += 8) {
+              const uint32_t t = t_o + (j0 < RT ? j0 : R + j0 - RT);
+              const float* f = facs + wg * RT + (j0 < RT ? j0 : j0 - RT);
+              float o[8];
+              tmem_ld_cols<8>(t, o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 w4 = *reinterpret_cast<const float4*>(mine + (j0 + j) * 4);
-              float m = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w));
-              m = fmaxf(m - (E4 ? kTopE4m3 : kTopBf16), ref[j0 + j]);
-              f[j] = fast_exp2(ref[j0 + j] - m);
-              ref[j0 + j] = m;
-              l[j0 + j] *= f[j];
-            }
-            if (!fresh) {
-#pragma unroll
-              for (int part = 0; part < L::kParts; ++part) {
-                float o[8];
-                tmem_ld_cols<8>(t_o + part * R + j0, o);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] *= f[j];
-                tmem_st_cols<8>(t_o + part * R + j0, o);
-              }
+              for (int j = 0; j < 8; ++j) o[j] *= f[j];
+              tmem_st_cols<8>(t, o);
             }
           }
-          named_barrier(1 + wg, 128);  // `mine` is read
         }
 
         uint8_t* pbuf = smem + L::kPOff + x * L::kPBytes + me * 16;
@@ -939,7 +962,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           uint8_t* vrows = smem + slot_off(item);
           wait(full(item % NS), (item / NS) & 1);
           uint32_t odd = 0;
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < kPieces; ++c) {
             const uint4 w = *reinterpret_cast<const uint4*>(vrows + L::at(me, c, kTreeKeys));
             odd |= nonfinite_bits<FMT>(w.x) | nonfinite_bits<FMT>(w.y) | nonfinite_bits<FMT>(w.z) |
@@ -1025,9 +1048,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
 #pragma unroll
       for (int o = 16 / RT; o > 0; o >>= 1) l[0] += __shfl_xor_sync(~0u, l[0], o);
       if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = l[0];
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-        if (me == j) refs[wg * RT + j] = ref[j];
       // the last P V of this warpgroup's O
       const uint32_t last = it - 1;
       if (!L::kTurns) values_done(last);
@@ -1045,9 +1065,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + out0;
       const bool second = L::kTurns && walk.nt > 1;  // both warpgroups had tiles
       const int w0 = L::kTurns ? static_cast<int>((it - walk.nt) & 1) : wg;  // that of the first tile
-#pragma unroll
-      for (int j0 = 0; j0 < RO; j0 += 8) {
-        if (j0 >= n_rows) break;
+      // (rolled: straight-line code that runs once per piece would wait for
+      // its instructions longer than it runs)
+#pragma unroll 1
+      for (int j0 = 0; j0 < min(RO, n_rows); j0 += 8) {
         float o[8], sum[8], rr[8];
         // one accumulator's 8 columns, its parts joined
         auto columns = [&](uint32_t t, float (&y)[8]) {
@@ -1135,17 +1156,32 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 31;
   const int x = blockIdx.x * kTreeJoinWarps + (threadIdx.x >> 5);  // node * Hq + head
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // all that the lengths decide, while the pieces are still being computed
   const TreeSeq s = tree_seq<R>(a, b);
+  int64_t before = 0, total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int64_t units = b0 + lane < a.B ? tree_seq<R>(a, b0 + lane).units(a.Hkv) : 0;
+    total += units;
+    before += b0 + lane < b ? units : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(~0u, total, o);
+    before += __shfl_xor_sync(~0u, before, o);
+  }
   const int n = x / a.Hq, h = x - n * a.Hq;
-  if (n >= s.n) return;
   const int hkv = h / a.G;
   const int r = n * a.G + (h - hkv * a.G);
   const int block = r / R, in = r - block * R;
-  const int64_t per = tree_share(a.prefix[a.B], ctas);
-  const int64_t first = a.prefix[b] + (static_cast<int64_t>(hkv) * s.rb + block) * s.tiles;
-  const int c0 = static_cast<int>(first / per);
-  const int c1 = static_cast<int>((first + s.tiles - 1) / per);
+  int c0 = 0, c1 = 0;
+  if (n < s.n) {
+    const int64_t per = tree_share(total, ctas);
+    const int64_t first = before + (static_cast<int64_t>(hkv) * s.rb + block) * s.tiles;
+    c0 = static_cast<int>(first / per);
+    c1 = static_cast<int>((first + s.tiles - 1) / per);
+  }
+  // (every thread waits, so that what follows this kernel follows the first too)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;
   float ref = -FLT_MAX, l = 0.f, acc[W];
 #pragma unroll
@@ -1166,7 +1202,7 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
 #pragma unroll
     for (int i = 0; i < W; ++i) acc[i] *= f_old;
     const int count = min(32, c1 - base + 1);
-#pragma unroll 8
+#pragma unroll 16
     for (int j = 0; j < count; ++j) {
       const int cj = base + j;
       const float w = __shfl_sync(~0u, f, j);
