@@ -59,6 +59,10 @@ constexpr int kTreeKeys = 128;      // keys per tile
 // warps after the 8 of the softmax
 constexpr int kTreeProducer = 8, kTreeIssueS = 9, kTreeIssueO = 10, kTreeQuery = 11;
 constexpr int kTreeThreads = 12 * 32;
+// A (sequence, head, row block) costs its first CTA about this many tiles more
+// (its queries, first maximum, ragged end and result); the line counts them,
+// so that CTAs with many short ones get fewer tiles.
+constexpr int kTreePieceCost = 3;
 constexpr int kTreeScaleRing = 8;   // tiles whose e4m3 scales are kept
 // T5: buckets of the distances -kTreeNear .. 63 are tabulated per CTA, and the
 // table's entries of a KV head's query heads per piece where they fit.
@@ -97,8 +101,7 @@ struct TreeArgs {
 struct TreeRows {
   float scale[kTreeMaxRows];    // log2(e) * scale, and what undoes the operand's scaling (e4m3)
   float bias[kTreeMaxRows];     // ALiBi: its slope; T5: the bias of every distance <= one_lo_max
-  uint64_t sees[kTreeMaxRows];  // nodes a row sees
-  uint64_t seen[kTreeMaxNodes]; // rows that see a node
+  uint32_t seen[kTreeMaxNodes][2];  // rows that see a node, 32 a word
   int64_t out[kTreeMaxRows];    // its element offset in o
   int64_t lse[kTreeMaxRows];    // its index in lse
   int pos[kTreeMaxRows];        // its position
@@ -162,7 +165,9 @@ struct TreeLayout {
 struct TreeSeq {
   int row0, n, ctx, keys;  // first query row, nodes, context length, context + nodes
   int tile0, tiles, rb;    // first key tile any node sees, tiles, row blocks
-  __device__ __forceinline__ int units(int Hkv) const { return Hkv * rb * tiles; }
+  // of the line: per (head, row block) the piece cost, then the tiles
+  __device__ __forceinline__ int span() const { return kTreePieceCost + tiles; }
+  __device__ __forceinline__ int units(int Hkv) const { return Hkv * rb * span(); }
 };
 
 template <int R>
@@ -189,29 +194,34 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
 // block) by (sequence, head, row block).
 template <int R>
 struct TreeWalk {
-  int64_t left;       // tiles of the piece not walked yet
-  int b, off, units;  // current sequence, its tiles walked or before the piece, all its tiles
+  int64_t left;       // of the CTA's part of the line, not walked yet
+  int b, off, units;  // current sequence, how much of its part is walked, its length
   TreeSeq s;
   int hkv, block, t0, nt;  // this step: head, row block, first tile, tiles
   __device__ __forceinline__ bool next(const TreeArgs& a) {
-    if (left <= 0) return false;
-    while (off >= units) {
-      off -= units;
-      s = tree_seq<R>(a, ++b);
-      units = s.units(a.Hkv);
+    while (left > 0) {
+      while (off >= units) {
+        off -= units;
+        s = tree_seq<R>(a, ++b);
+        units = s.units(a.Hkv);
+      }
+      const int span = s.span();
+      const int seg = off / span;
+      const int in = off - seg * span;
+      const int n = static_cast<int>(min(static_cast<int64_t>(span - in), left));
+      left -= n;
+      off += n;
+      t0 = max(in - kTreePieceCost, 0);
+      nt = in + n - kTreePieceCost - t0;
+      hkv = seg / s.rb;
+      block = seg - hkv * s.rb;
+      if (nt > 0) return true;
     }
-    const int seg = off / s.tiles;
-    t0 = off - seg * s.tiles;
-    hkv = seg / s.rb;
-    block = seg - hkv * s.rb;
-    nt = static_cast<int>(min(static_cast<int64_t>(s.tiles - t0), left));
-    left -= nt;
-    off += nt;
-    return true;
+    return false;
   }
 };
 
-// Tiles per CTA of a line of `total`.
+// A CTA's part of a line of `total`.
 __device__ __forceinline__ int64_t tree_share(int64_t total, int ctas) {
   return (total + ctas - 1) / ctas;
 }
@@ -301,6 +311,30 @@ __device__ __forceinline__ void fma_rows(const float (&x)[N], float f, float* y)
     f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), f2, f2_pack(y[j], y[j + 1])), y[j], y[j + 1]);
 }
 
+// Row j's x[j] of all 32 lanes combined, for row lane / (32 / N): lanes trade
+// halves of their rows, the upper ones keeping the upper half, until one row
+// is left to each.
+template <int N, typename Op>
+__device__ __forceinline__ float by_halves(const float (&x)[N], int lane, Op op) {
+  float y[N / 2];
+  {
+    const bool up = (lane & 16) != 0;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j)
+      y[j] = op(up ? x[j + N / 2] : x[j], __shfl_xor_sync(~0u, up ? x[j] : x[j + N / 2], 16));
+  }
+#pragma unroll
+  for (int n = N / 2, o = 8; n > 1; n >>= 1, o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int j = 0; j < n / 2; ++j)
+      y[j] = op(up ? y[j + n / 2] : y[j], __shfl_xor_sync(~0u, up ? y[j] : y[j + n / 2], o));
+  }
+#pragma unroll
+  for (int o = 16 / N; o > 0; o >>= 1) y[0] = op(y[0], __shfl_xor_sync(~0u, y[0], o));
+  return y[0];
+}
+
 // Whether `x` holds for any thread of the named barrier's `count`.
 __device__ __forceinline__ bool barrier_or(uint32_t id, uint32_t count, bool x) {
   uint32_t r;
@@ -376,69 +410,38 @@ __device__ __forceinline__ float t5_bias_log2(const TreeArgs& a, int rel, int h)
   return bias_to_log2(a.t5_table[t5_bucket(rel, a.t5) * a.Hq + h]);
 }
 
-// ------------------------------------------------------------- query warp
+// ---------------------------------------------------------------- queries
 // One piece's query rows as the K-major operand `dst` (kN rows; e4m3: first
-// parts in rows 0 .. R - 1, second parts from row R on) and their TreeRows.
+// parts in rows 0 .. R - 1, second parts from row R on) and their TreeRows, by
+// warp w of nw.
 template <int D, int FMT, int R>
-__device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeWalk<R>& w, int lane,
-                                                  uint8_t* dst, TreeRows* info, float* t5_slice,
-                                                  bool bias) {
+__device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeWalk<R>& wk, int w, int nw,
+                                                  int lane, uint8_t* dst, TreeRows* info,
+                                                  float* t5_slice, bool bias) {
   using L = TreeLayout<D, FMT, R>;
-  const TreeSeq& s = w.s;
-  const int n_rows = s.n * a.G - w.block * R;  // of this block, may exceed R
-  const uint64_t node_bits = s.n >= 64 ? ~0ull : (1ull << s.n) - 1ull;
-  auto sees_of = [&](int n) -> uint64_t {
-    const uint64_t m = a.mask ? static_cast<uint64_t>(a.mask[s.row0 + n]) : ~0ull >> (63 - n);
-    return m & node_bits;
-  };
-  for (int n = lane; n < s.n; n += 32) info->depth[n] = __popcll(sees_of(n) & ~(1ull << n));
-  for (int r = lane; r < R; r += 32) {
-    uint64_t sees = 0;
-    float slope = 0.f;
-    int pos = s.ctx, head = w.hkv * a.G;
-    int64_t out = 0, lse = 0;
-    if (r < n_rows) {
-      const int x = w.block * R + r;
-      const int n = x / a.G;
-      sees = sees_of(n);
-      pos += __popcll(sees & ~(1ull << n));
-      head += x - n * a.G;
-      out = static_cast<int64_t>(s.row0 + n) * a.o_t + static_cast<int64_t>(head) * a.o_h;
-      lse = static_cast<int64_t>(head) * a.T + s.row0 + n;
-      if (bias) {
-        if (a.alibi_slopes) slope = a.alibi_slopes[head];
-        else if (a.t5.one_lo_max != INT_MIN) slope = t5_bias_log2(a, a.t5.one_lo_max, head);
-      }
-    }
-    info->scale[r] = a.scale_log2;
-    info->bias[r] = slope;
-    info->sees[r] = sees;
-    info->pos[r] = pos;
-    info->head[r] = head;
-    info->out[r] = out;
-    info->lse[r] = lse;
-  }
-  __syncwarp();
+  const TreeSeq& s = wk.s;
+  const int n_rows = s.n * a.G - wk.block * R;  // of this block, may exceed R
   constexpr int kLanes = D / 8;        // lanes of a row, 8 elements each
   constexpr int kPass = 32 / kLanes;   // rows per pass
-  constexpr int kFlight = R / kPass < 8 ? R / kPass : 8;
+  constexpr int kFlight = 4;
   const int c = lane % kLanes, sub = lane / kLanes;
-  for (int r0 = 0; r0 < R; r0 += kPass * kFlight) {
+  for (int p0 = w; p0 * kPass < R; p0 += nw * kFlight) {
     uint4 x[kFlight];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int r = r0 + f * kPass + sub;
+      const int r = (p0 + f * nw) * kPass + sub;
       x[f] = make_uint4(0, 0, 0, 0);
-      if (r < n_rows) {
-        const int at = w.block * R + r;
+      if (r < min(R, n_rows)) {
+        const int at = wk.block * R + r;
         const int n = at / a.G;
         x[f] = *reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(s.row0 + n) * a.q_t +
-                                               (w.hkv * a.G + at - n * a.G) * a.q_h + c * 8);
+                                               (wk.hkv * a.G + at - n * a.G) * a.q_h + c * 8);
       }
     }
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int r = r0 + f * kPass + sub;
+      const int r = (p0 + f * nw) * kPass + sub;
+      if ((p0 + f * nw) * kPass >= R) break;
       if (FMT == kCacheBf16) {
         *reinterpret_cast<uint4*>(dst + L::at(r, c, R)) = x[f];
         continue;
@@ -471,21 +474,58 @@ __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeW
           make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
       *reinterpret_cast<uint2*>(dst + L::at(R + r, c >> 1, 2 * R) + (c & 1) * 8) =
           make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      if (c == 0) info->scale[r] = a.scale_log2 / f1 / f2;
+      // the other way round: 2^(e - 134)
+      if (c == 0)
+        info->scale[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e1) << 23) *
+                         __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
     }
   }
+  const uint64_t node_bits = s.n >= 64 ? ~0ull : (1ull << s.n) - 1ull;
+  auto sees_of = [&](int n) -> uint64_t {
+    const uint64_t m = a.mask ? static_cast<uint64_t>(a.mask[s.row0 + n]) : ~0ull >> (63 - n);
+    return m & node_bits;
+  };
+  for (int r0 = w * 32; r0 < R; r0 += nw * 32) {
+    const int r = r0 + lane;
+    uint64_t sees = 0;
+    if (r < R) {
+      float slope = 0.f;
+      int pos = s.ctx, head = wk.hkv * a.G;
+      int64_t out = 0, lse = 0;
+      if (r < n_rows) {
+        const int x = wk.block * R + r;
+        const int n = x / a.G;
+        sees = sees_of(n);
+        pos += __popcll(sees & ~(1ull << n));
+        head += x - n * a.G;
+        out = static_cast<int64_t>(s.row0 + n) * a.o_t + static_cast<int64_t>(head) * a.o_h;
+        lse = static_cast<int64_t>(head) * a.T + s.row0 + n;
+        if (bias) {
+          if (a.alibi_slopes) slope = a.alibi_slopes[head];
+          else if (a.t5.one_lo_max != INT_MIN) slope = t5_bias_log2(a, a.t5.one_lo_max, head);
+        }
+      } else {
+        sees = node_bits;  // rows of padding count as seeing every node
+      }
+      info->bias[r] = slope;
+      info->pos[r] = pos;
+      info->head[r] = head;
+      info->out[r] = out;
+      info->lse[r] = lse;
+    }
+    for (int n = 0; n < s.n; ++n) {
+      const uint32_t rows = __ballot_sync(~0u, (sees >> n) & 1ull);
+      if (lane == (n & 31)) info->seen[n][r0 / 32] = rows;
+    }
+  }
+  if (w == nw - 1)
+    for (int n = lane; n < s.n; n += 32) info->depth[n] = __popcll(sees_of(n) & ~(1ull << n));
   if (bias && a.t5_table && a.t5_buckets * a.G <= kTreeT5Slice) {
 #pragma unroll 4
-    for (int i = lane; i < a.t5_buckets * a.G; i += 32) {
+    for (int i = w * 32 + lane; i < a.t5_buckets * a.G; i += nw * 32) {
       const int k = i / a.G;
-      t5_slice[i] = bias_to_log2(a.t5_table[k * a.Hq + w.hkv * a.G + (i - k * a.G)]);
+      t5_slice[i] = bias_to_log2(a.t5_table[k * a.Hq + wk.hkv * a.G + (i - k * a.G)]);
     }
-  }
-  for (int n = lane; n < s.n; n += 32) {
-    uint64_t m = 0;
-#pragma unroll 8
-    for (int r = 0; r < R; ++r) m |= ((info->sees[r] >> n) & 1ull) << r;
-    info->seen[n] = m;
   }
 }
 
@@ -676,13 +716,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     }
   } else if (warp == kTreeQuery) {
     // ------------------------------------------------------------- queries
-    uint32_t u = 0;
-    bool ok = true;
+    // (the first piece's are laid out by the softmax warps, which have
+    // nothing else to do yet)
+    uint32_t u = 1;
+    bool ok = walk.next(a);
     while (ok && walk.next(a)) {
       const int x = u & 1;
       if (u >= 2) ok = __all_sync(~0u, mbar_wait(q_free(x), ((u >> 1) - 1) & 1, ctl));
       if (!ok) break;
-      tree_load_queries<D, FMT, R>(a, walk, lane, smem + L::kQOff + x * L::kQBytes,
+      tree_load_queries<D, FMT, R>(a, walk, 0, 1, lane, smem + L::kQOff + x * L::kQBytes,
                                    reinterpret_cast<TreeRows*>(smem + L::kRowsOff + x * L::kRowsBytes),
                                    reinterpret_cast<float*>(smem + L::kT5Off) + x * kTreeT5Slice, BIAS != 0);
       fence_async_shared();
@@ -772,7 +814,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     while (walk.next(a)) {
       const TreeSeq& s = walk.s;
       const TreeRows* info = reinterpret_cast<const TreeRows*>(smem + L::kRowsOff + (u & 1) * L::kRowsBytes);
-      wait(q_full(u & 1), (u >> 1) & 1);
+      if (u == 0) {
+        tree_load_queries<D, FMT, R>(a, walk, warp, 8, lane, smem + L::kQOff,
+                                     reinterpret_cast<TreeRows*>(smem + L::kRowsOff),
+                                     reinterpret_cast<float*>(smem + L::kT5Off), BIAS != 0);
+        fence_async_shared();
+        named_barrier(3, 256);
+        if (tid == 0) mbar_arrive(q_full(0));
+      } else {
+        wait(q_full(u & 1), (u >> 1) & 1);
+      }
       float ref[RT], l[RT];
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
@@ -828,6 +879,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         const bool masked = key0 + kTreeKeys > s.ctx || (a.wl >= 0 && key0 < s.ctx + s.n - 1 - a.wl);
         const int node = key - s.ctx;
         const int key_pos = node >= 0 ? s.ctx + (node < s.n ? info->depth[node] : 0) : key;
+        bool hidden = false;  // from some row
         if constexpr (BIAS != 0) {
           if (a.alibi_slopes) {
 #pragma unroll
@@ -854,15 +906,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           }
         }
         if (masked) {
-          const uint32_t seen = node < 0 ? ~0u : node < s.n ? static_cast<uint32_t>(info->seen[node] >> row0) : 0u;
-#pragma unroll
-          for (int j = 0; j < RT; ++j)
-            if (!((seen >> j) & 1u)) sc[j] = -INFINITY;
+          uint32_t seen = node < 0 ? ~0u : node < s.n ? info->seen[node][row0 / 32] : 0u;
           if (a.wl >= 0) {
 #pragma unroll
             for (int j = 0; j < RT; ++j)
-              if (info->pos[row0 + j] - key_pos > a.wl) sc[j] = -INFINITY;
+              if (info->pos[row0 + j] - key_pos > a.wl) seen &= ~(1u << j);
           }
+          constexpr uint32_t kRows = RT == 32 ? ~0u : (1u << RT % 32) - 1u;
+          hidden = (seen & kRows) != kRows;
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+            if (!((seen >> j) & 1u)) sc[j] = -INFINITY;
         }
 
         // the weight buffer is free, and with turns this warpgroup's O at rest
@@ -876,13 +930,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           over = fmax3(over, d0, d1);
         }
         if (barrier_or(1 + wg, 128, over > (E4 ? kOverE4m3 : kOverBf16) || fresh)) {
-          float keep = 0.f;
-#pragma unroll
-          for (int j = 0; j < RT; ++j) {
-            const float m = warp_max(sc[j]);
-            if (lane == j) keep = m;
-          }
-          if (lane < RT) mine[lane * 4 + (warp & 3)] = keep;
+          const float top = by_halves<RT>(sc, lane, [](float x, float y) { return fmaxf(x, y); });
+          if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = top;
           named_barrier(1 + wg, 128);
           if ((warp & 3) == 0 && lane < RT) {
             const float4 w4 = *reinterpret_cast<const float4*>(mine + lane * 4);
@@ -954,19 +1003,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
         bool mend = false;
         if (masked) {
-          // 0 * NaN is NaN: an infinite or NaN value that some row must not see
-          // (stale rows of a page among them) is taken out of the tile, and
-          // added to the rows that do see it once P V of the tile is in O
+          // 0 * NaN is NaN: rows behind the sequence's end are zeroed (they hold
+          // anything), and an infinite or NaN value of a key hidden from some
+          // row is taken out of the tile and added to the rows that do see it
+          // once P V of the tile is in O
           constexpr int kPieces = L::kRowBytes / 16;
           const uint32_t item = 2 * it + 1;
           uint8_t* vrows = smem + slot_off(item);
           wait(full(item % NS), (item / NS) & 1);
           uint32_t odd = 0;
+          if (key >= s.keys) {
+            if (L::kTurns || wg == 0) {
 #pragma unroll 4
-          for (int c = 0; c < kPieces; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vrows + L::at(me, c, kTreeKeys));
-            odd |= nonfinite_bits<FMT>(w.x) | nonfinite_bits<FMT>(w.y) | nonfinite_bits<FMT>(w.z) |
-                   nonfinite_bits<FMT>(w.w);
+              for (int c = 0; c < kPieces; ++c)
+                *reinterpret_cast<uint4*>(vrows + L::at(me, c, kTreeKeys)) = make_uint4(0, 0, 0, 0);
+            }
+          } else if (hidden) {
+#pragma unroll 4
+            for (int c = 0; c < kPieces; ++c) {
+              const uint4 w = *reinterpret_cast<const uint4*>(vrows + L::at(me, c, kTreeKeys));
+              odd |= nonfinite_bits<FMT>(w.x) | nonfinite_bits<FMT>(w.y) | nonfinite_bits<FMT>(w.z) |
+                     nonfinite_bits<FMT>(w.w);
+            }
           }
           constexpr uint32_t kAll = L::kTurns ? 128 : 256;  // threads of the tile
           const uint32_t b_all = L::kTurns ? 1 + wg : 3;
@@ -1034,20 +1092,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
       }
 
-      // ---- the piece's result.  Row sums over the warpgroup's keys: lanes
-      // trade halves of their rows, upper lanes keeping the upper half
-#pragma unroll
-      for (int n = RT, o = 16; n > 1; n >>= 1, o >>= 1) {
-        const bool up = (lane & o) != 0;
-#pragma unroll
-        for (int j = 0; j < n / 2; ++j) {
-          const float send = up ? l[j] : l[j + n / 2];
-          l[j] = (up ? l[j + n / 2] : l[j]) + __shfl_xor_sync(~0u, send, o);
-        }
-      }
-#pragma unroll
-      for (int o = 16 / RT; o > 0; o >>= 1) l[0] += __shfl_xor_sync(~0u, l[0], o);
-      if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = l[0];
+      // ---- the piece's result: row sums over the warpgroup's keys, then O
+      const float total = by_halves<RT>(l, lane, [](float x, float y) { return x + y; });
+      if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = total;
       // the last P V of this warpgroup's O
       const uint32_t last = it - 1;
       if (!L::kTurns) values_done(last);
@@ -1176,7 +1223,7 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
   int c0 = 0, c1 = 0;
   if (n < s.n) {
     const int64_t per = tree_share(total, ctas);
-    const int64_t first = before + (static_cast<int64_t>(hkv) * s.rb + block) * s.tiles;
+    const int64_t first = before + (static_cast<int64_t>(hkv) * s.rb + block) * s.span() + kTreePieceCost;
     c0 = static_cast<int>(first / per);
     c1 = static_cast<int>((first + s.tiles - 1) / per);
   }
