@@ -605,31 +605,44 @@ def sdpa_status_string(status: int) -> str:
 
 
 # ------------------------------------------------------------------- serving
-def _on_device(ref: torch.Tensor, **tensors):
-    """Every given tensor on ref's GPU, which is the current one."""
-    dev = ref.device
-    if dev.type != "cuda":
+# These calls sit in a generation loop whose kernels take a few microseconds, so
+# each reads what it needs of a tensor once and passes plain integers.
+_BF16, _E4M3, _F32, _F64 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.float64
+_I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
+
+
+def _device_stream(ref: torch.Tensor, *tensors):
+    """The raw current stream of ref's GPU, which must be the current one and every tensor's."""
+    dev = ref.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, which is not the current CUDA device")
-    for n, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, not on {dev}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, which is not the current CUDA device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors are on {t.device} and on cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, *shape: int):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {str(dtype)[6:]} {list(shape)}")
+def _bad(name: str, what: str):
+    raise ValueError(f"{name} must be {what}")
 
 
-def _heads(t: torch.Tensor, name: str, dims: int):
-    if t.dtype != torch.bfloat16 or t.dim() != dims or t.stride(-1) != 1:
-        raise ValueError(f"{name} must be bf16 with {dims} dimensions and a contiguous head_dim")
+def _rows(t: torch.Tensor, name: str, dims: int):
+    """Shape and strides of a bf16 tensor of head rows; the stride of a dimension that is never
+    stepped along is given as 8."""
+    st = t.stride()
+    sh = t.shape
+    if t.dtype != _BF16 or len(sh) != dims or (st[-1] != 1 and sh[-1] != 1):
+        _bad(name, f"bf16 with {dims} dimensions and a contiguous head_dim")
+    if 1 in sh:
+        st = tuple(8 if n == 1 else x for n, x in zip(sh, st))
+    return sh, st
 
 
-def _stride8(t: torch.Tensor, i: int) -> int:
-    """Stride of dimension i; one that is never taken may be anything."""
-    return t.stride(i) if t.shape[i] > 1 else 8
+def _alike(t: torch.Tensor, name: str, sh, st):
+    if t.dtype != _BF16 or t.shape != sh or (t.stride() != st and _rows(t, name, len(sh))[1] != st):
+        _bad(name, "bf16 with the shape and strides of its partner")
 
 
 def sdpa_rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, original_length=0,
@@ -644,7 +657,7 @@ def sdpa_rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, orig
                                                 float(factor), int(original_length),
                                                 float(beta_fast), float(beta_slow), out,
                                                 ctypes.byref(amplitude)), "sdpa_rope_frequencies")
-    return torch.tensor(list(out), dtype=torch.float64, device=device), amplitude.value
+    return torch.tensor(list(out), dtype=_F64, device=device), amplitude.value
 
 
 def sdpa_rope(q, k, freqs, positions=None, *, offset=0, interleaved=False, inverse=False,
@@ -656,96 +669,112 @@ def sdpa_rope(q, k, freqs, positions=None, *, offset=0, interleaved=False, inver
     ``inverse`` turns back: the gradient.  out_q=q, out_k=k works in place.
     """
     lib = load_library()
-    packed = q.dim() == 3
-    _heads(q, "q", 3 if packed else 4)
-    _on_device(q, k=k, freqs=freqs, positions=positions, out_q=out_q, out_k=out_k)
-    B, (L, Hq, d) = (1 if packed else q.shape[0]), q.shape[-3:]
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise ValueError("freqs must be a contiguous float64 vector")
-    pos_b = L
+    dims = q.dim()
+    if dims != 3 and dims != 4:
+        _bad("q", "[B, L, Hq, d] or [T, Hq, d]")
+    stream = _device_stream(q, k, freqs, positions, out_q, out_k)
+    qs, qst = _rows(q, "q", dims)
+    d, Hq, L = qs[-1], qs[-2], qs[-3]
+    B, zero = (qs[0], ()) if dims == 4 else (1, (8,))
+    if freqs.dtype != _F64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        _bad("freqs", "a contiguous float64 vector")
+    pos, pos_b = None, L
     if positions is not None:
-        if positions.dtype != torch.int32 or positions.shape != q.shape[:-2]:
-            raise ValueError("positions must be int32 [B, L] (packed: [T])")
-        if L > 1 and positions.stride(-1) != 1:
-            raise ValueError("positions must be contiguous along the sequence")
-        pos_b = L if packed or B == 1 else positions.stride(0)
-    out_q = torch.empty(q.shape, device=q.device, dtype=q.dtype) if out_q is None else out_q
+        if positions.dtype != _I32 or positions.shape != qs[:-2]:
+            _bad("positions", "int32 [B, L] (packed: [T])")
+        pst = positions.stride()
+        if L > 1 and pst[-1] != 1:
+            _bad("positions", "contiguous along the sequence")
+        pos, pos_b = positions.data_ptr(), (pst[0] if B > 1 else L)
+    if out_q is None:
+        out_q = torch.empty(qs, device=q.device, dtype=_BF16)
+    ost = _rows(out_q, "out_q", dims)[1]
+    if out_q.shape != qs:
+        _bad("out_q", f"{tuple(qs)}")
     if k is not None:
-        _heads(k, "k", q.dim())
-        if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d:
-            raise ValueError(f"k shape {tuple(k.shape)} does not match q {tuple(q.shape)}")
-        out_k = torch.empty(k.shape, device=k.device, dtype=k.dtype) if out_k is None else out_k
-    strides = []
-    for t, ref, n in ((q, q, "q"), (k, k, "k"), (out_q, q, "out_q"), (out_k if k is not None else None,
-                                                                     k, "out_k")):
-        if t is None:
-            strides += [0, 0, 0]
-            continue
-        _heads(t, n, q.dim())
-        if t.shape != ref.shape:
-            raise ValueError(f"{n} shape {tuple(t.shape)} is not {tuple(ref.shape)}")
-        strides += [8 if packed else _stride8(t, 0), _stride8(t, -3), _stride8(t, -2)]
-    if q.numel() == 0:
-        return out_q, (out_k if k is not None else None)
-    r = RopeDesc(B, L, Hq, 0 if k is None else k.shape[-2], d, *strides,
-                 positions.data_ptr() if positions is not None else None, pos_b, int(offset),
-                 freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0,
-                 1 if inverse else 0, float(amplitude))
-    _check(lib.sdpa_rope(ctypes.byref(r), _ptr(q), _ptr(k), _ptr(out_q), _ptr(out_k), _stream(q)),
-           "sdpa_rope")
-    return out_q, (out_k if k is not None else None)
+        ks, kst = _rows(k, "k", dims)
+        if ks[:-2] != qs[:-2] or ks[-1] != d:
+            raise ValueError(f"k shape {tuple(ks)} does not match q {tuple(qs)}")
+        if out_k is None:
+            out_k = torch.empty(ks, device=q.device, dtype=_BF16)
+        okst = _rows(out_k, "out_k", dims)[1]
+        if out_k.shape != ks:
+            _bad("out_k", f"{tuple(ks)}")
+        Hkv, kp, okp = ks[-2], k.data_ptr(), out_k.data_ptr()
+    else:
+        kst = okst = (0,) * dims
+        Hkv, kp, okp, out_k = 0, None, None, None
+    if B * L == 0:
+        return out_q, out_k
+    r = RopeDesc(B, L, Hq, Hkv, d, *zero, *qst[:-1], *zero, *kst[:-1], *zero, *ost[:-1], *zero,
+                 *okst[:-1], pos, pos_b, offset, freqs.data_ptr(), 2 * freqs.shape[0], interleaved,
+                 inverse, amplitude)
+    st = lib.sdpa_rope(ctypes.byref(r), q.data_ptr(), kp, out_q.data_ptr(), okp, stream)
+    if st:
+        raise SdpaError(st, "sdpa_rope")
+    return out_q, out_k
 
 
 def make_cache(k_cache, v_cache, k_scale=None, v_scale=None) -> KvCache:
     """Descriptor of a paged cache [num_pages, Hkv, page_size, d]: bf16, or float8_e4m3fn with
     uint8 scale exponents [num_pages, Hkv, page_size]."""
-    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    dt, sh, st = k_cache.dtype, k_cache.shape, k_cache.stride()
+    e4m3 = dt == _E4M3
+    if not e4m3 and dt != _BF16:
         raise ValueError("a cache is bf16 or float8_e4m3fn")
-    if (k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype
-            or v_cache.stride() != k_cache.stride() or k_cache.stride(-1) != 1):
+    if (len(sh) != 4 or v_cache.shape != sh or v_cache.dtype != dt or v_cache.stride() != st
+            or st[3] != 1):
         raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] alike in "
                          "type, shape and strides, with a contiguous head_dim")
-    _on_device(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    P, H, page, d = k_cache.shape
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
-    ss = [0, 0]
+    P, H, page, d = sh
+    sp = sh_ = 0
+    kp = vp = None
     if e4m3:
         if k_scale is None or v_scale is None:
             raise ValueError("an e4m3 cache needs k_scale and v_scale")
-        if (k_scale.dtype != torch.uint8 or tuple(k_scale.shape) != (P, H, page)
-                or k_scale.stride(-1) != 1 or v_scale.dtype != torch.uint8
-                or v_scale.shape != k_scale.shape or v_scale.stride() != k_scale.stride()):
+        ss = k_scale.stride()
+        if (k_scale.dtype != _U8 or k_scale.shape != sh[:3] or ss[2] != 1 or v_scale.dtype != _U8
+                or v_scale.shape != sh[:3] or v_scale.stride() != ss):
             raise ValueError("k_scale and v_scale must be uint8 [num_pages, Hkv, page_size] alike "
                              "in strides, with contiguous rows")
-        ss = [k_scale.stride(i) if k_scale.shape[i] > 1 else 16 for i in (0, 1)]
+        sp, sh_ = (ss[0] if P > 1 else 16), (ss[1] if H > 1 else 16)
+        kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("a bf16 cache has no scales")
-    st = [k_cache.stride(i) if k_cache.shape[i] > 1 else 16 for i in (0, 1, 2)]
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if e4m3 else None,
-                   v_scale.data_ptr() if e4m3 else None, CACHE_E4M3 if e4m3 else CACHE_BF16,
-                   P, page, H, d, *st, *ss)
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, 1 if e4m3 else 0, P, page, H, d,
+                   st[0] if P > 1 else 16, st[1] if H > 1 else 16, st[2] if page > 1 else 16, sp,
+                   sh_)
 
 
 def _table(page_table: torch.Tensor, B: int):
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B
-            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-        raise ValueError("page_table must be int32 [B, pages] with contiguous rows")
-    return page_table.shape[1], page_table.stride(0) if B > 1 else page_table.shape[1]
+    sh, st = page_table.shape, page_table.stride()
+    if page_table.dtype != _I32 or len(sh) != 2 or sh[0] != B or (sh[1] > 1 and st[1] != 1):
+        _bad("page_table", "int32 [B, pages] with contiguous rows")
+    return sh[1], (st[0] if B > 1 else sh[1])
+
+
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _bad(name, f"contiguous {str(dtype)[6:]} {list(shape)}")
+    return t.data_ptr()
 
 
 def sdpa_cache_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
     """Rows k, v [T, Hkv, d] into the cache at slots int64 [T] (page * page_size + row;
     negative: skipped), quantised if the cache is e4m3 (see sdpa_cache_append)."""
     lib = load_library()
+    stream = _device_stream(k_cache, v_cache, k_scale, v_scale, k, v, slots)
     c = make_cache(k_cache, v_cache, k_scale, v_scale)
-    _heads(k, "k", 3)
-    _same_layout(v, k, "v")
-    _on_device(k_cache, k=k, v=v, slots=slots)
-    if k.shape[1] != c.Hkv or k.shape[2] != c.d:
-        raise ValueError(f"k {tuple(k.shape)} does not fit the cache's heads")
-    _vector(slots, "slots", torch.int64, k.shape[0])
-    _check(lib.sdpa_cache_append(ctypes.byref(c), _ptr(k), _ptr(v), k.shape[0], _stride8(k, 0),
-                                 _stride8(k, 1), _ptr(slots), _stream(k)), "sdpa_cache_append")
+    sh, st = _rows(k, "k", 3)
+    _alike(v, "v", sh, st)
+    T, H, d = sh
+    if H != c.Hkv or d != c.d:
+        raise ValueError(f"k {tuple(sh)} does not fit the cache's heads")
+    sp = _vector(slots, "slots", _I64, (T,))
+    r = lib.sdpa_cache_append(ctypes.byref(c), k.data_ptr(), v.data_ptr(), T, st[0], st[1], sp,
+                              stream)
+    if r:
+        raise SdpaError(r, "sdpa_cache_append")
 
 
 def sdpa_cache_gather(k_cache, v_cache, page_table, cu_seqlens, total, k_scale=None, v_scale=None,
@@ -753,21 +782,24 @@ def sdpa_cache_gather(k_cache, v_cache, page_table, cu_seqlens, total, k_scale=N
     """The cached sequences as packed bf16 (k, v) [total, Hkv, d], sequence b's first
     cu_seqlens[b + 1] - cu_seqlens[b] positions at its rows (see sdpa_cache_gather)."""
     lib = load_library()
+    stream = _device_stream(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, k, v)
     c = make_cache(k_cache, v_cache, k_scale, v_scale)
-    _on_device(k_cache, page_table=page_table, cu_seqlens=cu_seqlens, k=k, v=v)
     B = cu_seqlens.numel() - 1
-    _vector(cu_seqlens, "cu_seqlens", torch.int32, B + 1)
+    cu = _vector(cu_seqlens, "cu_seqlens", _I32, (B + 1,))
     width, table_b = _table(page_table, B)
     shape = (int(total), c.Hkv, c.d)
-    k = torch.empty(shape, device=k_cache.device, dtype=torch.bfloat16) if k is None else k
-    v = torch.empty(shape, device=k_cache.device, dtype=torch.bfloat16) if v is None else v
-    _heads(k, "k", 3)
-    if tuple(k.shape) != shape:
-        raise ValueError(f"k must be {list(shape)}")
-    _same_layout(v, k, "v")
-    _check(lib.sdpa_cache_gather(ctypes.byref(c), B, _ptr(page_table), width, table_b,
-                                 _ptr(cu_seqlens), int(total), _ptr(k), _ptr(v), _stride8(k, 0),
-                                 _stride8(k, 1), _stream(k_cache)), "sdpa_cache_gather")
+    if k is None:
+        k = torch.empty(shape, device=k_cache.device, dtype=_BF16)
+    if v is None:
+        v = torch.empty_like(k)
+    sh, st = _rows(k, "k", 3)
+    if sh != shape:
+        _bad("k", f"{list(shape)}")
+    _alike(v, "v", sh, st)
+    r = lib.sdpa_cache_gather(ctypes.byref(c), B, page_table.data_ptr(), width, table_b, cu,
+                              shape[0], k.data_ptr(), v.data_ptr(), st[0], st[1], stream)
+    if r:
+        raise SdpaError(r, "sdpa_cache_gather")
     return k, v
 
 
@@ -780,41 +812,40 @@ def sdpa_tree_fwd(q, k_cache, v_cache, page_table, ctx_lens, cu_nodes, max_nodes
     per sequence is plain decoding.  The nodes' own keys are in the cache already, at positions
     ctx_lens[b] and on (see sdpa_tree_fwd in include/sdpa.h)."""
     lib = load_library()
+    stream = _device_stream(k_cache, v_cache, k_scale, v_scale, q, page_table, ctx_lens, cu_nodes,
+                            tree_mask, t5_table, alibi_slopes, out, lse, workspace)
     c = make_cache(k_cache, v_cache, k_scale, v_scale)
-    _heads(q, "q", 3)
-    _on_device(k_cache, q=q, page_table=page_table, ctx_lens=ctx_lens, cu_nodes=cu_nodes,
-               tree_mask=tree_mask, t5_table=t5_table, alibi_slopes=alibi_slopes, out=out, lse=lse,
-               workspace=workspace)
-    T, Hq, d = q.shape
+    sh, qst = _rows(q, "q", 3)
+    T, Hq, d = sh
     if d != c.d:
         raise ValueError("q and the cache differ in head_dim")
     B = ctx_lens.numel()
-    _vector(ctx_lens, "ctx_lens", torch.int32, B)
-    _vector(cu_nodes, "cu_nodes", torch.int32, B + 1)
-    if tree_mask is not None:
-        _vector(tree_mask, "tree_mask", torch.int64, T)
+    ctx = _vector(ctx_lens, "ctx_lens", _I32, (B,))
+    cu = _vector(cu_nodes, "cu_nodes", _I32, (B + 1,))
+    mask = None if tree_mask is None else _vector(tree_mask, "tree_mask", _I64, (T,))
     width, table_b = _table(page_table, B)
-    out = torch.empty(q.shape, device=q.device, dtype=q.dtype) if out is None else out
-    _heads(out, "out", 3)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+    if out is None:
+        out = torch.empty(sh, device=q.device, dtype=_BF16)
+    osh, ost = _rows(out, "out", 3)
+    if osh != sh:
+        _bad("out", "of q's shape")
     if lse is None:
-        lse = torch.empty(Hq, T, device=q.device, dtype=torch.float32)
-    _vector(lse, "lse", torch.float32, Hq, T)
-    t = Tree(B, T, int(max_nodes), Hq, _stride8(q, 0), _stride8(q, 1), _stride8(out, 0),
-             _stride8(out, 1), cu_nodes.data_ptr(), ctx_lens.data_ptr(), page_table.data_ptr(),
-             width, table_b, tree_mask.data_ptr() if tree_mask is not None else None,
-             int(window_left))
-    bd = make_bias(None, t5_table, t5_num_buckets, t5_max_distance, t5_bidirectional,
-                   (B, Hq, 0, 0), alibi_slopes)
+        lse = torch.empty(Hq, T, device=q.device, dtype=_F32)
+    lp = _vector(lse, "lse", _F32, (Hq, T))
+    t = Tree(B, T, max_nodes, Hq, qst[0], qst[1], ost[0], ost[1], cu, ctx, page_table.data_ptr(),
+             width, table_b, mask, window_left)
+    bias = None
+    if t5_table is not None or alibi_slopes is not None:
+        bias = ctypes.byref(make_bias(None, t5_table, t5_num_buckets, t5_max_distance,
+                                      t5_bidirectional, (B, Hq, 0, 0), alibi_slopes))
+    tp, cp = ctypes.byref(t), ctypes.byref(c)
     if workspace is None:
-        need = int(lib.sdpa_tree_fwd_workspace_size(ctypes.byref(t), ctypes.byref(c)))
-        workspace = torch.empty(max(need, 256), device=q.device, dtype=torch.uint8)
-    sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    st = lib.sdpa_tree_fwd(ctypes.byref(t), ctypes.byref(c), _ptr(q), ctypes.byref(bd), sc,
-                           _ptr(out), _ptr(lse), _ptr(workspace),
-                           workspace.numel() * workspace.element_size(), _stream(q))
-    _check(st, "sdpa_tree_fwd")
+        workspace = torch.empty(lib.sdpa_tree_fwd_workspace_size(tp, cp), device=q.device,
+                                dtype=_U8)
+    r = lib.sdpa_tree_fwd(tp, cp, q.data_ptr(), bias, d ** -0.5 if scale is None else scale,
+                          out.data_ptr(), lp, workspace.data_ptr(), workspace.nbytes, stream)
+    if r:
+        raise SdpaError(r, "sdpa_tree_fwd")
     return out, lse
 
 
@@ -823,8 +854,8 @@ def sdpa_tree_fwd_workspace_size(q, k_cache, v_cache, page_table, ctx_lens, cu_n
     """Bytes of the workspace of sdpa_tree_fwd for these tensors (0: they do not fit together)."""
     c = make_cache(k_cache, v_cache, k_scale, v_scale)
     width, table_b = _table(page_table, ctx_lens.numel())
-    st = (_stride8(q, 0), _stride8(q, 1))
-    t = Tree(ctx_lens.numel(), q.shape[0], int(max_nodes), q.shape[1], *st, *st,
+    sh, st = _rows(q, "q", 3)
+    t = Tree(ctx_lens.numel(), sh[0], int(max_nodes), sh[1], st[0], st[1], st[0], st[1],
              cu_nodes.data_ptr(), ctx_lens.data_ptr(), page_table.data_ptr(), width, table_b, None,
              -1)
     return int(load_library().sdpa_tree_fwd_workspace_size(ctypes.byref(t), ctypes.byref(c)))
@@ -839,30 +870,33 @@ def sdpa_spec_verify(target, draft, tokens, parents, u_accept, u_sample):
     u_sample float32 [B].
     """
     lib = load_library()
-    if target.dtype != torch.float32 or target.dim() != 3 or target.stride(2) != 1:
-        raise ValueError("target must be float32 [B, N, V] with a contiguous vocabulary")
-    _on_device(target, draft=draft, tokens=tokens, parents=parents, u_accept=u_accept,
-               u_sample=u_sample)
-    B, N, V = target.shape
+    stream = _device_stream(target, draft, tokens, parents, u_accept, u_sample)
+    sh, tst = target.shape, target.stride()
+    if target.dtype != _F32 or len(sh) != 3 or (tst[2] != 1 and sh[2] != 1):
+        _bad("target", "float32 [B, N, V] with a contiguous vocabulary")
+    B, N, V = sh
+    dp = xp = pp = up = None
+    dst = (0, 0)
     if draft is not None:
-        if draft.dtype != torch.float32 or draft.shape != target.shape or draft.stride(2) != 1:
-            raise ValueError("draft must be float32 [B, N, V] with a contiguous vocabulary")
+        dst = draft.stride()
+        if draft.dtype != _F32 or draft.shape != sh or (dst[2] != 1 and V != 1):
+            _bad("draft", "float32 [B, N, V] with a contiguous vocabulary")
+        dp = draft.data_ptr()
     if N > 1:
         if draft is None:
             raise ValueError("draft distributions are needed when there are drafted nodes")
-        _vector(tokens, "tokens", torch.int32, B, N)
-        _vector(u_accept, "u_accept", torch.float32, B, N)
-    if parents is not None:
-        _vector(parents, "parents", torch.int32, B, N)
-    _vector(u_sample, "u_sample", torch.float32, B)
-    i32 = dict(device=target.device, dtype=torch.int32)
-    path, accepted, token = torch.empty(B, N, **i32), torch.empty(B, **i32), torch.empty(B, **i32)
-    ds = (draft.stride(0), draft.stride(1)) if draft is not None else (0, 0)
-    s = Verify(B, N, V, target.stride(0), target.stride(1), *ds, target.data_ptr(),
-               draft.data_ptr() if draft is not None else None,
-               tokens.data_ptr() if tokens is not None else None,
-               parents.data_ptr() if parents is not None else None,
-               u_accept.data_ptr() if u_accept is not None else None, u_sample.data_ptr())
-    _check(lib.sdpa_spec_verify(ctypes.byref(s), _ptr(path), _ptr(accepted), _ptr(token),
-                                _stream(target)), "sdpa_spec_verify")
+        xp = _vector(tokens, "tokens", _I32, (B, N))
+        up = _vector(u_accept, "u_accept", _F32, (B, N))
+        if parents is not None:
+            pp = _vector(parents, "parents", _I32, (B, N))
+    us = _vector(u_sample, "u_sample", _F32, (B,))
+    dev = target.device
+    path = torch.empty(B, N, device=dev, dtype=_I32)
+    accepted = torch.empty(B, device=dev, dtype=_I32)
+    token = torch.empty(B, device=dev, dtype=_I32)
+    s = Verify(B, N, V, tst[0], tst[1], dst[0], dst[1], target.data_ptr(), dp, xp, pp, up, us)
+    r = lib.sdpa_spec_verify(ctypes.byref(s), path.data_ptr(), accepted.data_ptr(),
+                             token.data_ptr(), stream)
+    if r:
+        raise SdpaError(r, "sdpa_spec_verify")
     return path, accepted, token

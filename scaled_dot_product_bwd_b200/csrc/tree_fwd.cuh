@@ -893,15 +893,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           } else {
             const uint8_t* buckets = smem + L::kBucketOff;
             const float* slice = reinterpret_cast<const float*>(smem + L::kT5Off) + (u & 1) * kTreeT5Slice;
-            const bool in_slice = a.t5_buckets * a.G <= kTreeT5Slice;
-            const bool deep = a.t5.one_lo_max < -kTreeNear;  // buckets beyond the tabulated distances
             const int head0 = walk.hkv * a.G;
+            if (a.t5_buckets * a.G <= kTreeT5Slice && a.t5.one_lo_max >= -kTreeNear) {
+              // eight lookups in flight, without a branch between them
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-              const int rel = key_pos - info->pos[row0 + j], head = info->head[row0 + j];
-              int k = buckets[max(rel, -kTreeNear) + kTreeNear];
-              if (deep && rel < -kTreeNear) k = t5_bucket(rel, a.t5);
-              sc[j] += in_slice ? slice[k * a.G + head - head0] : bias_to_log2(a.t5_table[k * a.Hq + head]);
+              for (int j0 = 0; j0 < RT; j0 += 8) {
+                int at[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  at[j] = buckets[max(key_pos - info->pos[row0 + j0 + j], -kTreeNear) + kTreeNear];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sc[j0 + j] += slice[at[j] * a.G + info->head[row0 + j0 + j] - head0];
+              }
+            } else {
+              // a table too large for the slice, or buckets beyond the tabulated distances
+#pragma unroll
+              for (int j = 0; j < RT; ++j) {
+                const int rel = key_pos - info->pos[row0 + j];
+                const int k = rel < -kTreeNear ? t5_bucket(rel, a.t5) : buckets[rel + kTreeNear];
+                sc[j] += bias_to_log2(a.t5_table[k * a.Hq + info->head[row0 + j]]);
+              }
             }
           }
         }
