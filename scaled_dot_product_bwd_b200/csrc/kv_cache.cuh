@@ -79,73 +79,93 @@ struct AppendArgs {
   const int64_t* slots;
 };
 
-constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = 4;  // rows in flight per lane group
+// Both kernels: a CTA takes kCacheRows rows of K (blockIdx.y = 0) or V with all
+// heads.  Its first threads find where each row lies in the cache; then a
+// thread keeps one 16-byte piece of one head (several when the heads are
+// many) and goes through the rows, four in flight.
+constexpr int kCacheThreads = 256;
+constexpr int kCacheRows = 16;
 
-// One lane group (D / 8 lanes, 8 elements each) per (token, head) row of K or
-// V; blockIdx.y picks K or V.
+struct CacheCells {
+  int64_t off[kCacheRows];    // of the row in the cache, elements; < 0: none
+  int64_t scale[kCacheRows];  // of its scales
+};
+
+__device__ __forceinline__ void cache_cell(CacheCells& s, int i, const CacheView& c, int64_t page, int row) {
+  s.off[i] = page < 0 ? -1 : page * c.s_page + row * c.s_row;
+  s.scale[i] = page * c.ss_page + row;
+}
+
+// One lane group (D / 8 lanes, 8 elements each) holds a row of one head.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const AppendArgs a) {
   constexpr int kLanes = D / 8;
-  constexpr int kGroups = kAppendThreads / kLanes;
+  constexpr int kGroups = kCacheThreads / kLanes;
+  constexpr int kFlight = 4;
+  __shared__ CacheCells cells;
   const bool is_v = blockIdx.y != 0;
-  const __nv_bfloat16* src = is_v ? a.v : a.k;
-  const int lane = threadIdx.x % kLanes;
-  const int64_t n_rows = a.T * a.c.Hkv;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kGroups * kAppendRows) +
-                     threadIdx.x / kLanes;
-  const int64_t n_slots = a.c.num_pages << a.c.page_shift;
-  uint4 x[kAppendRows];
-  int64_t slot[kAppendRows];
-  int head[kAppendRows];
-#pragma unroll
-  for (int i = 0; i < kAppendRows; ++i) {
-    const int64_t r = r0 + static_cast<int64_t>(i) * kGroups;
-    slot[i] = -1;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r < n_rows) {
-      const int64_t t = r / a.c.Hkv;
-      head[i] = static_cast<int>(r - t * a.c.Hkv);
-      slot[i] = a.slots[t];
-      x[i] = *reinterpret_cast<const uint4*>(src + t * a.kv_t + head[i] * a.kv_h + lane * 8);
-    }
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kCacheRows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kCacheRows), a.T - t0));
+  if (threadIdx.x < rows) {
+    const int64_t slot = a.slots[t0 + threadIdx.x];
+    int64_t page = -1;
+    if (slot >= a.c.num_pages << a.c.page_shift) atomicOr(&g_device_status, kStatusBadSeqlens);
+    else if (slot >= 0) page = slot >> a.c.page_shift;
+    cache_cell(cells, threadIdx.x, a.c, page, static_cast<int>(slot & (a.c.page_size - 1)));
   }
+  __syncthreads();
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  // groups side by side over the heads, the rest over rows
+  const int across = min(a.c.Hkv, kGroups);
+  const int down = kGroups / across;
+  const int sub = group / across;
+  if (sub >= down) return;  // whole groups, after the last barrier
+  const __nv_bfloat16* src0 = (is_v ? a.v : a.k) + t0 * a.kv_t + lane * 8;
+  for (int h = group - sub * across; h < a.c.Hkv; h += across) {
+    const __nv_bfloat16* src = src0 + h * a.kv_h;
+    for (int r0 = sub; r0 < rows; r0 += down * kFlight) {
+      uint4 x[kFlight];
 #pragma unroll
-  for (int i = 0; i < kAppendRows; ++i) {
-    if (slot[i] >= n_slots) {
-      atomicOr(&g_device_status, kStatusBadSeqlens);
-      slot[i] = -1;
-    }
-    const int64_t page = slot[i] >> a.c.page_shift;
-    const int row = static_cast<int>(slot[i] & (a.c.page_size - 1));
-    if (FMT == kCacheBf16) {
-      if (slot[i] >= 0) {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? a.c.v : a.c.k) +
-                             page * a.c.s_page + head[i] * a.c.s_head + row * a.c.s_row;
-        *reinterpret_cast<uint4*>(dst + lane * 8) = x[i];
-      }
-    } else {
-      // largest finite magnitude: bf16 magnitudes order as their bits
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
-        m = max(m, lo < 0x7f80u ? lo : 0u);
-        m = max(m, hi < 0x7f80u ? hi : 0u);
+      for (int f = 0; f < kFlight; ++f) {
+        const int r = r0 + f * down;
+        x[f] = r < rows ? __ldcs(reinterpret_cast<const uint4*>(src + r * a.kv_t)) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int s = kLanes / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(~0u, m, s));
-      const uint32_t e = e4m3_scale_byte(__uint_as_float(m << 16));
-      // 2^(127 - e): e in 1 .. 254 keeps it a normal float except at 254
-      const float inv = e8m0_float(254u - e);
-      if (slot[i] >= 0) {
-        uint8_t* dst = static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + page * a.c.s_page +
-                       head[i] * a.c.s_head + row * a.c.s_row;
-        *reinterpret_cast<uint2*>(dst + lane * 8) = bf16x8_to_e4m3(x[i], inv);
-        if (lane == 0)
-          (is_v ? a.c.vs : a.c.ks)[page * a.c.ss_page + head[i] * a.c.ss_head + row] =
-              static_cast<uint8_t>(e);
+      for (int f = 0; f < kFlight; ++f) {
+        const int r = r0 + f * down;
+        const int64_t off = r < rows ? cells.off[r] : -1;
+        if (FMT == kCacheBf16) {
+          if (off >= 0)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? a.c.v : a.c.k) + off +
+                                      h * a.c.s_head + lane * 8) = x[f];
+        } else {
+          // largest magnitude: bf16 magnitudes order as their bits
+          const uint32_t w[4] = {x[f].x & 0x7fff7fffu, x[f].y & 0x7fff7fffu, x[f].z & 0x7fff7fffu,
+                                 x[f].w & 0x7fff7fffu};
+          constexpr uint32_t kGroup = kLanes == 16 ? 0xffffu : 0xffu;
+          const uint32_t members = kGroup << (threadIdx.x & 31 & ~(kLanes - 1));
+          uint32_t m2 = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+#pragma unroll
+          for (int s = kLanes / 2; s > 0; s >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(members, m2, s));
+          uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+          if (m >= 0x7f80u) {  // the largest finite one, then
+            m = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t lo = w[j] & 0xffffu, hi = w[j] >> 16;
+              m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            }
+#pragma unroll
+            for (int s = kLanes / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(members, m, s));
+          }
+          const uint32_t e = e4m3_scale_byte(__uint_as_float(m << 16));
+          if (off >= 0) {
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + off + h * a.c.s_head +
+                                      lane * 8) = bf16x8_to_e4m3(x[f], e8m0_float(254u - e));
+            if (lane == 0)
+              (is_v ? a.c.vs : a.c.ks)[cells.scale[r] + h * a.c.ss_head] = static_cast<uint8_t>(e);
+          }
+        }
       }
     }
   }
@@ -169,87 +189,83 @@ struct GatherArgs {
   int64_t kv_t, kv_h;
 };
 
-constexpr int kGatherThreads = 256;
-constexpr int kGatherRows = 16;  // packed rows per CTA
-
-// kGatherRows packed rows of all heads, K (blockIdx.y = 0) or V per CTA.  The
-// first kGatherRows threads find their row's sequence (binary search in
-// cu_seqlens) and page; then lane groups copy (row, head) pieces.
+// The first threads find their row's sequence (binary search in cu_seqlens)
+// and page.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const GatherArgs a) {
-  __shared__ int64_t cell[kGatherRows];   // page * page_size + row, or -1
+__global__ void __launch_bounds__(kCacheThreads) cache_gather_kernel(const GatherArgs a) {
+  constexpr int kLanes = FMT == kCacheBf16 ? D / 8 : D / 16;  // 16 stored bytes per lane
+  constexpr int kGroups = kCacheThreads / kLanes;
+  constexpr int kFlight = 4;
+  __shared__ CacheCells cells;
   const bool is_v = blockIdx.y != 0;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGatherRows;
-  if (threadIdx.x < kGatherRows) {
-    const int64_t r = r0 + threadIdx.x;
-    int64_t at = -1;
+  const int64_t r00 = static_cast<int64_t>(blockIdx.x) * kCacheRows;
+  if (threadIdx.x < kCacheRows) {
+    const int64_t r = r00 + threadIdx.x;
+    int64_t page = -1, pos = 0;
     if (r < a.total && r < a.cu[a.B]) {
       int lo = 0, hi = a.B;  // cu[lo] <= r < cu[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (a.cu[mid] <= r) lo = mid; else hi = mid;
       }
-      const int64_t pos = r - a.cu[lo];
+      pos = r - a.cu[lo];
       const int64_t col = pos >> a.c.page_shift;
-      int64_t page = -1;
       if (pos >= 0 && r < a.cu[lo + 1] && col < a.width) page = a.table[lo * a.table_b + col];
-      if (page >= 0 && page < a.c.num_pages)
-        at = (page << a.c.page_shift) + (pos & (a.c.page_size - 1));
-      else
+      if (page < 0 || page >= a.c.num_pages) {
         atomicOr(&g_device_status, kStatusBadSeqlens);
-    }
-    cell[threadIdx.x] = at;
-  }
-  __syncthreads();
-  constexpr int kLanes = FMT == kCacheBf16 ? D / 8 : D / 16;  // 16 stored bytes per lane
-  const int n = kGatherRows * a.c.Hkv * kLanes;
-  constexpr int kFlight = 4;
-  for (int base = threadIdx.x; base < n; base += kFlight * kGatherThreads) {
-    uint4 x[kFlight];
-    __nv_bfloat16* dst[kFlight];
-    uint32_t e[kFlight];
-#pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int it = base + f * kGatherThreads;
-      dst[f] = nullptr;
-      if (it >= n) continue;
-      const int lane = it % kLanes;
-      const int rh = it / kLanes;
-      const int row = rh / a.c.Hkv, h = rh - row * a.c.Hkv;
-      const int64_t at = cell[row];
-      if (at < 0) continue;
-      const int64_t page = at >> a.c.page_shift;
-      const int in = static_cast<int>(at & (a.c.page_size - 1));
-      const int64_t off = page * a.c.s_page + h * a.c.s_head + in * a.c.s_row;
-      dst[f] = (is_v ? a.v : a.k) + (r0 + row) * a.kv_t + h * a.kv_h;
-      if (FMT == kCacheBf16) {
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? a.c.v : a.c.k) + off;
-        x[f] = *reinterpret_cast<const uint4*>(src + lane * 8);
-        dst[f] += lane * 8;
-      } else {
-        const uint8_t* src = static_cast<const uint8_t*>(is_v ? a.c.v : a.c.k) + off;
-        x[f] = *reinterpret_cast<const uint4*>(src + lane * 16);
-        e[f] = (is_v ? a.c.vs : a.c.ks)[page * a.c.ss_page + h * a.c.ss_head + in];
-        dst[f] += lane * 16;
+        page = -1;
       }
     }
+    cache_cell(cells, threadIdx.x, a.c, page, static_cast<int>(pos & (a.c.page_size - 1)));
+  }
+  __syncthreads();
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int across = min(a.c.Hkv, kGroups);
+  const int down = kGroups / across;
+  const int sub = group / across;
+  if (sub >= down) return;
+  __nv_bfloat16* dst0 = (is_v ? a.v : a.k) + r00 * a.kv_t;
+  for (int h = group - sub * across; h < a.c.Hkv; h += across) {
+    for (int r0 = sub; r0 < kCacheRows; r0 += down * kFlight) {
+      uint4 x[kFlight];
+      uint32_t e[kFlight];
+      bool has[kFlight];
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      if (!dst[f]) continue;
-      if (FMT == kCacheBf16) {
-        *reinterpret_cast<uint4*>(dst[f]) = x[f];
-      } else {
-        const float s = e8m0_float(e[f]);
-        const uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 lo = e4m3x2_floats(w[j] & 0xffffu), hi = e4m3x2_floats(w[j] >> 16);
-          o[2 * j] = pack_bf16x2(lo.x * s, lo.y * s);
-          o[2 * j + 1] = pack_bf16x2(hi.x * s, hi.y * s);
+      for (int f = 0; f < kFlight; ++f) {
+        const int r = r0 + f * down;
+        const int64_t off = r < kCacheRows ? cells.off[r] : -1;
+        has[f] = off >= 0;
+        if (!has[f]) continue;
+        if (FMT == kCacheBf16) {
+          x[f] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_v ? a.c.v : a.c.k) +
+                                                       off + h * a.c.s_head + lane * 8));
+        } else {
+          x[f] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(is_v ? a.c.v : a.c.k) + off +
+                                                       h * a.c.s_head + lane * 16));
+          e[f] = (is_v ? a.c.vs : a.c.ks)[cells.scale[r] + h * a.c.ss_head];
         }
-        *reinterpret_cast<uint4*>(dst[f]) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst[f] + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f) {
+        if (!has[f]) continue;
+        __nv_bfloat16* dst = dst0 + (r0 + f * down) * a.kv_t + h * a.kv_h;
+        if (FMT == kCacheBf16) {
+          __stcs(reinterpret_cast<uint4*>(dst + lane * 8), x[f]);
+        } else {
+          const float s = e8m0_float(e[f]);
+          const uint64_t s2 = f2_pack(s, s);
+          const uint32_t w[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 v = e4m3x2_floats(j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
+            float y0, y1;
+            f2_unpack(f2_mul(f2_pack(v.x, v.y), s2), y0, y1);
+            o[j] = pack_bf16x2(y0, y1);
+          }
+          __stcs(reinterpret_cast<uint4*>(dst + lane * 16), make_uint4(o[0], o[1], o[2], o[3]));
+          __stcs(reinterpret_cast<uint4*>(dst + lane * 16 + 8), make_uint4(o[4], o[5], o[6], o[7]));
+        }
       }
     }
   }

@@ -35,8 +35,9 @@ struct RopeArgs {
   float amplitude, sign; // sign = -1 turns back
 };
 
-constexpr int kRopeTokens = 4;
+constexpr int kRopeTokens = 16;   // per CTA, at most
 constexpr int kRopeThreads = 256;
+constexpr int kRopeFlight = 4;    // items (16 elements) in flight per thread
 
 // How the pairs of a head lie in its 16-byte pieces.
 enum RopeMode : int {
@@ -48,9 +49,7 @@ enum RopeMode : int {
 // cos and sin of one (token, pair).  The angle is formed in float64 and
 // reduced to a fraction of a turn there: at position 10^6 a float32 angle of
 // the fastest pair would be off by up to 0.03 rad.
-__device__ __forceinline__ float2 rope_cos_sin(const RopeArgs& a, int64_t token, int i) {
-  const int64_t b = token / a.L;
-  const int64_t l = token - b * a.L;
+__device__ __forceinline__ float2 rope_cos_sin(const RopeArgs& a, int b, int l, int i) {
   const int64_t pos = a.positions ? a.positions[b * a.pos_b + l] : a.offset + l;
   const double turns = static_cast<double>(pos) * (a.freqs[i] * 0.15915494309189533577);
   float s, c;
@@ -68,11 +67,9 @@ __device__ __forceinline__ float2 bf16x2_floats(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// The head's row of `token` in the inputs and outputs.
-__device__ __forceinline__ void rope_row(const RopeArgs& a, int64_t token, int h,
+// Head h's row of token (b, l) in the inputs and outputs.
+__device__ __forceinline__ void rope_row(const RopeArgs& a, int b, int l, int h,
                                          const __nv_bfloat16*& src, __nv_bfloat16*& dst) {
-  const int64_t b = token / a.L;
-  const int64_t l = token - b * a.L;
   if (h < a.Hq) {
     src = a.q + b * a.q_b + l * a.q_l + h * a.q_h;
     dst = a.qo + b * a.qo_b + l * a.qo_l + h * a.qo_h;
@@ -84,7 +81,8 @@ __device__ __forceinline__ void rope_row(const RopeArgs& a, int64_t token, int h
 }
 
 // An item is 16 elements of one head, read whole before any is written (the
-// call may be in place).  Four items are in flight per thread.
+// call may be in place).  A CTA's tokens are chosen so that its items are one
+// batch of four per thread: they are on their way while the angles are formed.
 template <int D, int MODE>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   __shared__ __align__(16) float2 cs[kRopeTokens][D / 2];
@@ -92,14 +90,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.per_cta;
   const int nt = static_cast<int>(min(static_cast<int64_t>(a.per_cta), a.tokens - t0));
   const int tid = threadIdx.x;
-  for (int x = tid; x < nt * a.half; x += kRopeThreads) {
-    const int t = x / a.half;
-    cs[t][x - t * a.half] = rope_cos_sin(a, t0 + t, x - t * a.half);
+  __shared__ int row_b[kRopeTokens], row_l[kRopeTokens];
+  if (tid < nt) {
+    row_b[tid] = static_cast<int>((t0 + tid) / a.L);
+    row_l[tid] = static_cast<int>((t0 + tid) - static_cast<int64_t>(row_b[tid]) * a.L);
   }
   __syncthreads();
+  auto angles = [&] {
+    for (int x = tid; x < nt * a.half; x += kRopeThreads) {
+      const int t = x / a.half;
+      cs[t][x - t * a.half] = rope_cos_sin(a, row_b[t], row_l[t], x - t * a.half);
+    }
+    __syncthreads();
+  };
 
   if constexpr (MODE == kRopeHalfAny) {
     // 8 elements per lane; a warp holds 256 / D heads' rows
+    angles();
     constexpr int kLanes = D / 8;
     const int warp_rows = 32 / kLanes;
     __nv_bfloat16* mine = rows + (tid / 32) * 256;
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       int t = 0;
       if (r < n_rows) {
         t = r / a.H;
-        rope_row(a, t0 + t, r - t * a.H, src, dst);
+        rope_row(a, row_b[t], row_l[t], r - t * a.H, src, dst);
         *reinterpret_cast<uint4*>(mine + sub * D + c * 8) =
             *reinterpret_cast<const uint4*>(src + c * 8);
       }
@@ -142,16 +149,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     }
   } else {
     constexpr int kItems = D / 16;  // per head
-    constexpr int kFlight = 4;
     const int per_token = a.H * kItems;
     const int n_items = nt * per_token;
     const int turned = a.half / 8;  // kRopeHalf: items of a head that turn
-    for (int base = tid; base < n_items; base += kFlight * kRopeThreads) {
-      uint4 xa[kFlight], xb[kFlight];
-      __nv_bfloat16* pa[kFlight];
-      int tk[kFlight], off_b[kFlight], ci[kFlight];
+    for (int base = tid; base - tid < n_items; base += kRopeFlight * kRopeThreads) {
+      uint4 xa[kRopeFlight], xb[kRopeFlight];
+      __nv_bfloat16* pa[kRopeFlight];
+      int tk[kRopeFlight], off_b[kRopeFlight], ci[kRopeFlight];
 #pragma unroll
-      for (int f = 0; f < kFlight; ++f) {
+      for (int f = 0; f < kRopeFlight; ++f) {
         const int it = base + f * kRopeThreads;
         pa[f] = nullptr;
         if (it < n_items) {
@@ -171,17 +177,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
           }
           const __nv_bfloat16* src;
           __nv_bfloat16* dst;
-          rope_row(a, t0 + t, h, src, dst);
-          xa[f] = *reinterpret_cast<const uint4*>(src + ea);
-          xb[f] = *reinterpret_cast<const uint4*>(src + eb);
+          rope_row(a, row_b[t], row_l[t], h, src, dst);
+          xa[f] = __ldcs(reinterpret_cast<const uint4*>(src + ea));
+          xb[f] = __ldcs(reinterpret_cast<const uint4*>(src + eb));
           pa[f] = dst + ea;
           off_b[f] = eb - ea;
           tk[f] = t;
           ci[f] = c;
         }
       }
+      if (base == tid) angles();  // under the first batch's loads
 #pragma unroll
-      for (int f = 0; f < kFlight; ++f) {
+      for (int f = 0; f < kRopeFlight; ++f) {
         if (!pa[f]) continue;
         uint32_t* wa = reinterpret_cast<uint32_t*>(&xa[f]);
         uint32_t* wb = reinterpret_cast<uint32_t*>(&xb[f]);
@@ -208,8 +215,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
             wb[e] = pack_bf16x2(x2.x, x2.y);
           }
         }
-        *reinterpret_cast<uint4*>(pa[f]) = xa[f];
-        *reinterpret_cast<uint4*>(pa[f] + off_b[f]) = xb[f];
+        __stcs(reinterpret_cast<uint4*>(pa[f]), xa[f]);
+        __stcs(reinterpret_cast<uint4*>(pa[f] + off_b[f]), xb[f]);
       }
     }
   }

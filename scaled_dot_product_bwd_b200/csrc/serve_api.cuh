@@ -218,8 +218,10 @@ sdpa_status_t sdpa_rope(const sdpa_rope_desc* r, const void* q, const void* k, v
   a.sign = r->inverse ? -1.f : 1.f;
   const int sms = sm_count();
   if (sms <= 0) return SDPA_ERR_CUDA;
-  // one token per CTA until every SM has its CTAs, then four share a CTA
-  a.per_cta = a.tokens <= 8ll * sms ? 1 : kRopeTokens;
+  // as many tokens per CTA as make one batch of loads, one where that would
+  // leave SMs without work
+  const int fill = kRopeFlight * kRopeThreads / (a.H * static_cast<int>(r->d) / 16);
+  a.per_cta = a.tokens <= 8ll * sms ? 1 : std::max(1, std::min(kRopeTokens, fill));
   const int mode = r->interleaved ? kRopeInterleaved : (a.half % 8 == 0 ? kRopeHalf : kRopeHalfAny);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e = r->d == 128 ? launch_rope<128>(a, mode, cs) : launch_rope<64>(a, mode, cs);
@@ -284,18 +286,15 @@ sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const
   a.kv_t = kv_t;
   a.kv_h = kv_h;
   a.slots = slots;
-  const int64_t rows_per_cta = kAppendThreads / (cache->d / 8) * kAppendRows;
-  const int64_t grid = (T * a.c.Hkv + rows_per_cta - 1) / rows_per_cta;
-  if (grid >= (1ll << 31)) return SDPA_ERR_UNSUPPORTED;
-  const dim3 g(static_cast<unsigned>(grid), 2);
+  const dim3 g(static_cast<unsigned>((T + kCacheRows - 1) / kCacheRows), 2);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
   if (cache->d == 128) {
-    if (e4m3) cache_append_kernel<128, kCacheE4m3><<<g, kAppendThreads, 0, cs>>>(a);
-    else cache_append_kernel<128, kCacheBf16><<<g, kAppendThreads, 0, cs>>>(a);
+    if (e4m3) cache_append_kernel<128, kCacheE4m3><<<g, kCacheThreads, 0, cs>>>(a);
+    else cache_append_kernel<128, kCacheBf16><<<g, kCacheThreads, 0, cs>>>(a);
   } else {
-    if (e4m3) cache_append_kernel<64, kCacheE4m3><<<g, kAppendThreads, 0, cs>>>(a);
-    else cache_append_kernel<64, kCacheBf16><<<g, kAppendThreads, 0, cs>>>(a);
+    if (e4m3) cache_append_kernel<64, kCacheE4m3><<<g, kCacheThreads, 0, cs>>>(a);
+    else cache_append_kernel<64, kCacheBf16><<<g, kCacheThreads, 0, cs>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
@@ -324,15 +323,15 @@ sdpa_status_t sdpa_cache_gather(const sdpa_kv_cache* cache, int64_t B, const int
   a.v = static_cast<__nv_bfloat16*>(v);
   a.kv_t = kv_t;
   a.kv_h = kv_h;
-  const dim3 g(static_cast<unsigned>((total + kGatherRows - 1) / kGatherRows), 2);
+  const dim3 g(static_cast<unsigned>((total + kCacheRows - 1) / kCacheRows), 2);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
   if (cache->d == 128) {
-    if (e4m3) cache_gather_kernel<128, kCacheE4m3><<<g, kGatherThreads, 0, cs>>>(a);
-    else cache_gather_kernel<128, kCacheBf16><<<g, kGatherThreads, 0, cs>>>(a);
+    if (e4m3) cache_gather_kernel<128, kCacheE4m3><<<g, kCacheThreads, 0, cs>>>(a);
+    else cache_gather_kernel<128, kCacheBf16><<<g, kCacheThreads, 0, cs>>>(a);
   } else {
-    if (e4m3) cache_gather_kernel<64, kCacheE4m3><<<g, kGatherThreads, 0, cs>>>(a);
-    else cache_gather_kernel<64, kCacheBf16><<<g, kGatherThreads, 0, cs>>>(a);
+    if (e4m3) cache_gather_kernel<64, kCacheE4m3><<<g, kCacheThreads, 0, cs>>>(a);
+    else cache_gather_kernel<64, kCacheBf16><<<g, kCacheThreads, 0, cs>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
