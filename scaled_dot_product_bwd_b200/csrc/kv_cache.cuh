@@ -77,14 +77,15 @@ struct AppendArgs {
   const __nv_bfloat16* v;
   int64_t T, kv_t, kv_h;
   const int64_t* slots;
+  int rows;  // per CTA, <= kCacheRows
 };
 
-// Both kernels: a CTA takes kCacheRows rows of K (blockIdx.y = 0) or V with all
+// Both kernels: a CTA takes `rows` rows of K (blockIdx.y = 0) or V with all
 // heads.  Its first threads find where each row lies in the cache; then a
 // thread keeps one 16-byte piece of one head (several when the heads are
 // many) and goes through the rows, four in flight.
 constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 16;
+constexpr int kCacheRows = 64;  // at most
 
 struct CacheCells {
   int64_t off[kCacheRows];    // of the row in the cache, elements; < 0: none
@@ -104,8 +105,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const Appen
   constexpr int kFlight = 4;
   __shared__ CacheCells cells;
   const bool is_v = blockIdx.y != 0;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kCacheRows;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kCacheRows), a.T - t0));
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.T - t0));
   if (threadIdx.x < rows) {
     const int64_t slot = a.slots[t0 + threadIdx.x];
     int64_t page = -1;
@@ -187,6 +188,7 @@ struct GatherArgs {
   __nv_bfloat16* k;
   __nv_bfloat16* v;
   int64_t kv_t, kv_h;
+  int rows;
 };
 
 // The first threads find their row's sequence (binary search in cu_seqlens)
@@ -198,8 +200,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_gather_kernel(const Gathe
   constexpr int kFlight = 4;
   __shared__ CacheCells cells;
   const bool is_v = blockIdx.y != 0;
-  const int64_t r00 = static_cast<int64_t>(blockIdx.x) * kCacheRows;
-  if (threadIdx.x < kCacheRows) {
+  const int64_t r00 = static_cast<int64_t>(blockIdx.x) * a.rows;
+  if (threadIdx.x < a.rows) {
     const int64_t r = r00 + threadIdx.x;
     int64_t page = -1, pos = 0;
     if (r < a.total && r < a.cu[a.B]) {
@@ -226,14 +228,14 @@ __global__ void __launch_bounds__(kCacheThreads) cache_gather_kernel(const Gathe
   if (sub >= down) return;
   __nv_bfloat16* dst0 = (is_v ? a.v : a.k) + r00 * a.kv_t;
   for (int h = group - sub * across; h < a.c.Hkv; h += across) {
-    for (int r0 = sub; r0 < kCacheRows; r0 += down * kFlight) {
+    for (int r0 = sub; r0 < a.rows; r0 += down * kFlight) {
       uint4 x[kFlight];
       uint32_t e[kFlight];
       bool has[kFlight];
 #pragma unroll
       for (int f = 0; f < kFlight; ++f) {
         const int r = r0 + f * down;
-        const int64_t off = r < kCacheRows ? cells.off[r] : -1;
+        const int64_t off = r < a.rows ? cells.off[r] : -1;
         has[f] = off >= 0;
         if (!has[f]) continue;
         if (FMT == kCacheBf16) {

@@ -84,7 +84,7 @@ __device__ __forceinline__ void rope_row(const RopeArgs& a, int b, int l, int h,
 // call may be in place).  A CTA's tokens are chosen so that its items are one
 // batch of four per thread: they are on their way while the angles are formed.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a) {
   __shared__ __align__(16) float2 cs[kRopeTokens][D / 2];
   __shared__ __align__(16) __nv_bfloat16 rows[MODE == kRopeHalfAny ? kRopeThreads * 8 : 8];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.per_cta;
@@ -99,7 +99,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   auto angles = [&] {
     for (int x = tid; x < nt * a.half; x += kRopeThreads) {
       const int t = x / a.half;
-      cs[t][x - t * a.half] = rope_cos_sin(a, row_b[t], row_l[t], x - t * a.half);
+      const int i = x - t * a.half;
+      // kRopeHalf: pairs i, i + 1 of item c (8 c + 2 e, + 1) at place e of the
+      // items' rows, so that neighbouring items' threads read neighbouring words
+      const int at = MODE == kRopeHalf ? ((i & 7) >> 1) * (D / 8) + (i >> 3) * 2 + (i & 1) : i;
+      cs[t][at] = rope_cos_sin(a, row_b[t], row_l[t], i);
     }
     __syncthreads();
   };
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float2 x1 = bf16x2_floats(wa[e]), x2 = bf16x2_floats(wb[e]);
-            const float4 t4 = *reinterpret_cast<const float4*>(row + ci[f] * 8 + 2 * e);
+            const float4 t4 = *reinterpret_cast<const float4*>(row + e * (D / 8) + ci[f] * 2);
             rope_turn(make_float2(t4.x, t4.y), x1.x, x2.x);
             rope_turn(make_float2(t4.z, t4.w), x1.y, x2.y);
             wa[e] = pack_bf16x2(x1.x, x1.y);

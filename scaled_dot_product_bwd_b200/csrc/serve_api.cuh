@@ -64,6 +64,17 @@ sdpa_status_t check_cache(const sdpa_kv_cache* c, CacheView& v) {
   return SDPA_OK;
 }
 
+// Rows per CTA of the cache kernels: few where that spreads a short call over
+// the SMs, up to kCacheRows where each CTA's search for its rows is to be paid
+// for by as much copying as possible (four CTAs per SM and of K and V stay).
+int cache_rows(int64_t total) {
+  const int sms = sm_count();
+  if (sms <= 0) return 0;
+  int rows = 2;
+  while (rows < kCacheRows && total >= 2ll * rows * 4 * sms) rows *= 2;
+  return rows;
+}
+
 // 4-D map of a cache tensor along (head_dim, row, head, page): boxes of
 // box_rows rows of one head of one page, 128 bytes (or a whole 64-byte row)
 // wide, swizzled as wide as they are.  A page past the last reads as zeros.
@@ -286,7 +297,9 @@ sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const
   a.kv_t = kv_t;
   a.kv_h = kv_h;
   a.slots = slots;
-  const dim3 g(static_cast<unsigned>((T + kCacheRows - 1) / kCacheRows), 2);
+  a.rows = cache_rows(T);
+  if (!a.rows) return SDPA_ERR_CUDA;
+  const dim3 g(static_cast<unsigned>((T + a.rows - 1) / a.rows), 2);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
   if (cache->d == 128) {
@@ -323,7 +336,9 @@ sdpa_status_t sdpa_cache_gather(const sdpa_kv_cache* cache, int64_t B, const int
   a.v = static_cast<__nv_bfloat16*>(v);
   a.kv_t = kv_t;
   a.kv_h = kv_h;
-  const dim3 g(static_cast<unsigned>((total + kCacheRows - 1) / kCacheRows), 2);
+  a.rows = cache_rows(total);
+  if (!a.rows) return SDPA_ERR_CUDA;
+  const dim3 g(static_cast<unsigned>((total + a.rows - 1) / a.rows), 2);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
   if (cache->d == 128) {
