@@ -480,7 +480,10 @@ sdpa_status_t sdpa_spec_verify(const sdpa_verify* s, int32_t* path, int32_t* acc
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, spec_verify_kernel, a) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+  const bool held = s->V <= static_cast<int64_t>(cluster) * kVerifyThreads * kVerifyHeld;
+  const cudaError_t e = held ? cudaLaunchKernelEx(&cfg, spec_verify_kernel<true>, a)
+                             : cudaLaunchKernelEx(&cfg, spec_verify_kernel<false>, a);
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
 }  // extern "C"

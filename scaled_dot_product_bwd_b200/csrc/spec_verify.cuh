@@ -9,8 +9,7 @@
 //
 // Everything a first child's test needs is two numbers per node, read for
 // all nodes at once; only a rejection (and the final draw) takes a pass over
-// the vocabulary, and it recomputes w from p, q and the earlier sums Z instead
-// of storing it.  A typical sequence therefore reads one row pair, 8 V bytes,
+// the vocabulary.  A typical sequence therefore reads one row pair, 8 V bytes,
 // and the call is bound by latency: its chain of dependent loads, one cluster
 // exchange per pass and the final search.  A cluster of CTAs shares a
 // sequence's passes, so one sequence is not left to one SM's loads, and the
@@ -43,15 +42,18 @@ constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyMaxNodes = 64;
 constexpr int kVerifyMaxCluster = 8;
+constexpr int kVerifyHeld = 8;  // entries of a CTA's piece that a thread keeps in registers
+
+// max(w - q, 0) with w = t * inv (t itself for the first rejection, w = p)
+__device__ __forceinline__ double verify_left(double w, float q) {
+  return fmax(w - static_cast<double>(q), 0.0);
+}
 
 // What m rejections leave of x: t_m = max(w_{m-1} - q, 0), unnormalised, with
 // w_j = t_j * inv[j]; m = 0: p itself.
 __device__ __forceinline__ double verify_weight(float p, float q, int m, const double* inv) {
   double t = p;
-  for (int j = 1; j <= m; ++j) {
-    if (j > 1) t *= inv[j - 1];
-    t = fmax(t - static_cast<double>(q), 0.0);
-  }
+  for (int j = 1; j <= m; ++j) t = verify_left(j > 1 ? t * inv[j - 1] : t, q);
   return t;
 }
 
@@ -62,7 +64,11 @@ __device__ __forceinline__ double warp_sum(double x) {
 }
 
 // The cluster's CTAs hold equal consecutive pieces of the vocabulary, a CTA's
-// warps equal consecutive pieces of its own.
+// warps equal consecutive pieces of its own.  HELD: a warp's piece fits its
+// threads' registers (kVerifyHeld entries each), so a node's p and q are read
+// once for all its rejections; else every pass reads them again and computes
+// the weights from the earlier sums.
+template <bool HELD>
 __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const VerifyArgs a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -75,8 +81,8 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
   __shared__ unsigned int first_ok[2];                  // bit n: n passes against w = p
   __shared__ float px[kVerifyMaxNodes], qx[kVerifyMaxNodes], ux[kVerifyMaxNodes];
   __shared__ double inv[kVerifyMaxNodes + 1];
-  __shared__ double warp_tot[kVerifyWarps];
-  __shared__ double cta_tot[2][kVerifyMaxCluster];      // written by every CTA of the cluster
+  // every warp's sum of the cluster, by two passes in turn
+  __shared__ double sums[2][kVerifyMaxCluster * kVerifyWarps];
 
   if (tid < kVerifyMaxNodes) kids[tid] = 0;
   __syncthreads();
@@ -85,9 +91,10 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
     if (tid > 0 && tid < a.N) {
       const int64_t at = static_cast<int64_t>(b) * a.N + tid;
       const int parent = a.parents ? a.parents[at] : tid - 1;
+      const int x = a.tokens[at];
+      const float u = a.u_accept[at];
       if (parent >= tid) atomicOr(&g_device_status, kStatusBadSeqlens);
       if (parent >= 0 && parent < tid) {
-        const int x = a.tokens[at];
         float p = 0.f, q = 0.f;
         if (x >= 0 && x < a.V) {
           p = a.target[b * a.t_b + parent * a.t_n + x];
@@ -95,7 +102,6 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
         } else {
           atomicOr(&g_device_status, kStatusBadSeqlens);
         }
-        const float u = a.u_accept[at];
         px[tid] = p;
         qx[tid] = q;
         ux[tid] = u;
@@ -117,39 +123,57 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
   const int hi = min(cta_hi, lo + seg);
   int passes = 0;
 
-  // Sum over the vocabulary of what m rejections leave of target[at]: the
-  // total, with this CTA's warp sums in warp_tot and every CTA's in cta_tot.
+  // HELD: entry lo + lane + 32 i of target[at] (then of what is left of it)
+  // and of draft[at]
+  double held[HELD ? kVerifyHeld : 1];
+  float drawn[HELD ? kVerifyHeld : 1];
+
+  // Sum over the vocabulary of what m rejections leave of target[at].
   auto sum_pass = [&](int at, int m) -> double {
     const float* p = a.target + b * a.t_b + at * a.t_n;
     const float* q = m ? a.draft + b * a.d_b + at * a.d_n : p;
     double acc = 0.0;
-    for (int x0 = lo + lane; x0 < hi; x0 += 32 * 8) {
-      float pv[8], qv[8];
+    if constexpr (HELD) {
+      if (m <= 1) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int x = x0 + 32 * i;
-        pv[i] = x < hi ? p[x] : 0.f;
-        qv[i] = m && x < hi ? q[x] : 0.f;
+        for (int i = 0; i < kVerifyHeld; ++i) {
+          const int x = lo + lane + 32 * i;
+          drawn[i] = m && x < hi ? q[x] : 0.f;
+          held[i] = x < hi ? static_cast<double>(p[x]) : 0.0;
+        }
       }
+      const double f = m > 1 ? inv[m - 1] : 1.0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc += verify_weight(pv[i], qv[i], m, inv);
+      for (int i = 0; i < kVerifyHeld; ++i) {
+        if (m > 0) held[i] = verify_left(held[i] * f, drawn[i]);
+        acc += held[i];
+      }
+    } else {
+      for (int x0 = lo + lane; x0 < hi; x0 += 32 * 8) {
+        float pv[8], qv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x = x0 + 32 * i;
+          pv[i] = x < hi ? p[x] : 0.f;
+          qv[i] = m && x < hi ? q[x] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc += verify_weight(pv[i], qv[i], m, inv);
+      }
     }
     acc = warp_sum(acc);
-    __syncthreads();  // earlier readers of warp_tot
-    if (lane == 0) warp_tot[warp] = acc;
-    __syncthreads();
-    double (*tot)[kVerifyMaxCluster] = cta_tot;
-    if (tid < C) {
-      double mine = 0.0;
-      for (int w = 0; w < kVerifyWarps; ++w) mine += warp_tot[w];
-      double* there = cluster.map_shared_rank(&tot[passes & 1][rank], tid);
-      *there = mine;
-    }
+    double* mine = sums[passes & 1];
+    if (lane < C) *cluster.map_shared_rank(mine + rank * kVerifyWarps + warp, lane) = acc;
     cluster.sync();
+    // all warps of the cluster add the same numbers in the same order
     double total = 0.0;
-    for (int r = 0; r < C; ++r) total += tot[passes & 1][r];
+#pragma unroll
+    for (int i = 0; i < kVerifyMaxCluster * kVerifyWarps / 32; ++i) {
+      const int k = lane + 32 * i;
+      if (k < C * kVerifyWarps) total += mine[k];
+    }
     ++passes;
-    return total;
+    return warp_sum(total);
   };
 
   // every thread of the cluster walks alike
@@ -174,9 +198,8 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
       ++n_acc;
       if (rank == 0 && tid == 0) a.path[static_cast<int64_t>(b) * a.N + n_acc] = n;
     } else {
-      total = sum_pass(at, m + 1);
-      ++m;
-      __syncthreads();
+      total = sum_pass(at, ++m);
+      // (inv[m] was last read before the pass's barrier)
       if (tid == 0) inv[m] = total > 0.0 ? 1.0 / total : 0.0;
       __syncthreads();
     }
@@ -189,57 +212,53 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
     if (tid == 0) a.accepted[b] = n_acc;
   }
 
-  // the piece in which the cumulative weight first exceeds u * total; where
-  // rounding (or u = 1) leaves none, the last piece with any weight
+  // the warp piece in which the cumulative weight first exceeds u * total;
+  // where rounding (or u = 1) leaves none, the last piece with any weight.
+  // Every warp scans all pieces' sums, four neighbours to a lane.
   const double aim = static_cast<double>(a.u_sample[b]) * total;
-  const double* tot = cta_tot[(passes - 1) & 1];
-  int pick = -1, last = -1;
-  double base = 0.0, base_last = 0.0, run = 0.0;
-  for (int r = 0; r < C; ++r) {
-    if (tot[r] > 0.0) {
-      last = r;
-      base_last = run;
-      if (pick < 0 && run + tot[r] > aim) {
-        pick = r;
-        base = run;
+  const double* last_sums = sums[(passes - 1) & 1];
+  constexpr int kPer = kVerifyMaxCluster * kVerifyWarps / 32;
+  double part[kPer], mine = 0.0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = lane * kPer + i;
+    part[i] = k < C * kVerifyWarps ? last_sums[k] : 0.0;
+    mine += part[i];
+  }
+  double before = mine;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const double y = __shfl_up_sync(~0u, before, s);
+    if (lane >= s) before += y;
+  }
+  before -= mine;
+  int pick = -1, last = -1;       // pieces of this lane
+  double base = 0.0, base_last = 0.0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (part[i] > 0.0) {
+      last = lane * kPer + i;
+      base_last = before;
+      if (pick < 0 && before + part[i] > aim) {
+        pick = last;
+        base = before;
       }
     }
-    run += tot[r];
+    before += part[i];
   }
-  if (pick < 0) {
-    pick = last;
-    base = base_last;
-  }
-  if (pick < 0) {
+  const unsigned int picks = __ballot_sync(~0u, pick >= 0), lasts = __ballot_sync(~0u, last >= 0);
+  if (!lasts) {  // no weight anywhere
     if (rank == 0 && tid == 0) a.next_token[b] = 0;
     return;
   }
-  if (rank != pick) return;
-  int wpick = -1, wlast = -1;
-  double wbase = base, wbase_last = base;
-  run = base;
-  for (int w = 0; w < kVerifyWarps; ++w) {
-    if (warp_tot[w] > 0.0) {
-      wlast = w;
-      wbase_last = run;
-      if (wpick < 0 && run + warp_tot[w] > aim) {
-        wpick = w;
-        wbase = run;
-      }
-    }
-    run += warp_tot[w];
-  }
-  if (wpick < 0) {
-    wpick = wlast;
-    wbase = wbase_last;
-  }
-  if (warp != wpick) return;
+  const int from = picks ? __ffs(picks) - 1 : 31 - __clz(lasts);
+  const int piece = __shfl_sync(~0u, picks ? pick : last, from);
+  double run = __shfl_sync(~0u, picks ? base : base_last, from);
+  if (piece != rank * kVerifyWarps + warp) return;
   const float* p = a.target + b * a.t_b + at * a.t_n;
   const float* q = m ? a.draft + b * a.d_b + at * a.d_n : p;
   int token = -1, seen = 0;
-  for (int x0 = lo; x0 < hi && token < 0; x0 += 32) {
-    const int x = x0 + lane;
-    const double w = x < hi ? verify_weight(p[x], m ? q[x] : 0.f, m, inv) : 0.0;
+  auto search = [&](int x0, double w) {
     double cum = w;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -247,10 +266,20 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
       if (lane >= s) cum += y;
     }
     const unsigned int some = __ballot_sync(~0u, w > 0.0);
-    const unsigned int over = __ballot_sync(~0u, w > 0.0 && wbase + cum > aim);
+    const unsigned int over = __ballot_sync(~0u, w > 0.0 && run + cum > aim);
     if (some) seen = x0 + 31 - __clz(some);
     if (over) token = x0 + __ffs(over) - 1;
-    wbase += __shfl_sync(~0u, cum, 31);
+    run += __shfl_sync(~0u, cum, 31);
+  };
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kVerifyHeld; ++i)
+      if (token < 0) search(lo + 32 * i, held[i]);
+  } else {
+    for (int x0 = lo; x0 < hi && token < 0; x0 += 32) {
+      const int x = x0 + lane;
+      search(x0, x < hi ? verify_weight(p[x], m ? q[x] : 0.f, m, inv) : 0.0);
+    }
   }
   if (lane == 0) a.next_token[b] = token >= 0 ? token : seen;
 }
