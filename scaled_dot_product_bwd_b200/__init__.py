@@ -1,8 +1,9 @@
 """Fused scaled-dot-product attention (forward + deterministic backward) for
 NVIDIA B200 (sm_100a): hand-written tcgen05 / TMA kernels behind a C ABI
-(include/sdpa.h), with this package as its thin Python binding.
+(include/sdpa.h), with this package as its thin Python binding, and the serving
+entry points (include/sdpa_serve.h) beside it.
 
-The shared library is loaded on first use; importing the package does not
+The shared libraries are loaded on first use; importing the package does not
 touch the GPU.
 """
 from .binding import (  # noqa: F401
@@ -19,8 +20,6 @@ from .binding import (  # noqa: F401
     sdpa_bwd_noalloc,
     sdpa_bwd_varlen,
     sdpa_bwd_workspace_size,
-    sdpa_cache_append,
-    sdpa_cache_gather,
     sdpa_debug_wait_timeout,
     sdpa_exp2_fma,
     sdpa_fire_backward,
@@ -28,12 +27,18 @@ from .binding import (  # noqa: F401
     sdpa_fwd,
     sdpa_fwd_varlen,
     sdpa_read_device_status,
-    sdpa_rope,
-    sdpa_rope_frequencies,
     sdpa_set_wait_limit_ns,
-    sdpa_spec_verify,
     sdpa_status_string,
     sdpa_t5_bucket,
+)
+from .serve import (  # noqa: F401
+    SERVE_EXPORTED,
+    load_serve_library,
+    sdpa_cache_append,
+    sdpa_cache_gather,
+    sdpa_rope,
+    sdpa_rope_frequencies,
+    sdpa_spec_verify,
     sdpa_tree_fwd,
     sdpa_tree_fwd_workspace_size,
 )

@@ -31,12 +31,7 @@ EXPORTED = ("sdpa_fwd", "sdpa_fwd_varlen", "sdpa_bwd", "sdpa_bwd_phases", "sdpa_
             "sdpa_bwd_bias_grad", "sdpa_bwd_bias_grad_workspace_size", "sdpa_t5_bucket",
             "sdpa_exp2_fma", "sdpa_read_device_status", "sdpa_set_wait_limit_ns",
             "sdpa_debug_wait_timeout", "sdpa_status_string", "sdpa_fire_table",
-            "sdpa_fire_backward_workspace_size", "sdpa_fire_backward", "sdpa_rope",
-            "sdpa_rope_frequencies", "sdpa_cache_append", "sdpa_cache_gather", "sdpa_tree_fwd",
-            "sdpa_tree_fwd_workspace_size", "sdpa_spec_verify")
-
-CACHE_BF16, CACHE_E4M3 = 0, 1
-ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+            "sdpa_fire_backward_workspace_size", "sdpa_fire_backward")
 
 
 class SdpaError(RuntimeError):
@@ -73,39 +68,6 @@ class Varlen(ctypes.Structure):
     _fields_ = [("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
                 ("max_seqlen_q", ctypes.c_int64), ("max_seqlen_k", ctypes.c_int64),
                 ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64)]
-
-
-class RopeDesc(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_int64) for n in
-                 ("B", "L", "Hq", "Hkv", "d", "q_b", "q_l", "q_h", "k_b", "k_l", "k_h",
-                  "qo_b", "qo_l", "qo_h", "ko_b", "ko_l", "ko_h")]
-                + [("positions", ctypes.c_void_p), ("pos_b", ctypes.c_int64),
-                   ("offset", ctypes.c_int64), ("freqs", ctypes.c_void_p),
-                   ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                   ("inverse", ctypes.c_int32), ("amplitude", ctypes.c_float)])
-
-
-class KvCache(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
-                + [("format", ctypes.c_int32)]
-                + [(n, ctypes.c_int64) for n in
-                   ("num_pages", "page_size", "Hkv", "d", "stride_page", "stride_head",
-                    "stride_row", "scale_stride_page", "scale_stride_head")])
-
-
-class Tree(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "T", "max_nodes", "Hq", "q_t", "q_h", "o_t",
-                                               "o_h")]
-                + [(n, ctypes.c_void_p) for n in ("cu_nodes", "ctx_lens", "page_table")]
-                + [("table_width", ctypes.c_int64), ("table_b", ctypes.c_int64),
-                   ("tree_mask", ctypes.c_void_p), ("window_left", ctypes.c_int64)])
-
-
-class Verify(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "N", "V", "target_b", "target_n", "draft_b",
-                                               "draft_n")]
-                + [(n, ctypes.c_void_p) for n in ("target", "draft", "tokens", "parents",
-                                                  "u_accept", "u_sample")])
 
 
 _lib = None
@@ -162,24 +124,6 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sdpa_fire_backward_workspace_size.restype = sz
     lib.sdpa_fire_backward.argtypes = [fp, i64, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.sdpa_fire_backward.restype = i32
-    cp = ctypes.POINTER(KvCache)
-    f64 = ctypes.c_double
-    lib.sdpa_rope.argtypes = [ctypes.POINTER(RopeDesc), vp, vp, vp, vp, vp]
-    lib.sdpa_rope.restype = i32
-    lib.sdpa_rope_frequencies.argtypes = [i32, f64, i32, f64, i64, f64, f64,
-                                          ctypes.POINTER(f64), ctypes.POINTER(f32)]
-    lib.sdpa_rope_frequencies.restype = i32
-    lib.sdpa_cache_append.argtypes = [cp, vp, vp, i64, i64, i64, vp, vp]
-    lib.sdpa_cache_append.restype = i32
-    lib.sdpa_cache_gather.argtypes = [cp, i64, vp, i64, i64, vp, i64, vp, vp, i64, i64, vp]
-    lib.sdpa_cache_gather.restype = i32
-    tp = ctypes.POINTER(Tree)
-    lib.sdpa_tree_fwd.argtypes = [tp, cp, vp, bp, f32, vp, vp, vp, sz, vp]
-    lib.sdpa_tree_fwd.restype = i32
-    lib.sdpa_tree_fwd_workspace_size.argtypes = [tp, cp]
-    lib.sdpa_tree_fwd_workspace_size.restype = sz
-    lib.sdpa_spec_verify.argtypes = [ctypes.POINTER(Verify), vp, vp, vp, vp]
-    lib.sdpa_spec_verify.restype = i32
     lib.sdpa_status_string.argtypes = [i32]
     lib.sdpa_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -546,12 +490,18 @@ def sdpa_exp2_fma(x: torch.Tensor) -> torch.Tensor:
 
 
 def sdpa_read_device_status() -> int:
-    """Synchronise the current stream; return (and clear) the device status code."""
-    return int(load_library().sdpa_read_device_status(_stream()))
+    """Synchronise the current stream; return (and clear) the device status code, of the
+    attention kernels or, where theirs is clear, of the serving ones."""
+    from . import serve
+    status = int(load_library().sdpa_read_device_status(_stream()))
+    serving = serve.read_device_status(_stream())
+    return status or serving
 
 
 def sdpa_set_wait_limit_ns(ns: int):
+    from . import serve
     load_library().sdpa_set_wait_limit_ns(int(ns))
+    serve.load_serve_library().sdpa_serve_set_wait_limit_ns(int(ns))
 
 
 def sdpa_debug_wait_timeout():
@@ -602,301 +552,3 @@ def sdpa_fire_backward(w1, b1, w2, b2, c, threshold, Lq, Lk, d_table):
 
 def sdpa_status_string(status: int) -> str:
     return load_library().sdpa_status_string(int(status)).decode()
-
-
-# ------------------------------------------------------------------- serving
-# These calls sit in a generation loop whose kernels take a few microseconds, so
-# each reads what it needs of a tensor once and passes plain integers.
-_BF16, _E4M3, _F32, _F64 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.float64
-_I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
-
-
-def _device_stream(ref: torch.Tensor, *tensors):
-    """The raw current stream of ref's GPU, which must be the current one and every tensor's."""
-    dev = ref.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev}, which is not the current CUDA device")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors are on {t.device} and on cuda:{dev}")
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _bad(name: str, what: str):
-    raise ValueError(f"{name} must be {what}")
-
-
-def _rows(t: torch.Tensor, name: str, dims: int):
-    """Shape and strides of a bf16 tensor of head rows; the stride of a dimension that is never
-    stepped along is given as 8."""
-    st = t.stride()
-    sh = t.shape
-    if t.dtype != _BF16 or len(sh) != dims or (st[-1] != 1 and sh[-1] != 1):
-        _bad(name, f"bf16 with {dims} dimensions and a contiguous head_dim")
-    if 1 in sh:
-        st = tuple(8 if n == 1 else x for n, x in zip(sh, st))
-    return sh, st
-
-
-def _alike(t: torch.Tensor, name: str, sh, st):
-    if t.dtype != _BF16 or t.shape != sh or (t.stride() != st and _rows(t, name, len(sh))[1] != st):
-        _bad(name, "bf16 with the shape and strides of its partner")
-
-
-def sdpa_rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, original_length=0,
-                          beta_fast=32.0, beta_slow=1.0, device="cuda"):
-    """(freqs float64 [rot / 2] on ``device``, amplitude) for sdpa_rope: radians per position,
-    unscaled or scaled for longer contexts ("linear", "ntk", "yarn"; see include/sdpa.h)."""
-    if scaling not in ROPE_SCALINGS:
-        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
-    out = (ctypes.c_double * max(int(rot) // 2, 1))()
-    amplitude = ctypes.c_float()
-    _check(load_library().sdpa_rope_frequencies(int(rot), float(base), ROPE_SCALINGS[scaling],
-                                                float(factor), int(original_length),
-                                                float(beta_fast), float(beta_slow), out,
-                                                ctypes.byref(amplitude)), "sdpa_rope_frequencies")
-    return torch.tensor(list(out), dtype=_F64, device=device), amplitude.value
-
-
-def sdpa_rope(q, k, freqs, positions=None, *, offset=0, interleaved=False, inverse=False,
-              amplitude=1.0, out_q=None, out_k=None):
-    """q and k turned by their positions (see sdpa_rope in include/sdpa.h): (out_q, out_k).
-
-    q [B, L, Hq, d] and k [B, L, Hkv, d], or packed [T, Hq, d] and [T, Hkv, d]; k may be None.
-    ``positions`` int32 [B, L] (or [T]); without it row l has position ``offset`` + l.
-    ``inverse`` turns back: the gradient.  out_q=q, out_k=k works in place.
-    """
-    lib = load_library()
-    dims = q.dim()
-    if dims != 3 and dims != 4:
-        _bad("q", "[B, L, Hq, d] or [T, Hq, d]")
-    stream = _device_stream(q, k, freqs, positions, out_q, out_k)
-    qs, qst = _rows(q, "q", dims)
-    d, Hq, L = qs[-1], qs[-2], qs[-3]
-    B, zero = (qs[0], ()) if dims == 4 else (1, (8,))
-    if freqs.dtype != _F64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        _bad("freqs", "a contiguous float64 vector")
-    pos, pos_b = None, L
-    if positions is not None:
-        if positions.dtype != _I32 or positions.shape != qs[:-2]:
-            _bad("positions", "int32 [B, L] (packed: [T])")
-        pst = positions.stride()
-        if L > 1 and pst[-1] != 1:
-            _bad("positions", "contiguous along the sequence")
-        pos, pos_b = positions.data_ptr(), (pst[0] if B > 1 else L)
-    if out_q is None:
-        out_q = torch.empty(qs, device=q.device, dtype=_BF16)
-    ost = _rows(out_q, "out_q", dims)[1]
-    if out_q.shape != qs:
-        _bad("out_q", f"{tuple(qs)}")
-    if k is not None:
-        ks, kst = _rows(k, "k", dims)
-        if ks[:-2] != qs[:-2] or ks[-1] != d:
-            raise ValueError(f"k shape {tuple(ks)} does not match q {tuple(qs)}")
-        if out_k is None:
-            out_k = torch.empty(ks, device=q.device, dtype=_BF16)
-        okst = _rows(out_k, "out_k", dims)[1]
-        if out_k.shape != ks:
-            _bad("out_k", f"{tuple(ks)}")
-        Hkv, kp, okp = ks[-2], k.data_ptr(), out_k.data_ptr()
-    else:
-        kst = okst = (0,) * dims
-        Hkv, kp, okp, out_k = 0, None, None, None
-    if B * L == 0:
-        return out_q, out_k
-    r = RopeDesc(B, L, Hq, Hkv, d, *zero, *qst[:-1], *zero, *kst[:-1], *zero, *ost[:-1], *zero,
-                 *okst[:-1], pos, pos_b, offset, freqs.data_ptr(), 2 * freqs.shape[0], interleaved,
-                 inverse, amplitude)
-    st = lib.sdpa_rope(ctypes.byref(r), q.data_ptr(), kp, out_q.data_ptr(), okp, stream)
-    if st:
-        raise SdpaError(st, "sdpa_rope")
-    return out_q, out_k
-
-
-def make_cache(k_cache, v_cache, k_scale=None, v_scale=None) -> KvCache:
-    """Descriptor of a paged cache [num_pages, Hkv, page_size, d]: bf16, or float8_e4m3fn with
-    uint8 scale exponents [num_pages, Hkv, page_size]."""
-    dt, sh, st = k_cache.dtype, k_cache.shape, k_cache.stride()
-    e4m3 = dt == _E4M3
-    if not e4m3 and dt != _BF16:
-        raise ValueError("a cache is bf16 or float8_e4m3fn")
-    if (len(sh) != 4 or v_cache.shape != sh or v_cache.dtype != dt or v_cache.stride() != st
-            or st[3] != 1):
-        raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] alike in "
-                         "type, shape and strides, with a contiguous head_dim")
-    P, H, page, d = sh
-    sp = sh_ = 0
-    kp = vp = None
-    if e4m3:
-        if k_scale is None or v_scale is None:
-            raise ValueError("an e4m3 cache needs k_scale and v_scale")
-        ss = k_scale.stride()
-        if (k_scale.dtype != _U8 or k_scale.shape != sh[:3] or ss[2] != 1 or v_scale.dtype != _U8
-                or v_scale.shape != sh[:3] or v_scale.stride() != ss):
-            raise ValueError("k_scale and v_scale must be uint8 [num_pages, Hkv, page_size] alike "
-                             "in strides, with contiguous rows")
-        sp, sh_ = (ss[0] if P > 1 else 16), (ss[1] if H > 1 else 16)
-        kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("a bf16 cache has no scales")
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, 1 if e4m3 else 0, P, page, H, d,
-                   st[0] if P > 1 else 16, st[1] if H > 1 else 16, st[2] if page > 1 else 16, sp,
-                   sh_)
-
-
-def _table(page_table: torch.Tensor, B: int):
-    sh, st = page_table.shape, page_table.stride()
-    if page_table.dtype != _I32 or len(sh) != 2 or sh[0] != B or (sh[1] > 1 and st[1] != 1):
-        _bad("page_table", "int32 [B, pages] with contiguous rows")
-    return sh[1], (st[0] if B > 1 else sh[1])
-
-
-def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        _bad(name, f"contiguous {str(dtype)[6:]} {list(shape)}")
-    return t.data_ptr()
-
-
-def sdpa_cache_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
-    """Rows k, v [T, Hkv, d] into the cache at slots int64 [T] (page * page_size + row;
-    negative: skipped), quantised if the cache is e4m3 (see sdpa_cache_append)."""
-    lib = load_library()
-    stream = _device_stream(k_cache, v_cache, k_scale, v_scale, k, v, slots)
-    c = make_cache(k_cache, v_cache, k_scale, v_scale)
-    sh, st = _rows(k, "k", 3)
-    _alike(v, "v", sh, st)
-    T, H, d = sh
-    if H != c.Hkv or d != c.d:
-        raise ValueError(f"k {tuple(sh)} does not fit the cache's heads")
-    sp = _vector(slots, "slots", _I64, (T,))
-    r = lib.sdpa_cache_append(ctypes.byref(c), k.data_ptr(), v.data_ptr(), T, st[0], st[1], sp,
-                              stream)
-    if r:
-        raise SdpaError(r, "sdpa_cache_append")
-
-
-def sdpa_cache_gather(k_cache, v_cache, page_table, cu_seqlens, total, k_scale=None, v_scale=None,
-                      k=None, v=None):
-    """The cached sequences as packed bf16 (k, v) [total, Hkv, d], sequence b's first
-    cu_seqlens[b + 1] - cu_seqlens[b] positions at its rows (see sdpa_cache_gather)."""
-    lib = load_library()
-    stream = _device_stream(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, k, v)
-    c = make_cache(k_cache, v_cache, k_scale, v_scale)
-    B = cu_seqlens.numel() - 1
-    cu = _vector(cu_seqlens, "cu_seqlens", _I32, (B + 1,))
-    width, table_b = _table(page_table, B)
-    shape = (int(total), c.Hkv, c.d)
-    if k is None:
-        k = torch.empty(shape, device=k_cache.device, dtype=_BF16)
-    if v is None:
-        v = torch.empty_like(k)
-    sh, st = _rows(k, "k", 3)
-    if sh != shape:
-        _bad("k", f"{list(shape)}")
-    _alike(v, "v", sh, st)
-    r = lib.sdpa_cache_gather(ctypes.byref(c), B, page_table.data_ptr(), width, table_b, cu,
-                              shape[0], k.data_ptr(), v.data_ptr(), st[0], st[1], stream)
-    if r:
-        raise SdpaError(r, "sdpa_cache_gather")
-    return k, v
-
-
-def sdpa_tree_fwd(q, k_cache, v_cache, page_table, ctx_lens, cu_nodes, max_nodes, *,
-                  k_scale=None, v_scale=None, tree_mask=None, window_left=-1, t5_table=None,
-                  t5_num_buckets=32, t5_max_distance=128, t5_bidirectional=True,
-                  alibi_slopes=None, scale=None, out=None, lse=None, workspace=None):
-    """O [T, Hq, d], LSE [Hq, T]: each sequence's nodes over its cached context and over the
-    nodes that ``tree_mask`` (int64 [T], bit j: sees node j; None: a chain) shows them.  One node
-    per sequence is plain decoding.  The nodes' own keys are in the cache already, at positions
-    ctx_lens[b] and on (see sdpa_tree_fwd in include/sdpa.h)."""
-    lib = load_library()
-    stream = _device_stream(k_cache, v_cache, k_scale, v_scale, q, page_table, ctx_lens, cu_nodes,
-                            tree_mask, t5_table, alibi_slopes, out, lse, workspace)
-    c = make_cache(k_cache, v_cache, k_scale, v_scale)
-    sh, qst = _rows(q, "q", 3)
-    T, Hq, d = sh
-    if d != c.d:
-        raise ValueError("q and the cache differ in head_dim")
-    B = ctx_lens.numel()
-    ctx = _vector(ctx_lens, "ctx_lens", _I32, (B,))
-    cu = _vector(cu_nodes, "cu_nodes", _I32, (B + 1,))
-    mask = None if tree_mask is None else _vector(tree_mask, "tree_mask", _I64, (T,))
-    width, table_b = _table(page_table, B)
-    if out is None:
-        out = torch.empty(sh, device=q.device, dtype=_BF16)
-    osh, ost = _rows(out, "out", 3)
-    if osh != sh:
-        _bad("out", "of q's shape")
-    if lse is None:
-        lse = torch.empty(Hq, T, device=q.device, dtype=_F32)
-    lp = _vector(lse, "lse", _F32, (Hq, T))
-    t = Tree(B, T, max_nodes, Hq, qst[0], qst[1], ost[0], ost[1], cu, ctx, page_table.data_ptr(),
-             width, table_b, mask, window_left)
-    bias = None
-    if t5_table is not None or alibi_slopes is not None:
-        bias = ctypes.byref(make_bias(None, t5_table, t5_num_buckets, t5_max_distance,
-                                      t5_bidirectional, (B, Hq, 0, 0), alibi_slopes))
-    tp, cp = ctypes.byref(t), ctypes.byref(c)
-    if workspace is None:
-        workspace = torch.empty(lib.sdpa_tree_fwd_workspace_size(tp, cp), device=q.device,
-                                dtype=_U8)
-    r = lib.sdpa_tree_fwd(tp, cp, q.data_ptr(), bias, d ** -0.5 if scale is None else scale,
-                          out.data_ptr(), lp, workspace.data_ptr(), workspace.nbytes, stream)
-    if r:
-        raise SdpaError(r, "sdpa_tree_fwd")
-    return out, lse
-
-
-def sdpa_tree_fwd_workspace_size(q, k_cache, v_cache, page_table, ctx_lens, cu_nodes, max_nodes, *,
-                                 k_scale=None, v_scale=None) -> int:
-    """Bytes of the workspace of sdpa_tree_fwd for these tensors (0: they do not fit together)."""
-    c = make_cache(k_cache, v_cache, k_scale, v_scale)
-    width, table_b = _table(page_table, ctx_lens.numel())
-    sh, st = _rows(q, "q", 3)
-    t = Tree(ctx_lens.numel(), sh[0], int(max_nodes), sh[1], st[0], st[1], st[0], st[1],
-             cu_nodes.data_ptr(), ctx_lens.data_ptr(), page_table.data_ptr(), width, table_b, None,
-             -1)
-    return int(load_library().sdpa_tree_fwd_workspace_size(ctypes.byref(t), ctypes.byref(c)))
-
-
-def sdpa_spec_verify(target, draft, tokens, parents, u_accept, u_sample):
-    """(path int32 [B, N], accepted int32 [B], next_token int32 [B]) of drafted trees, by
-    rejection sampling with the given uniform numbers (see sdpa_spec_verify in include/sdpa.h).
-
-    target, draft float32 [B, N, V]: the distributions after each node (draft may be None when
-    N = 1); tokens int32 [B, N]; parents int32 [B, N] or None (a chain); u_accept float32 [B, N];
-    u_sample float32 [B].
-    """
-    lib = load_library()
-    stream = _device_stream(target, draft, tokens, parents, u_accept, u_sample)
-    sh, tst = target.shape, target.stride()
-    if target.dtype != _F32 or len(sh) != 3 or (tst[2] != 1 and sh[2] != 1):
-        _bad("target", "float32 [B, N, V] with a contiguous vocabulary")
-    B, N, V = sh
-    dp = xp = pp = up = None
-    dst = (0, 0)
-    if draft is not None:
-        dst = draft.stride()
-        if draft.dtype != _F32 or draft.shape != sh or (dst[2] != 1 and V != 1):
-            _bad("draft", "float32 [B, N, V] with a contiguous vocabulary")
-        dp = draft.data_ptr()
-    if N > 1:
-        if draft is None:
-            raise ValueError("draft distributions are needed when there are drafted nodes")
-        xp = _vector(tokens, "tokens", _I32, (B, N))
-        up = _vector(u_accept, "u_accept", _F32, (B, N))
-        if parents is not None:
-            pp = _vector(parents, "parents", _I32, (B, N))
-    us = _vector(u_sample, "u_sample", _F32, (B,))
-    dev = target.device
-    path = torch.empty(B, N, device=dev, dtype=_I32)
-    accepted = torch.empty(B, device=dev, dtype=_I32)
-    token = torch.empty(B, device=dev, dtype=_I32)
-    s = Verify(B, N, V, tst[0], tst[1], dst[0], dst[1], target.data_ptr(), dp, xp, pp, up, us)
-    r = lib.sdpa_spec_verify(ctypes.byref(s), path.data_ptr(), accepted.data_ptr(),
-                             token.data_ptr(), stream)
-    if r:
-        raise SdpaError(r, "sdpa_spec_verify")
-    return path, accepted, token

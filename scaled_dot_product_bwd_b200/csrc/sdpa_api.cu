@@ -950,5 +950,3 @@ sdpa_status_t sdpa_fire_backward(const sdpa_fire* fire, int64_t Lq, int64_t Lk,
 }
 
 }  // extern "C"
-
-#include "serve_api.cuh"

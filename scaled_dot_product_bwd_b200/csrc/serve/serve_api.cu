@@ -1,15 +1,97 @@
-// serve_api.cuh -- host side of the serving entry points declared in
-// include/sdpa.h: rotary positions, the paged cache, tree attention over it
-// and the verification of drafted tokens.  Part of the library's one
-// translation unit (included by sdpa_api.cu, whose helpers it uses).
-#pragma once
+// serve_api.cu -- host side of the serving entry points declared in
+// include/sdpa_serve.h: argument validation, tensor maps, launches and the
+// library's status word.  A library and translation unit of its own, so that
+// the attention kernels are built from their own sources alone; the few host
+// helpers that both need (tensor-map entry point, T5 thresholds) are repeated.
+#include <cuda.h>
+#include <cuda_runtime.h>
 
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "sdpa_serve.h"
 #include "kv_cache.cuh"
 #include "rope.cuh"
 #include "spec_verify.cuh"
 #include "tree_fwd.cuh"
 
+using namespace sdpa;
+
 namespace {
+
+uint64_t g_wait_limit_ns = 2000000000ull;
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Integer thresholds of the T5 log buckets, evaluated in float64 exactly as
+// the closed form reads: large(n) = max_exact + trunc(ln(n / max_exact) /
+// ln(max_distance / max_exact) * (half - max_exact)).
+bool fill_t5(T5Spec& t, int nb, int md, int bidir) {
+  const int half = bidir ? nb / 2 : nb;
+  const int me = half / 2;
+  if (me < 1 || md <= me) return false;
+  const int K = half - me;
+  if (K > kMaxT5Thresholds) return false;
+  t.half = half;
+  t.max_exact = me;
+  t.bidirectional = bidir ? 1 : 0;
+  t.nthr = K;
+  const double denom = std::log(static_cast<double>(md) / static_cast<double>(me));
+  auto large = [&](int64_t n) -> int64_t {
+    const double v = std::log(static_cast<double>(n) / static_cast<double>(me)) / denom *
+                     static_cast<double>(half - me);
+    return me + static_cast<int64_t>(v);
+  };
+  // thr[k]: the first n whose closed form reaches max_exact + k.  It is found
+  // from its real-valued inverse (a decoding step makes one call, which must
+  // not walk all distances up to max_distance).
+  const int64_t limit = 4 * static_cast<int64_t>(md) + 1024;
+  int64_t n = me;
+  for (int k = 0; k < K; ++k) {
+    const int64_t guess = static_cast<int64_t>(me * std::exp(denom * k / (half - me)));
+    n = std::max(n, std::min(guess, limit));
+    while (n > me && large(n - 1) >= me + k) --n;
+    while (n < limit && large(n) < me + k) ++n;
+    t.thr[k] = (n < limit) ? static_cast<int>(n) : INT_MAX;
+  }
+  for (int k = K; k < kMaxT5Thresholds; ++k) t.thr[k] = INT_MAX;
+  // the capped bucket (half - 1) holds every n >= thr[K - 1]
+  const int sat = t.thr[K - 1];
+  t.one_lo_max = sat == INT_MAX ? INT_MIN : -sat;
+  t.one_hi_min = bidir ? sat : 0;
+  t.log_scale = static_cast<float>(static_cast<double>(half - me) / std::log2(static_cast<double>(md) / me));
+  t.inv_max_exact = static_cast<float>(1.0 / me);
+  return true;
+}
+
+int clamp_window(int64_t w, int64_t L) {
+  if (w < 0) return -1;
+  return static_cast<int>(w > L ? L : w);
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 bool good_stride(int64_t v, int64_t multiple) {
   return v > 0 && v % multiple == 0 && v < (1ll << 38);
@@ -485,5 +567,17 @@ sdpa_status_t sdpa_spec_verify(const sdpa_verify* s, int32_t* path, int32_t* acc
                              : cudaLaunchKernelEx(&cfg, spec_verify_kernel<false>, a);
   return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
+
+sdpa_status_t sdpa_serve_read_device_status(void* stream) {
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SDPA_ERR_CUDA;
+  unsigned int h = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&h, g_device_status, sizeof(h)) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero)) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (h & kStatusTimeout) return SDPA_ERR_TIMEOUT;
+  if (h & (kStatusMisaligned | kStatusBadSeqlens)) return SDPA_ERR_UNSUPPORTED;
+  return SDPA_OK;
+}
+
+void sdpa_serve_set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns = ns < 1000 ? 1000 : ns; }
 
 }  // extern "C"

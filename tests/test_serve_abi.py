@@ -1,15 +1,18 @@
 """Refusals of the serving entry points, on the host before any work is queued
 (no GPU needed), and the host arithmetic of the rotary frequencies."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
 import torch
 
 from oracle import serve_oracle as so
-from scaled_dot_product_bwd_b200 import binding
+from scaled_dot_product_bwd_b200 import binding, serve
 from scaled_dot_product_bwd_b200.build import build
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = ctypes.c_void_p(0x10000)   # aligned, never dereferenced: validation fails first
 NULL = ctypes.c_void_p(0)
 
@@ -17,7 +20,7 @@ NULL = ctypes.c_void_p(0)
 @pytest.fixture(scope="module")
 def lib():
     build()
-    return binding.load_library()
+    return serve.load_serve_library()
 
 
 def _fields(cls, base, kw):
@@ -30,28 +33,46 @@ def _rope(**kw):
                 rot=64, interleaved=0, inverse=0, amplitude=1.0)
     for t, h in (("q", 4), ("k", 2), ("qo", 4), ("ko", 2)):
         base.update({f"{t}_b": 10 * h * 64, f"{t}_l": h * 64, f"{t}_h": 64})
-    return _fields(binding.RopeDesc, base, kw)
+    return _fields(serve.RopeDesc, base, kw)
 
 
 def _cache(**kw):
     base = dict(k=0x10000, v=0x10000, k_scale=0x10000, v_scale=0x10000, format=1, num_pages=10,
                 page_size=64, Hkv=2, d=64, stride_page=2 * 64 * 64, stride_head=64 * 64,
                 stride_row=64, scale_stride_page=128, scale_stride_head=64)
-    return _fields(binding.KvCache, base, kw)
+    return _fields(serve.KvCache, base, kw)
 
 
 def _tree(**kw):
     base = dict(B=2, T=8, max_nodes=4, Hq=4, q_t=256, q_h=64, o_t=256, o_h=64, cu_nodes=0x10000,
                 ctx_lens=0x10000, page_table=0x10000, table_width=5, table_b=5, tree_mask=0x10000,
                 window_left=-1)
-    return _fields(binding.Tree, base, kw)
+    return _fields(serve.Tree, base, kw)
 
 
 def _verify(**kw):
     base = dict(B=2, N=4, V=100, target_b=400, target_n=100, draft_b=400, draft_n=100,
                 target=0x10000, draft=0x10000, tokens=0x10000, parents=0x10000, u_accept=0x10000,
                 u_sample=0x10000)
-    return _fields(binding.Verify, base, kw)
+    return _fields(serve.Verify, base, kw)
+
+
+def test_library_exports_what_the_header_declares(lib):
+    text = open(os.path.join(ROOT, "include", "sdpa_serve.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"\b(sdpa_[a-z0-9_]+)\s*\(", text))
+    assert names == set(serve.SERVE_EXPORTED)
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def test_missing_libraries_fail_loudly(tmp_path, monkeypatch):
+    with pytest.raises(RuntimeError):
+        serve.load_serve_library(str(tmp_path / "missing.so"))
+    monkeypatch.setattr(serve, "_bind", None)
+    monkeypatch.setattr(serve, "BIND_PATH", str(tmp_path / "missing.so"))
+    with pytest.raises(RuntimeError):
+        serve.sdpa_spec_verify(None, None, None, None, None, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -81,7 +102,7 @@ def test_rope_refuses_pointers(lib):
                                 dict(scaling="yarn", factor=2.0, original_length=7, beta_fast=4.0)])
 @pytest.mark.parametrize("rot", [4, 32, 58, 128])
 def test_rope_frequencies(lib, rot, kw):
-    f, amp = binding.sdpa_rope_frequencies(rot, 10000.0, device="cpu", **kw)
+    f, amp = serve.sdpa_rope_frequencies(rot, 10000.0, device="cpu", **kw)
     ref, ref_amp = so.rope_frequencies(rot, 10000.0, **kw)
     assert f.dtype == torch.float64 and np.allclose(f.numpy(), ref, rtol=1e-13, atol=0)
     assert amp == pytest.approx(ref_amp, rel=1e-7)
@@ -95,10 +116,10 @@ def test_rope_frequencies(lib, rot, kw):
 def test_rope_frequencies_refuse(lib, kw):
     kw = dict(kw)
     with pytest.raises(binding.SdpaError) as e:
-        binding.sdpa_rope_frequencies(kw.pop("rot", 64), kw.pop("base", 10000.0), device="cpu", **kw)
+        serve.sdpa_rope_frequencies(kw.pop("rot", 64), kw.pop("base", 10000.0), device="cpu", **kw)
     assert e.value.status == 1
     with pytest.raises(ValueError):
-        binding.sdpa_rope_frequencies(64, scaling="other", device="cpu")
+        serve.sdpa_rope_frequencies(64, scaling="other", device="cpu")
 
 
 BAD_CACHES = [
@@ -192,10 +213,10 @@ def test_binding_refuses_host_tensors():
     q, k = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     cache = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
     i32 = torch.zeros(2, dtype=torch.int32)
-    for call in (lambda: binding.sdpa_rope(q, k, torch.zeros(32, dtype=torch.float64)),
-                 lambda: binding.sdpa_cache_append(k, k, torch.zeros(3, dtype=torch.int64), cache, cache),
-                 lambda: binding.sdpa_cache_gather(cache, cache, i32[:1, None], i32, 3),
-                 lambda: binding.sdpa_tree_fwd(q, cache, cache, i32[:1, None], i32[:1], i32, 4),
-                 lambda: binding.sdpa_spec_verify(torch.zeros(1, 1, 9), None, None, None, None, torch.zeros(1))):
+    for call in (lambda: serve.sdpa_rope(q, k, torch.zeros(32, dtype=torch.float64)),
+                 lambda: serve.sdpa_cache_append(k, k, torch.zeros(3, dtype=torch.int64), cache, cache),
+                 lambda: serve.sdpa_cache_gather(cache, cache, i32[:1, None], i32, 3),
+                 lambda: serve.sdpa_tree_fwd(q, cache, cache, i32[:1, None], i32[:1], i32, 4),
+                 lambda: serve.sdpa_spec_verify(torch.zeros(1, 1, 9), None, None, None, None, torch.zeros(1))):
         with pytest.raises(ValueError):
             call()
