@@ -201,7 +201,7 @@ sdpa_status_t check_tree(const sdpa_tree* t, const sdpa_kv_cache* c, CacheView& 
   if (t->table_width > (1ll << 30) / c->page_size) return SDPA_ERR_UNSUPPORTED;
   const int64_t tiles = (t->table_width * c->page_size + kTreeKeys - 1) / kTreeKeys;
   const int64_t blocks = (t->max_nodes * (t->Hq / c->Hkv) + 15) / 16;
-  if (tiles * blocks >= (1ll << 31) / c->Hkv) return SDPA_ERR_UNSUPPORTED;
+  if ((tiles + 3) * blocks >= (1ll << 31) / c->Hkv) return SDPA_ERR_UNSUPPORTED;  // (3: a piece's cost)
   if (!good_stride(t->q_t, 8) || !good_stride(t->q_h, 8) || !good_stride(t->o_t, 8) ||
       !good_stride(t->o_h, 8))
     return SDPA_ERR_INVALID_ARG;

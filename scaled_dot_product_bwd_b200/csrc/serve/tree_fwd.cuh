@@ -59,10 +59,13 @@ constexpr int kTreeKeys = 128;      // keys per tile
 // warps after the 8 of the softmax
 constexpr int kTreeProducer = 8, kTreeIssueS = 9, kTreeIssueO = 10, kTreeQuery = 11;
 constexpr int kTreeThreads = 12 * 32;
-// A (sequence, head, row block) costs its first CTA about this many tiles more
-// (its queries, first maximum, ragged end and result); the line counts them,
-// so that CTAs with many short ones get fewer tiles.
-constexpr int kTreePieceCost = 3;
+// A (sequence, head, row block) costs its first CTA about three tiles more (its
+// queries, first maximum, ragged end and result).  The line counts them, so
+// that CTAs with many short ones get fewer tiles; where a CTA's share is a few
+// tiles of one piece, every CTA pays once and they count as nothing.
+__device__ __forceinline__ int tree_piece_cost(int64_t tiles, int ctas) {
+  return tiles >= 8ll * ctas ? 3 : 0;
+}
 constexpr int kTreeScaleRing = 8;   // tiles whose e4m3 scales are kept
 // T5: buckets of the distances -kTreeNear .. 63 are tabulated per CTA, and the
 // table's entries of a KV head's query heads per piece where they fit.
@@ -165,9 +168,8 @@ struct TreeLayout {
 struct TreeSeq {
   int row0, n, ctx, keys;  // first query row, nodes, context length, context + nodes
   int tile0, tiles, rb;    // first key tile any node sees, tiles, row blocks
-  // of the line: per (head, row block) the piece cost, then the tiles
-  __device__ __forceinline__ int span() const { return kTreePieceCost + tiles; }
-  __device__ __forceinline__ int units(int Hkv) const { return Hkv * rb * span(); }
+  // length on the line: per (head, row block) the piece cost, then the tiles
+  __device__ __forceinline__ int units(int Hkv, int cost) const { return Hkv * rb * (cost + tiles); }
 };
 
 template <int R>
@@ -195,6 +197,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
 template <int R>
 struct TreeWalk {
   int64_t left;       // of the CTA's part of the line, not walked yet
+  int cost;           // of a piece
   int b, off, units;  // current sequence, how much of its part is walked, its length
   TreeSeq s;
   int hkv, block, t0, nt;  // this step: head, row block, first tile, tiles
@@ -203,16 +206,16 @@ struct TreeWalk {
       while (off >= units) {
         off -= units;
         s = tree_seq<R>(a, ++b);
-        units = s.units(a.Hkv);
+        units = s.units(a.Hkv, cost);
       }
-      const int span = s.span();
+      const int span = cost + s.tiles;
       const int seg = off / span;
       const int in = off - seg * span;
       const int n = static_cast<int>(min(static_cast<int64_t>(span - in), left));
       left -= n;
       off += n;
-      t0 = max(in - kTreePieceCost, 0);
-      nt = in + n - kTreePieceCost - t0;
+      t0 = max(in - cost, 0);
+      nt = in + n - cost - t0;
       hkv = seg / s.rb;
       block = seg - hkv * s.rb;
       if (nt > 0) return true;
@@ -412,12 +415,10 @@ __device__ __forceinline__ float t5_bias_log2(const TreeArgs& a, int rel, int h)
 
 // ---------------------------------------------------------------- queries
 // One piece's query rows as the K-major operand `dst` (kN rows; e4m3: first
-// parts in rows 0 .. R - 1, second parts from row R on) and their TreeRows, by
-// warp w of nw.
+// parts in rows 0 .. R - 1, second parts from row R on), by warp w of nw.
 template <int D, int FMT, int R>
 __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeWalk<R>& wk, int w, int nw,
-                                                  int lane, uint8_t* dst, TreeRows* info,
-                                                  float* t5_slice, bool bias) {
+                                                  int lane, uint8_t* dst, TreeRows* info) {
   using L = TreeLayout<D, FMT, R>;
   const TreeSeq& s = wk.s;
   const int n_rows = s.n * a.G - wk.block * R;  // of this block, may exceed R
@@ -480,6 +481,14 @@ __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeW
                          __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
     }
   }
+}
+
+// The rest of the piece's TreeRows.
+template <int D, int FMT, int R>
+__device__ __forceinline__ void tree_load_rows(const TreeArgs& a, const TreeWalk<R>& wk, int w, int nw,
+                                               int lane, TreeRows* info, float* t5_slice, bool bias) {
+  const TreeSeq& s = wk.s;
+  const int n_rows = s.n * a.G - wk.block * R;  // of this block, may exceed R
   const uint64_t node_bits = s.n >= 64 ? ~0ull : (1ull << s.n) - 1ull;
   auto sees_of = [&](int n) -> uint64_t {
     const uint64_t m = a.mask ? static_cast<uint64_t>(a.mask[s.row0 + n]) : ~0ull >> (63 - n);
@@ -567,6 +576,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   int64_t* start_left = reinterpret_cast<int64_t*>(misc + 32);
   int* start_b = reinterpret_cast<int*>(misc + 40);
   int* start_off = reinterpret_cast<int*>(misc + 44);
+  int* start_cost = reinterpret_cast<int*>(misc + 8);
   TreeSeq* start_seq = reinterpret_cast<TreeSeq*>(misc + 48);  // 28 bytes
 
   if (warp == kTreeIssueS) {
@@ -581,7 +591,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         mbar_init(s_free(x), L::kSoftWarps);
         mbar_init(p_full(x), L::kSoftWarps);
         mbar_init(pv_done(x), 1);
-        mbar_init(q_full(x), 1);
+        mbar_init(q_full(x), 8);
         mbar_init(q_free(x), 8);
         mbar_init(drain(x), 1);
       }
@@ -593,33 +603,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   } else if (warp == kTreeProducer) {
-    // the line of tiles: its length, and where this CTA's piece begins
+    // the line of tiles: its length, and where this CTA's part begins
     TreeSeq s{};
-    int64_t units = 0, total = 0;
+    int64_t tiles = 0, pieces = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
-      units = 0;
       if (b < a.B) {
         s = tree_seq<R>(a, b);
-        units = s.units(a.Hkv);
+        tiles += s.units(a.Hkv, 0);
+        pieces += s.rb * a.Hkv;
       }
-      total += units;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      tiles += __shfl_xor_sync(~0u, tiles, o);
+      pieces += __shfl_xor_sync(~0u, pieces, o);
+    }
+    const int cost = tree_piece_cost(tiles, gridDim.x);
+    const int64_t total = tiles + cost * pieces;
     const int64_t per = tree_share(total, gridDim.x);
     const int64_t from = per * blockIdx.x;
-    if (lane == 0) *start_left = max(min(total - from, per), static_cast<int64_t>(0));
+    if (lane == 0) {
+      *start_left = max(min(total - from, per), static_cast<int64_t>(0));
+      *start_cost = cost;
+    }
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
-      if (a.B > 32) {  // else the first pass's values are at hand
-        units = 0;
-        if (b < a.B) {
-          s = tree_seq<R>(a, b);
-          units = s.units(a.Hkv);
-        }
-      }
+      if (a.B > 32 && b < a.B) s = tree_seq<R>(a, b);  // else the first pass's are at hand
+      const int64_t units = b < a.B ? s.units(a.Hkv, cost) : 0;
       int64_t upto = units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -650,7 +662,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   walk.b = *start_b;
   walk.off = *start_off;
   walk.s = *start_seq;
-  walk.units = walk.s.units(a.Hkv);
+  walk.cost = *start_cost;
+  walk.units = walk.s.units(a.Hkv, walk.cost);
 
   if (warp == kTreeProducer) {
     // ------------------------------------------------------------ producer
@@ -724,12 +737,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       const int x = u & 1;
       if (u >= 2) ok = __all_sync(~0u, mbar_wait(q_free(x), ((u >> 1) - 1) & 1, ctl));
       if (!ok) break;
-      tree_load_queries<D, FMT, R>(a, walk, 0, 1, lane, smem + L::kQOff + x * L::kQBytes,
-                                   reinterpret_cast<TreeRows*>(smem + L::kRowsOff + x * L::kRowsBytes),
-                                   reinterpret_cast<float*>(smem + L::kT5Off) + x * kTreeT5Slice, BIAS != 0);
+      TreeRows* info = reinterpret_cast<TreeRows*>(smem + L::kRowsOff + x * L::kRowsBytes);
+      tree_load_queries<D, FMT, R>(a, walk, 0, 1, lane, smem + L::kQOff + x * L::kQBytes, info);
+      tree_load_rows<D, FMT, R>(a, walk, 0, 1, lane, info,
+                                reinterpret_cast<float*>(smem + L::kT5Off) + x * kTreeT5Slice, BIAS != 0);
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(x));
+      if (lane < 8) mbar_arrive(q_full(x));
       ++u;
     }
   } else if (warp == kTreeIssueS || warp == kTreeIssueO) {
@@ -815,12 +829,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       const TreeSeq& s = walk.s;
       const TreeRows* info = reinterpret_cast<const TreeRows*>(smem + L::kRowsOff + (u & 1) * L::kRowsBytes);
       if (u == 0) {
-        tree_load_queries<D, FMT, R>(a, walk, warp, 8, lane, smem + L::kQOff,
-                                     reinterpret_cast<TreeRows*>(smem + L::kRowsOff),
-                                     reinterpret_cast<float*>(smem + L::kT5Off), BIAS != 0);
+        TreeRows* first = reinterpret_cast<TreeRows*>(smem + L::kRowsOff);
+        tree_load_queries<D, FMT, R>(a, walk, warp, 8, lane, smem + L::kQOff, first);
         fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(0));  // S can begin
+        tree_load_rows<D, FMT, R>(a, walk, warp, 8, lane, first, reinterpret_cast<float*>(smem + L::kT5Off),
+                                  BIAS != 0);
         named_barrier(3, 256);
-        if (tid == 0) mbar_arrive(q_full(0));
       } else {
         wait(q_full(u & 1), (u >> 1) & 1);
       }
@@ -1216,16 +1232,24 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
   const int x = blockIdx.x * kTreeJoinWarps + (threadIdx.x >> 5);  // node * Hq + head
   // all that the lengths decide, while the pieces are still being computed
   const TreeSeq s = tree_seq<R>(a, b);
-  int64_t before = 0, total = 0;
+  int64_t tiles = 0, pieces = 0, tiles_before = 0, pieces_before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int64_t units = b0 + lane < a.B ? tree_seq<R>(a, b0 + lane).units(a.Hkv) : 0;
-    total += units;
-    before += b0 + lane < b ? units : 0;
+    if (b0 + lane >= a.B) continue;
+    const TreeSeq other = tree_seq<R>(a, b0 + lane);
+    const int t = other.units(a.Hkv, 0), p = other.rb * a.Hkv;
+    tiles += t;
+    pieces += p;
+    if (b0 + lane < b) {
+      tiles_before += t;
+      pieces_before += p;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(~0u, total, o);
-    before += __shfl_xor_sync(~0u, before, o);
+    tiles += __shfl_xor_sync(~0u, tiles, o);
+    pieces += __shfl_xor_sync(~0u, pieces, o);
+    tiles_before += __shfl_xor_sync(~0u, tiles_before, o);
+    pieces_before += __shfl_xor_sync(~0u, pieces_before, o);
   }
   const int n = x / a.Hq, h = x - n * a.Hq;
   const int hkv = h / a.G;
@@ -1233,8 +1257,10 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
   const int block = r / R, in = r - block * R;
   int c0 = 0, c1 = 0;
   if (n < s.n) {
-    const int64_t per = tree_share(total, ctas);
-    const int64_t first = before + (static_cast<int64_t>(hkv) * s.rb + block) * s.span() + kTreePieceCost;
+    const int cost = tree_piece_cost(tiles, ctas);
+    const int64_t per = tree_share(tiles + cost * pieces, ctas);
+    const int64_t first = tiles_before + cost * pieces_before +
+                          (static_cast<int64_t>(hkv) * s.rb + block) * (cost + s.tiles) + cost;
     c0 = static_cast<int>(first / per);
     c1 = static_cast<int>((first + s.tiles - 1) / per);
   }
