@@ -197,11 +197,11 @@ sdpa_status_t check_tree(const sdpa_tree* t, const sdpa_kv_cache* c, CacheView& 
   if ((reinterpret_cast<uintptr_t>(t->cu_nodes) & 3u) || (reinterpret_cast<uintptr_t>(t->ctx_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(t->page_table) & 3u) || (reinterpret_cast<uintptr_t>(t->tree_mask) & 7u))
     return SDPA_ERR_INVALID_ARG;
-  // positions, and the tiles of one sequence, are counted in 32 bits
+  // positions, and the tiles of the whole batch, are counted in 32 bits
   if (t->table_width > (1ll << 30) / c->page_size) return SDPA_ERR_UNSUPPORTED;
   const int64_t tiles = (t->table_width * c->page_size + kTreeKeys - 1) / kTreeKeys;
   const int64_t blocks = (t->max_nodes * (t->Hq / c->Hkv) + 15) / 16;
-  if ((tiles + 3) * blocks >= (1ll << 31) / c->Hkv) return SDPA_ERR_UNSUPPORTED;  // (3: a piece's cost)
+  if ((tiles + 3) * blocks >= ((1ll << 31) - (1ll << 16)) / (c->Hkv * t->B)) return SDPA_ERR_UNSUPPORTED;  // (3: a piece's cost)
   if (!good_stride(t->q_t, 8) || !good_stride(t->q_h, 8) || !good_stride(t->o_t, 8) ||
       !good_stride(t->o_h, 8))
     return SDPA_ERR_INVALID_ARG;

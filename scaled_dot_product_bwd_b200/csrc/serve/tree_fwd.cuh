@@ -63,9 +63,7 @@ constexpr int kTreeThreads = 12 * 32;
 // queries, first maximum, ragged end and result).  The line counts them, so
 // that CTAs with many short ones get fewer tiles; where a CTA's share is a few
 // tiles of one piece, every CTA pays once and they count as nothing.
-__device__ __forceinline__ int tree_piece_cost(int64_t tiles, int ctas) {
-  return tiles >= 8ll * ctas ? 3 : 0;
-}
+__device__ __forceinline__ int tree_piece_cost(int tiles, int ctas) { return tiles >= 8 * ctas ? 3 : 0; }
 constexpr int kTreeScaleRing = 8;   // tiles whose e4m3 scales are kept
 // T5: buckets of the distances -kTreeNear .. 63 are tabulated per CTA, and the
 // table's entries of a KV head's query heads per piece where they fit.
@@ -146,13 +144,16 @@ struct TreeLayout {
   static constexpr int kNumBars = 2 * kMaxSlots + 14;
   static constexpr int kMiscBytes = kNumBars * 8 + 128;
   static constexpr int kRingOff = (kMiscOff + kMiscBytes + 1023) / 1024 * 1024;
-  static constexpr int kFit = (232448 - kRingOff) / kTile / 2 * 2;
+  // (2 KB of the SM's shared memory stay free: a CTA of the joining kernel
+  // must find room beside this one to be ready when it ends)
+  static constexpr int kBudget = 230400;
+  static constexpr int kFit = (kBudget - kRingOff) / kTile / 2 * 2;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;  // K and V in turn: even
   static constexpr int kSmem = kRingOff + kSlots * kTile;
   static constexpr int kOCol = 2 * kN;                      // O^T after two S buffers
   static constexpr int kCols = kOCol + (kTurns ? 2 : 1) * kN;
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kSlots >= 4 && kSmem <= 232448, "shared memory budget");
+  static_assert(kSlots >= 4 && kSmem <= kBudget, "shared memory budget");
   static_assert(kCols <= 512, "tensor memory budget");
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "operand alignment");
   static_assert(kMiscOff % 16 == 0, "barrier alignment");
@@ -196,7 +197,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
 // block) by (sequence, head, row block).
 template <int R>
 struct TreeWalk {
-  int64_t left;       // of the CTA's part of the line, not walked yet
+  int left;           // of the CTA's part of the line, not walked yet
   int cost;           // of a piece
   int b, off, units;  // current sequence, how much of its part is walked, its length
   TreeSeq s;
@@ -211,7 +212,7 @@ struct TreeWalk {
       const int span = cost + s.tiles;
       const int seg = off / span;
       const int in = off - seg * span;
-      const int n = static_cast<int>(min(static_cast<int64_t>(span - in), left));
+      const int n = min(span - in, left);
       left -= n;
       off += n;
       t0 = max(in - cost, 0);
@@ -224,10 +225,8 @@ struct TreeWalk {
   }
 };
 
-// A CTA's part of a line of `total`.
-__device__ __forceinline__ int64_t tree_share(int64_t total, int ctas) {
-  return (total + ctas - 1) / ctas;
-}
+// A CTA's part of a line of `total` (which the host keeps below 2^31 - 2^16).
+__device__ __forceinline__ int tree_share(int total, int ctas) { return (total + ctas - 1) / ctas; }
 
 // ------------------------------------------------- operands of the products
 // Shared-memory matrix descriptor of a layout: 0 plain, 2 128-byte swizzle,
@@ -573,7 +572,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   uint32_t* dirty = reinterpret_cast<uint32_t*>(misc + 96);   // [2][4] bits of keys
-  int64_t* start_left = reinterpret_cast<int64_t*>(misc + 32);
+  int* start_left = reinterpret_cast<int*>(misc + 12);
   int* start_b = reinterpret_cast<int*>(misc + 40);
   int* start_off = reinterpret_cast<int*>(misc + 44);
   int* start_cost = reinterpret_cast<int*>(misc + 8);
@@ -605,7 +604,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   } else if (warp == kTreeProducer) {
     // the line of tiles: its length, and where this CTA's part begins
     TreeSeq s{};
-    int64_t tiles = 0, pieces = 0;
+    int tiles = 0, pieces = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       if (b < a.B) {
@@ -614,34 +613,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         pieces += s.rb * a.Hkv;
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      tiles += __shfl_xor_sync(~0u, tiles, o);
-      pieces += __shfl_xor_sync(~0u, pieces, o);
-    }
+    tiles = __reduce_add_sync(~0u, tiles);
+    pieces = __reduce_add_sync(~0u, pieces);
     const int cost = tree_piece_cost(tiles, gridDim.x);
-    const int64_t total = tiles + cost * pieces;
-    const int64_t per = tree_share(total, gridDim.x);
-    const int64_t from = per * blockIdx.x;
+    const int total = tiles + cost * pieces;
+    const int per = tree_share(total, gridDim.x);
+    const int from = min(per * static_cast<int>(blockIdx.x), total);
     if (lane == 0) {
-      *start_left = max(min(total - from, per), static_cast<int64_t>(0));
+      *start_left = min(total - from, per);
       *start_cost = cost;
     }
-    int64_t base = 0;
+    int base = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       if (a.B > 32 && b < a.B) s = tree_seq<R>(a, b);  // else the first pass's are at hand
-      const int64_t units = b < a.B ? s.units(a.Hkv, cost) : 0;
-      int64_t upto = units;
+      const int units = b < a.B ? s.units(a.Hkv, cost) : 0;
+      int upto = units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(~0u, upto, o);
+        const int y = __shfl_up_sync(~0u, upto, o);
         if (lane >= o) upto += y;
       }
-      const int64_t before = base + upto - units;
+      const int before = base + upto - units;
       if (b < a.B && before <= from && from < before + units) {
         *start_b = b;
-        *start_off = static_cast<int>(from - before);
+        *start_off = from - before;
         *start_seq = s;
       }
       base += __shfl_sync(~0u, upto, 31);
@@ -1232,7 +1228,7 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
   const int x = blockIdx.x * kTreeJoinWarps + (threadIdx.x >> 5);  // node * Hq + head
   // all that the lengths decide, while the pieces are still being computed
   const TreeSeq s = tree_seq<R>(a, b);
-  int64_t tiles = 0, pieces = 0, tiles_before = 0, pieces_before = 0;
+  int tiles = 0, pieces = 0, tiles_before = 0, pieces_before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     if (b0 + lane >= a.B) continue;
     const TreeSeq other = tree_seq<R>(a, b0 + lane);
@@ -1244,13 +1240,10 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
       pieces_before += p;
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    tiles += __shfl_xor_sync(~0u, tiles, o);
-    pieces += __shfl_xor_sync(~0u, pieces, o);
-    tiles_before += __shfl_xor_sync(~0u, tiles_before, o);
-    pieces_before += __shfl_xor_sync(~0u, pieces_before, o);
-  }
+  tiles = __reduce_add_sync(~0u, tiles);
+  pieces = __reduce_add_sync(~0u, pieces);
+  tiles_before = __reduce_add_sync(~0u, tiles_before);
+  pieces_before = __reduce_add_sync(~0u, pieces_before);
   const int n = x / a.Hq, h = x - n * a.Hq;
   const int hkv = h / a.G;
   const int r = n * a.G + (h - hkv * a.G);
@@ -1258,11 +1251,10 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
   int c0 = 0, c1 = 0;
   if (n < s.n) {
     const int cost = tree_piece_cost(tiles, ctas);
-    const int64_t per = tree_share(tiles + cost * pieces, ctas);
-    const int64_t first = tiles_before + cost * pieces_before +
-                          (static_cast<int64_t>(hkv) * s.rb + block) * (cost + s.tiles) + cost;
-    c0 = static_cast<int>(first / per);
-    c1 = static_cast<int>((first + s.tiles - 1) / per);
+    const int per = tree_share(tiles + cost * pieces, ctas);
+    const int first = tiles_before + cost * pieces_before + (hkv * s.rb + block) * (cost + s.tiles) + cost;
+    c0 = first / per;
+    c1 = (first + s.tiles - 1) / per;
   }
   // (every thread waits, so that what follows this kernel follows the first too)
   asm volatile("griddepcontrol.wait;" ::: "memory");
