@@ -214,7 +214,7 @@ sdpa_status_t check_tree(const sdpa_tree* t, const sdpa_kv_cache* c, CacheView& 
 template <int D, int FMT, int R, int BIAS>
 cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                         cudaStream_t st) {
-  using L = TreeLayout<D, FMT, R>;
+  using L = TreeLayout<D, FMT, R, BIAS>;
   auto kern = tree_fwd_kernel<D, FMT, R, BIAS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;

@@ -33,10 +33,11 @@
 //  * roles run on across pieces: a producer warp (TMA, one box per page
 //    piece, K and V in slots of their own so that K's is free as soon as S is
 //    there), a query warp that lays the next piece's rows out as an operand,
-//    an issuing thread each for S and for P V, and two softmax warpgroups.
-//    The softmax's chain of waits per tile (~700 cycles) is what a short row
-//    block would pay, so up to 32 rows the warpgroups take turns by tile, each
-//    with its own O; at 64 rows they share a tile by rows.
+//    an issuing thread each for S and for P V, and four softmax warpgroups
+//    of 16 rows.  The softmax's chain of waits per tile (~700 cycles) is what
+//    one warpgroup would pay again and again, so at 16 rows the four take
+//    turns by tile, each with an O of its own; at 32 two pairs do; at 64 they
+//    share every tile by rows.
 #pragma once
 
 #include <cfloat>
@@ -56,15 +57,17 @@ constexpr int kTreeMaxCtas = 148;   // one per SM; the workspace is sized for it
 constexpr int kTreeMaxNodes = 64;
 constexpr int kTreeMaxRows = 64;    // query rows of one product
 constexpr int kTreeKeys = 128;      // keys per tile
-// warps after the 8 of the softmax
-constexpr int kTreeProducer = 8, kTreeIssueS = 9, kTreeIssueO = 10, kTreeQuery = 11;
-constexpr int kTreeThreads = 12 * 32;
+constexpr int kTreeSoftWarps = 16;
+constexpr int kTreeProducer = 16, kTreeIssueS = 17, kTreeIssueO = 18, kTreeQuery = 19;  // the other warps
+constexpr int kTreeThreads = 20 * 32;
+constexpr int kTreeRT = 16;         // rows of a softmax thread
+// Named barriers: 1 .. 4 a softmax warpgroup, 5 all four, 6 + turn those of one tile.
+constexpr uint32_t kTreeBarAll = 5, kTreeBarTurn = 6;
 // A (sequence, head, row block) costs its first CTA about three tiles more (its
 // queries, first maximum, ragged end and result).  The line counts them, so
 // that CTAs with many short ones get fewer tiles; where a CTA's share is a few
 // tiles of one piece, every CTA pays once and they count as nothing.
 __device__ __forceinline__ int tree_piece_cost(int tiles, int ctas) { return tiles >= 8 * ctas ? 3 : 0; }
-constexpr int kTreeScaleRing = 8;   // tiles whose e4m3 scales are kept
 // T5: buckets of the distances -kTreeNear .. 63 are tabulated per CTA, and the
 // table's entries of a KV head's query heads per piece where they fit.
 constexpr int kTreeNear = 960, kTreeBuckets = kTreeNear + 64, kTreeT5Slice = 1024;
@@ -110,7 +113,7 @@ struct TreeRows {
   int depth[kTreeMaxNodes];     // of the sequence's nodes
 };
 
-template <int D, int FMT, int R>
+template <int D, int FMT, int R, int BIAS>
 struct TreeLayout {
   static constexpr bool kE4m3 = FMT == kCacheE4m3;
   static constexpr int kCell = kE4m3 ? 1 : 2;
@@ -122,27 +125,23 @@ struct TreeLayout {
   static constexpr int kN = kParts * R;                     // columns of S and of O^T
   static constexpr int kQBytes = kN * kRowBytes;
   static constexpr int kPBytes = kN * kTreeKeys * kCell;
-  // Up to 32 rows the softmax warpgroups take turns by tile, each with all
-  // rows and an O of its own; 64 rows of state do not fit a thread, and they
-  // take half the rows each.
-  static constexpr bool kTurns = R <= 32;
-  static constexpr int kRT = kTurns ? R : R / 2;            // rows of a softmax thread
-  static constexpr int kRO = R / 2;                         // rows it writes out
-  static constexpr int kSoftWarps = kTurns ? 4 : 8;         // that work on one tile
+  static constexpr int kGroups = R / kTreeRT;               // softmax warpgroups that share a tile
+  static constexpr int kTurns = 4 / kGroups;                // ... and how many such sets there are
+  static constexpr int kBufs = kTurns > 2 ? kTurns : 2;     // of S and of the weights
+  static constexpr int kRO = R / 4 > 8 ? R / 4 : 8;         // rows a warpgroup writes out
   static constexpr int kQOff = 0;
   static constexpr int kPOff = kQOff + 2 * kQBytes;
-  static constexpr int kScaleOff = kPOff + 2 * kPBytes;     // [kTreeScaleRing][K, V][128]
-  static constexpr int kRowsOff = kScaleOff + (kE4m3 ? kTreeScaleRing * 256 : 0);
+  static constexpr int kRowsOff = kPOff + kBufs * kPBytes;
   static constexpr int kRowsBytes = (static_cast<int>(sizeof(TreeRows)) + 15) / 16 * 16;
-  static constexpr int kMaxOff = kRowsOff + 2 * kRowsBytes;      // [2][kRT][4] floats
-  static constexpr int kRefOff = kMaxOff + 2 * kRT * 16;         // [2][kRT] floats
-  static constexpr int kFacOff = kRefOff + 2 * kRT * 4;          // [2][kRT] floats
-  static constexpr int kBucketOff = kFacOff + 2 * kRT * 4;       // [kTreeBuckets] bytes
-  static constexpr int kT5Off = kBucketOff + kTreeBuckets;       // [2][kTreeT5Slice] floats
-  static constexpr int kMiscOff = kT5Off + 2 * kTreeT5Slice * 4;
-  static constexpr int kMaxSlots = 12;                      // scales outlive their tile's slots
-  static constexpr int kNumBars = 2 * kMaxSlots + 14;
-  static constexpr int kMiscBytes = kNumBars * 8 + 128;
+  static constexpr int kMaxOff = kRowsOff + 2 * kRowsBytes;      // [4][kTreeRT][4] floats
+  static constexpr int kRefOff = kMaxOff + 4 * kTreeRT * 16;     // [4][kTreeRT] floats
+  static constexpr int kFacOff = kRefOff + 4 * kTreeRT * 4;      // [4][kTreeRT] floats
+  static constexpr int kBucketOff = kFacOff + 4 * kTreeRT * 4;   // [kTreeBuckets] bytes
+  static constexpr int kT5Off = kBucketOff + (BIAS ? kTreeBuckets : 0);  // [2][kTreeT5Slice] floats
+  static constexpr int kMiscOff = kT5Off + (BIAS ? 2 * kTreeT5Slice * 4 : 0);
+  static constexpr int kMaxSlots = 12;
+  static constexpr int kNumBars = 2 * kMaxSlots + 4 * kBufs + 6;
+  static constexpr int kMiscBytes = kNumBars * 8 + 160;
   static constexpr int kRingOff = (kMiscOff + kMiscBytes + 1023) / 1024 * 1024;
   // (2 KB of the SM's shared memory stay free: a CTA of the joining kernel
   // must find room beside this one to be ready when it ends)
@@ -150,8 +149,8 @@ struct TreeLayout {
   static constexpr int kFit = (kBudget - kRingOff) / kTile / 2 * 2;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;  // K and V in turn: even
   static constexpr int kSmem = kRingOff + kSlots * kTile;
-  static constexpr int kOCol = 2 * kN;                      // O^T after two S buffers
-  static constexpr int kCols = kOCol + (kTurns ? 2 : 1) * kN;
+  static constexpr int kOCol = kBufs * kN;                  // the O^T after the S buffers
+  static constexpr int kCols = kOCol + kTurns * kN;
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kSlots >= 4 && kSmem <= kBudget, "shared memory budget");
   static_assert(kCols <= 512, "tensor memory budget");
@@ -415,10 +414,10 @@ __device__ __forceinline__ float t5_bias_log2(const TreeArgs& a, int rel, int h)
 // ---------------------------------------------------------------- queries
 // One piece's query rows as the K-major operand `dst` (kN rows; e4m3: first
 // parts in rows 0 .. R - 1, second parts from row R on), by warp w of nw.
-template <int D, int FMT, int R>
+template <int D, int FMT, int R, int BIAS>
 __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeWalk<R>& wk, int w, int nw,
                                                   int lane, uint8_t* dst, TreeRows* info) {
-  using L = TreeLayout<D, FMT, R>;
+  using L = TreeLayout<D, FMT, R, BIAS>;
   const TreeSeq& s = wk.s;
   const int n_rows = s.n * a.G - wk.block * R;  // of this block, may exceed R
   constexpr int kLanes = D / 8;        // lanes of a row, 8 elements each
@@ -483,9 +482,9 @@ __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeW
 }
 
 // The rest of the piece's TreeRows.
-template <int D, int FMT, int R>
+template <int R, int BIAS>
 __device__ __forceinline__ void tree_load_rows(const TreeArgs& a, const TreeWalk<R>& wk, int w, int nw,
-                                               int lane, TreeRows* info, float* t5_slice, bool bias) {
+                                               int lane, TreeRows* info, float* t5_slice) {
   const TreeSeq& s = wk.s;
   const int n_rows = s.n * a.G - wk.block * R;  // of this block, may exceed R
   const uint64_t node_bits = s.n >= 64 ? ~0ull : (1ull << s.n) - 1ull;
@@ -508,7 +507,7 @@ __device__ __forceinline__ void tree_load_rows(const TreeArgs& a, const TreeWalk
         head += x - n * a.G;
         out = static_cast<int64_t>(s.row0 + n) * a.o_t + static_cast<int64_t>(head) * a.o_h;
         lse = static_cast<int64_t>(head) * a.T + s.row0 + n;
-        if (bias) {
+        if constexpr (BIAS != 0) {
           if (a.alibi_slopes) slope = a.alibi_slopes[head];
           else if (a.t5.one_lo_max != INT_MIN) slope = t5_bias_log2(a, a.t5.one_lo_max, head);
         }
@@ -528,7 +527,7 @@ __device__ __forceinline__ void tree_load_rows(const TreeArgs& a, const TreeWalk
   }
   if (w == nw - 1)
     for (int n = lane; n < s.n; n += 32) info->depth[n] = __popcll(sees_of(n) & ~(1ull << n));
-  if (bias && a.t5_table && a.t5_buckets * a.G <= kTreeT5Slice) {
+  if (BIAS != 0 && a.t5_table && a.t5_buckets * a.G <= kTreeT5Slice) {
 #pragma unroll 4
     for (int i = w * 32 + lane; i < a.t5_buckets * a.G; i += nw * 32) {
       const int k = i / a.G;
@@ -542,11 +541,12 @@ template <int D, int FMT, int R, int BIAS>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap mk,
     const __grid_constant__ CUtensorMap mv) {
-  using L = TreeLayout<D, FMT, R>;
+  using L = TreeLayout<D, FMT, R, BIAS>;
   constexpr bool E4 = L::kE4m3;
   constexpr int NS = L::kSlots;
-  constexpr int RT = L::kRT;
+  constexpr int RT = kTreeRT;
   constexpr int RO = L::kRO;
+  constexpr int TN = L::kTurns, NB = L::kBufs, RG = L::kGroups;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!smem_base_ok(smem)) {
     if (threadIdx.x == 0) atomicOr(&g_device_status, kStatusMisaligned);
@@ -559,19 +559,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   auto full = [&](int s) { return bar(s); };
   auto empty = [&](int s) { return bar(L::kMaxSlots + s); };
   constexpr int kB = 2 * L::kMaxSlots;
-  auto s_full = [&](int x) { return bar(kB + x); };       // S of a tile is in tensor memory
-  auto s_free = [&](int x) { return bar(kB + 2 + x); };   // ... and in registers
-  auto p_full = [&](int x) { return bar(kB + 4 + x); };   // weights are in shared memory
-  auto pv_done = [&](int x) { return bar(kB + 6 + x); };  // ... and added to O
-  auto q_full = [&](int x) { return bar(kB + 8 + x); };   // a piece's queries are laid out
-  auto q_free = [&](int x) { return bar(kB + 10 + x); };  // ... and the piece is done
-  auto drain = [&](int x) { return bar(kB + 12 + x); };
+  auto s_full = [&](int x) { return bar(kB + x); };            // S of a tile is in tensor memory
+  auto s_free = [&](int x) { return bar(kB + NB + x); };       // ... and in registers
+  auto p_full = [&](int x) { return bar(kB + 2 * NB + x); };   // weights are in shared memory
+  auto pv_done = [&](int x) { return bar(kB + 3 * NB + x); };  // ... and added to O
+  constexpr int kQ = kB + 4 * NB;
+  auto q_full = [&](int x) { return bar(kQ + x); };            // a piece's queries are laid out
+  auto q_free = [&](int x) { return bar(kQ + 2 + x); };        // ... and the piece is done
+  auto drain = [&](int x) { return bar(kQ + 4 + x); };
   // K of the CTA's tile `it` is item 2 it of the ring, its V item 2 it + 1
   auto slot_off = [&](uint32_t item) { return L::kRingOff + (item % NS) * L::kTile; };
   uint8_t* misc = smem + L::kMiscOff + L::kNumBars * 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
-  uint32_t* dirty = reinterpret_cast<uint32_t*>(misc + 96);   // [2][4] bits of keys
+  uint32_t* dirty = reinterpret_cast<uint32_t*>(misc + 80);   // [4 turns][4] bits of keys
   int* start_left = reinterpret_cast<int*>(misc + 12);
   int* start_b = reinterpret_cast<int*>(misc + 40);
   int* start_off = reinterpret_cast<int*>(misc + 44);
@@ -581,17 +582,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   if (warp == kTreeIssueS) {
     if (lane == 0) {
       *abort_flag = 0;
+      for (int x = 0; x < 16; ++x) dirty[x] = 0;
       for (int s = 0; s < NS; ++s) {
         mbar_init(full(s), 1);
         mbar_init(empty(s), 1);
       }
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < NB; ++x) {
         mbar_init(s_full(x), 1);
-        mbar_init(s_free(x), L::kSoftWarps);
-        mbar_init(p_full(x), L::kSoftWarps);
+        mbar_init(s_free(x), 4 * RG);
+        mbar_init(p_full(x), 4 * RG);
         mbar_init(pv_done(x), 1);
-        mbar_init(q_full(x), 8);
-        mbar_init(q_free(x), 8);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(q_full(x), kTreeSoftWarps);
+        mbar_init(q_free(x), kTreeSoftWarps);
         mbar_init(drain(x), 1);
       }
       fence_mbar_init();
@@ -643,8 +647,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       base += __shfl_sync(~0u, upto, 31);
       if (base > from) break;
     }
-  } else if (BIAS != 0 && warp < 8 && a.t5_table) {
-    for (int i = tid; i < kTreeBuckets; i += 256)
+  } else if (BIAS != 0 && warp < kTreeSoftWarps && a.t5_table) {
+    for (int i = tid; i < kTreeBuckets; i += kTreeSoftWarps * 32)
       smem[L::kBucketOff + i] = static_cast<uint8_t>(t5_bucket(i - kTreeNear, a.t5));
   }
   tc_fence_before();
@@ -686,9 +690,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         const int t = walk.t0 + i;
         const int next_page = i + 1 < walk.nt ? page_of(t + 1) : -1;
         const bool copy = page >= 0;
-        const bool scales = E4 && copy && page < a.num_pages;
         const int n_copy = __popc(__ballot_sync(~0u, copy));
-        const int n_scale = __popc(__ballot_sync(~0u, scales));
         const int r = ((walk.s.tile0 + t) * kTreeKeys + lane * a.box_rows) & (a.page_size - 1);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++item) {
@@ -696,22 +698,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           if (item >= NS) ok = mbar_wait(empty(item % NS), ((item / NS) - 1) & 1, ctl);
           ok = __all_sync(~0u, ok);
           if (!ok) break;
-          // the scales of both come with K.  Their place was tile it - 8's, whose
-          // P V is done: V's slot of tile it - 1 was free for that tile's copy, and
-          // the tile before it there is at most 7 tiles back.
-          if (lane == 0) mbar_expect_tx(f, n_copy * box_bytes + (kv == 0 ? 2u * n_scale * a.box_rows : 0u));
+          if (lane == 0) mbar_expect_tx(f, n_copy * box_bytes);
           __syncwarp();
           if (copy) {
             const uint32_t dst = sb + slot_off(item) + static_cast<uint32_t>(lane) * a.box_rows * L::kLine;
 #pragma unroll
             for (int h = 0; h < L::kHalves; ++h)
               tma_load_4d(dst + h * kTreeKeys * 128, kv ? &mv : &mk, f, h * 64, r, walk.hkv, page);
-          }
-          if (kv == 0 && scales) {
-            const int64_t off = page * a.ss_page + walk.hkv * a.ss_head + r;
-            const uint32_t dst = sb + L::kScaleOff + (it % kTreeScaleRing) * 256 + lane * a.box_rows;
-            bulk_load(dst, a.ks + off, a.box_rows, f);
-            bulk_load(dst + 128, a.vs + off, a.box_rows, f);
           }
         }
         page = next_page;
@@ -734,12 +727,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       if (u >= 2) ok = __all_sync(~0u, mbar_wait(q_free(x), ((u >> 1) - 1) & 1, ctl));
       if (!ok) break;
       TreeRows* info = reinterpret_cast<TreeRows*>(smem + L::kRowsOff + x * L::kRowsBytes);
-      tree_load_queries<D, FMT, R>(a, walk, 0, 1, lane, smem + L::kQOff + x * L::kQBytes, info);
-      tree_load_rows<D, FMT, R>(a, walk, 0, 1, lane, info,
-                                reinterpret_cast<float*>(smem + L::kT5Off) + x * kTreeT5Slice, BIAS != 0);
+      tree_load_queries<D, FMT, R, BIAS>(a, walk, 0, 1, lane, smem + L::kQOff + x * L::kQBytes, info);
+      tree_load_rows<R, BIAS>(a, walk, 0, 1, lane, info,
+                              reinterpret_cast<float*>(smem + L::kT5Off) + x * kTreeT5Slice);
       fence_async_shared();
       __syncwarp();
-      if (lane < 8) mbar_arrive(q_full(x));
+      if (lane < kTreeSoftWarps) mbar_arrive(q_full(x));
       ++u;
     }
   } else if (warp == kTreeIssueS || warp == kTreeIssueO) {
@@ -763,10 +756,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         if (is_s) ok = mbar_wait(q_full(u & 1), (u >> 1) & 1, ctl);
         const uint64_t qd = dk + ((L::kQOff + (u & 1) * L::kQBytes) >> 4);
         for (int i = 0; ok && i < walk.nt; ++i, ++it) {
-          const uint32_t x = it & 1, item = 2 * it + (is_s ? 0 : 1);
+          const uint32_t x = it % NB, item = 2 * it + (is_s ? 0 : 1);
           if (!(ok = mbar_wait(full(item % NS), (item / NS) & 1, ctl))) break;
           if (is_s) {  // S^T = K Q^T
-            if (it >= 2 && !(ok = mbar_wait(s_free(x), ((it >> 1) - 1) & 1, ctl))) break;
+            if (it >= NB && !(ok = mbar_wait(s_free(x), (it / NB - 1) & 1, ctl))) break;
             tc_fence_after();
             const uint64_t kd = dk + (slot_off(item) >> 4);
 #pragma unroll
@@ -775,12 +768,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
                             qd + (kmajor_koff(k, L::kN) >> 4), kIdS, k > 0 ? 1u : 0u);
             mma_commit(s_full(x));
           } else {  // O^T += V^T P^T; a piece's first tile in an O overwrites it
-            if (!(ok = mbar_wait(p_full(x), (it >> 1) & 1, ctl))) break;
+            if (!(ok = mbar_wait(p_full(x), (it / NB) & 1, ctl))) break;
             tc_fence_after();
             const uint64_t vd = dv + (slot_off(item) >> 4);
             const uint64_t pd = dp + ((L::kPOff + x * L::kPBytes) >> 4);
-            const uint32_t o = tmem + L::kOCol + (L::kTurns ? x * L::kN : 0);
-            const bool add = i >= (L::kTurns ? 2 : 1);
+            const uint32_t o = tmem + L::kOCol + (it % TN) * L::kN;
+            const bool add = i >= TN;
 #pragma unroll
             for (int k = 0; k < kTreeKeys / kStep; ++k)
               tree_mma<FMT>(o, vd + (k * kStep * L::kLine >> 4), pd + (k * kStep * 16 >> 4), kIdO,
@@ -803,12 +796,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     const int wg = warp >> 2;
     const int me = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int row0 = L::kTurns ? 0 : wg * RT;                     // first row of this thread's scores
-    const uint32_t t_o = tmem + lanes + L::kOCol + (L::kTurns ? wg * L::kN : row0);
-    float* wmax = reinterpret_cast<float*>(smem + L::kMaxOff);    // [2][RT][4 warps]
+    const uint32_t turn = wg / RG;          // takes the tiles it = turn (mod TN)
+    const int row0 = wg % RG * RT;          // first row of this thread's scores
+    const uint32_t t_o = tmem + lanes + L::kOCol + turn * L::kN + row0;
+    constexpr uint32_t kTileThreads = 128 * RG;  // that work on one tile
+    const uint32_t b_tile = RG == 1 ? 1 + wg : kTreeBarTurn + turn;
+    float* wmax = reinterpret_cast<float*>(smem + L::kMaxOff);    // [4][RT][4 warps]
     float* mine = wmax + wg * RT * 4;
-    float* refs = reinterpret_cast<float*>(smem + L::kRefOff);    // [2][RT]
-    float* facs = reinterpret_cast<float*>(smem + L::kFacOff);    // [2][RT]: what the last rescaling took
+    float* refs = reinterpret_cast<float*>(smem + L::kRefOff);    // [4][RT]
+    float* facs = reinterpret_cast<float*>(smem + L::kFacOff);    // [4][RT]: what the last rescaling took
     // After a wait that ran out the warps go on without waiting, through the
     // same barriers, so that no thread is left at one.
     bool ok = true;
@@ -818,7 +814,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       ok = __all_sync(~0u, ok);
     };
     auto values_done = [&](uint32_t j) {  // P V of tile j has been added to O
-      wait(pv_done(j & 1), (j >> 1) & 1);
+      wait(pv_done(j % NB), (j / NB) & 1);
       tc_fence_after();
     };
     while (walk.next(a)) {
@@ -826,13 +822,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       const TreeRows* info = reinterpret_cast<const TreeRows*>(smem + L::kRowsOff + (u & 1) * L::kRowsBytes);
       if (u == 0) {
         TreeRows* first = reinterpret_cast<TreeRows*>(smem + L::kRowsOff);
-        tree_load_queries<D, FMT, R>(a, walk, warp, 8, lane, smem + L::kQOff, first);
+        tree_load_queries<D, FMT, R, BIAS>(a, walk, warp, kTreeSoftWarps, lane, smem + L::kQOff, first);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full(0));  // S can begin
-        tree_load_rows<D, FMT, R>(a, walk, warp, 8, lane, first, reinterpret_cast<float*>(smem + L::kT5Off),
-                                  BIAS != 0);
-        named_barrier(3, 256);
+        tree_load_rows<R, BIAS>(a, walk, warp, kTreeSoftWarps, lane, first,
+                                reinterpret_cast<float*>(smem + L::kT5Off));
+        named_barrier(kTreeBarAll, kTreeSoftWarps * 32);
       } else {
         wait(q_full(u & 1), (u >> 1) & 1);
       }
@@ -843,12 +839,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         l[j] = 0.f;
       }
       bool fresh = true;  // no tile of the piece in this warpgroup's O yet
+      // e4m3: the scales of this thread's key, read one tile ahead: its page
+      // at the tile's start, the bytes at its end
+      uint32_t k_byte = 127, v_byte = 127;
+      int page = -1;
+      auto find_page = [&](int i) {
+        const int pos = (s.tile0 + walk.t0 + i) * kTreeKeys + me;
+        page = -1;
+        if (i < walk.nt && pos < s.keys)
+          page = a.table[static_cast<int64_t>(walk.b) * a.table_b + (pos >> a.page_shift)];
+      };
+      auto find_scales = [&](int i) {
+        const int pos = (s.tile0 + walk.t0 + i) * kTreeKeys + me;
+        if (page >= 0 && page < a.num_pages) {
+          const int64_t at = page * a.ss_page + walk.hkv * a.ss_head + (pos & (a.page_size - 1));
+          k_byte = a.ks[at];
+          v_byte = a.vs[at];
+        } else {
+          k_byte = v_byte = 127;
+        }
+      };
+      if constexpr (E4) {
+        const int i = static_cast<int>((turn - it) & (TN - 1));  // its first tile
+        find_page(i);
+        find_scales(i);
+      }
       for (int i = 0; i < walk.nt; ++i, ++it) {
-        if (L::kTurns && (it & 1) != static_cast<uint32_t>(wg)) continue;
-        const uint32_t x = it & 1;
+        if (it % TN != turn) continue;
+        const uint32_t x = it % NB;
         const int key0 = (s.tile0 + walk.t0 + i) * kTreeKeys;
         const int key = key0 + me;
-        wait(s_full(x), (it >> 1) & 1);
+        if constexpr (E4) find_page(i + TN);
+        wait(s_full(x), (it / NB) & 1);
         tc_fence_after();
         float sc[RT];
         tmem_ld_cols<RT>(tmem + lanes + x * L::kN + row0, sc);
@@ -867,9 +889,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         // scores in log2 units, plus the exponent of the key's value scale
         float v_inv = 1.f;
         if constexpr (E4) {
-          const uint8_t* sc8 = smem + L::kScaleOff + (it % kTreeScaleRing) * 256 + me;
-          const float kf = e8m0_float(sc8[0]);
-          const int ve = sc8[128];
+          const float kf = e8m0_float(k_byte);
+          const int ve = static_cast<int>(v_byte);
           v_inv = e8m0_float(static_cast<uint32_t>(max(254 - ve, 0)));
           const uint64_t kf2 = f2_pack(kf, kf);
           const float vx = static_cast<float>(ve - 127);
@@ -929,13 +950,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           }
         }
         if (masked) {
-          uint32_t seen = node < 0 ? ~0u : node < s.n ? info->seen[node][row0 / 32] : 0u;
+          uint32_t seen = node < 0 ? ~0u : node < s.n ? info->seen[node][row0 / 32] >> (row0 % 32) : 0u;
           if (a.wl >= 0) {
 #pragma unroll
             for (int j = 0; j < RT; ++j)
               if (info->pos[row0 + j] - key_pos > a.wl) seen &= ~(1u << j);
           }
-          constexpr uint32_t kRows = RT == 32 ? ~0u : (1u << RT % 32) - 1u;
+          constexpr uint32_t kRows = (1u << RT) - 1u;
           hidden = (seen & kRows) != kRows;
 #pragma unroll
           for (int j = 0; j < RT; ++j)
@@ -943,7 +964,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
 
         // the weight buffer is free, and with turns this warpgroup's O at rest
-        if (it >= 2) values_done(it - 2);
+        if (it >= NB) values_done(it - NB);
         // a new reference where a score has outgrown the old one
         float over = -INFINITY;
 #pragma unroll
@@ -963,7 +984,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
             refs[wg * RT + lane] = m;
             facs[wg * RT + lane] = fast_exp2(old - m);
           }
-          if (!L::kTurns && !fresh) values_done(it - 1);
+          if (TN < NB && !fresh) values_done(it - TN);
           named_barrier(1 + wg, 128);
 #pragma unroll
           for (int j = 0; j < RT; j += 4) {
@@ -1024,6 +1045,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
                 make_uint4(pack_bf16x2(sc[j], sc[j + 1]), pack_bf16x2(sc[j + 2], sc[j + 3]),
                            pack_bf16x2(sc[j + 4], sc[j + 5]), pack_bf16x2(sc[j + 6], sc[j + 7]));
         }
+        if constexpr (E4) find_scales(i + TN);
         bool mend = false;
         if (masked) {
           // 0 * NaN is NaN: rows behind the sequence's end are zeroed (they hold
@@ -1036,7 +1058,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           wait(full(item % NS), (item / NS) & 1);
           uint32_t odd = 0;
           if (key >= s.keys) {
-            if (L::kTurns || wg == 0) {
+            if (row0 == 0) {
 #pragma unroll 4
               for (int c = 0; c < kPieces; ++c)
                 *reinterpret_cast<uint4*>(vrows + L::at(me, c, kTreeKeys)) = make_uint4(0, 0, 0, 0);
@@ -1049,14 +1071,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
                      nonfinite_bits<FMT>(w.w);
             }
           }
-          constexpr uint32_t kAll = L::kTurns ? 128 : 256;  // threads of the tile
-          const uint32_t b_all = L::kTurns ? 1 + wg : 3;
-          mend = barrier_or(b_all, kAll, odd != 0);
+          mend = barrier_or(b_tile, kTileThreads, odd != 0);
           if (mend) {
-            uint32_t* bits = dirty + (L::kTurns ? wg * 4 : 0);
+            uint32_t* bits = dirty + turn * 4;
             const uint32_t some = __ballot_sync(~0u, odd != 0);
-            if (lane == 0) bits[warp & 3] = some;  // (both warpgroups write the same)
-            named_barrier(b_all, kAll);
+            if (lane == 0 && some) atomicOr(&bits[warp & 3], some);
+            named_barrier(b_tile, kTileThreads);
             // sc becomes what the rows of this thread miss in its column of O
 #pragma unroll
             for (int j = 0; j < RT; ++j) sc[j] = 0.f;
@@ -1081,8 +1101,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
                   if (E4 ? *src != 0 : *reinterpret_cast<const uint16_t*>(src) != 0) sc[j] += v;
                 }
               }
-            named_barrier(b_all, kAll);
-            if ((L::kTurns || wg == 0) && odd != 0) {
+            named_barrier(b_tile, kTileThreads);
+            if (row0 == 0 && me < 4) bits[me] = 0;
+            if (odd != 0) {
 #pragma unroll 1
               for (int c = 0; c < kPieces; ++c) {
                 uint4* p = reinterpret_cast<uint4*>(vrows + L::at(me, c, kTreeKeys));
@@ -1119,66 +1140,57 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       const float total = by_halves<RT>(l, lane, [](float x, float y) { return x + y; });
       if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = total;
       // the last P V of this warpgroup's O
-      const uint32_t last = it - 1;
-      if (!L::kTurns) values_done(last);
-      else if (!fresh) values_done((last & 1) == static_cast<uint32_t>(wg) ? last : last - 1);
-      constexpr uint32_t kAll = L::kTurns ? 256 : 128;  // threads whose results meet
-      const uint32_t b_all = L::kTurns ? 3 : 1 + wg;
+      if (!fresh) values_done(it - 1 - ((it - 1 - turn) & (TN - 1)));
+      constexpr uint32_t kMeet = TN == 1 ? 128 : kTreeSoftWarps * 32;  // threads whose results meet
+      const uint32_t b_meet = TN == 1 ? 1 + wg : kTreeBarAll;
       tc_fence_before();
-      named_barrier(b_all, kAll);
+      named_barrier(b_meet, kMeet);
       tc_fence_after();
 
       const bool whole = walk.t0 == 0 && walk.nt == s.tiles;
       const int slot = walk.t0 == 0 ? 1 : 0;  // 0: began in an earlier CTA
       const int out0 = wg * RO;               // first row that this thread writes
-      const int n_rows = s.n * a.G - walk.block * R - out0;  // from there on, may exceed RO
+      const int n_rows = min(R, s.n * a.G - walk.block * R) - out0;  // from there on, may exceed RO
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + out0;
-      const bool second = L::kTurns && walk.nt > 1;  // both warpgroups had tiles
-      const int w0 = L::kTurns ? static_cast<int>((it - walk.nt) & 1) : wg;  // that of the first tile
+      const int sets = min(walk.nt, TN);      // that had tiles, from the first tile's on
       // (rolled: straight-line code that runs once per piece would wait for
       // its instructions longer than it runs)
 #pragma unroll 1
       for (int j0 = 0; j0 < min(RO, n_rows); j0 += 8) {
+        const int row = out0 + j0;
         float o[8], sum[8], rr[8];
-        // one accumulator's 8 columns, its parts joined
-        auto columns = [&](uint32_t t, float (&y)[8]) {
-          tmem_ld_cols<8>(t, y);
-          if constexpr (E4) {
-            float rest[8];
-            tmem_ld_cols<8>(t + R, rest);
-            fma_rows<8>(rest, 1.f / kWeightRest, y);
-          }
-        };
-        auto sum_of = [&](int w, int row) {
-          const float4 l4 = *reinterpret_cast<const float4*>(wmax + (w * RT + row) * 4);
-          return (l4.x + l4.y) + (l4.z + l4.w);
-        };
-        const uint32_t t = tmem + lanes + L::kOCol + out0 + j0;
-        const int row = L::kTurns ? out0 + j0 : j0;   // in the warpgroups' arrays
-        columns(t + (L::kTurns ? w0 * L::kN : 0), o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          rr[j] = refs[w0 * RT + row + j];
-          sum[j] = sum_of(w0, row + j);
+          o[j] = sum[j] = 0.f;
+          rr[j] = -FLT_MAX;
         }
-        if (second) {
+#pragma unroll 1
+        for (int k = 0; k < sets; ++k) {
+          const int t = (it - walk.nt + k) & (TN - 1);
+          const int at = (t * RG + row / RT) * RT + row % RT;  // in the warpgroups' arrays
           float o2[8];
-          columns(t + (1 - w0) * L::kN, o2);
+          tmem_ld_cols<8>(tmem + lanes + L::kOCol + t * L::kN + row, o2);
+          if constexpr (E4) {
+            float rest[8];
+            tmem_ld_cols<8>(tmem + lanes + L::kOCol + t * L::kN + R + row, rest);
+            fma_rows<8>(rest, 1.f / kWeightRest, o2);
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float r2 = refs[(1 - w0) * RT + row + j];
+            const float4 l4 = *reinterpret_cast<const float4*>(wmax + (at + j) * 4);
+            const float r2 = refs[at + j];
             const float top = fmaxf(rr[j], r2);
             const float f1 = fast_exp2(rr[j] - top), f2 = fast_exp2(r2 - top);
             o[j] = o[j] * f1 + o2[j] * f2;
-            sum[j] = sum[j] * f1 + sum_of(1 - w0, row + j) * f2;
+            sum[j] = sum[j] * f1 + ((l4.x + l4.y) + (l4.z + l4.w)) * f2;
             rr[j] = top;
           }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (whole) o[j] *= sum[j] > 0.f || isnan(sum[j]) ? 1.f / sum[j] : 0.f;
-          if (me == j0 + j && j0 + j < n_rows) {
-            if (whole) a.lse[info->lse[out0 + j0 + j]] = (rr[j] + log2f(sum[j])) * kLn2;
+          if (me == j && j0 + j < n_rows) {
+            if (whole) a.lse[info->lse[row + j]] = (rr[j] + log2f(sum[j])) * kLn2;
             else a.part_ml[part + j0 + j] = make_float2(rr[j], sum[j]);
           }
         }
@@ -1191,7 +1203,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
               const bool up = lane & 1;
               const float got = __shfl_xor_sync(~0u, up ? o[j] : o[j + 1], 1);
               if (j0 + j + (up ? 1 : 0) < n_rows)
-                *reinterpret_cast<uint32_t*>(a.o + info->out[out0 + j0 + j + (up ? 1 : 0)] + (me & ~1)) =
+                *reinterpret_cast<uint32_t*>(a.o + info->out[row + j + (up ? 1 : 0)] + (me & ~1)) =
                     up ? pack_bf16x2(got, o[j + 1]) : pack_bf16x2(o[j], got);
             } else {
               if (j0 + j < n_rows) a.part_o[(part + j0 + j) * D + me] = o[j];
@@ -1201,7 +1213,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
       }
       tc_fence_before();
-      named_barrier(b_all, kAll);  // O, the sums and the references are read
+      named_barrier(b_meet, kMeet);  // O, the sums and the references are read
       if (lane == 0) mbar_arrive(q_free(u & 1));
       ++u;
     }
