@@ -673,23 +673,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     bool ok = true;
     while (ok && walk.next(a)) {
       const int* row = a.table + static_cast<int64_t>(walk.b) * a.table_b;
-      auto page_of = [&](int t) {
+      // page ids, a lane per box: 32 boxes ahead, and the 32 after them on their way
+      const int batch = 32 / boxes;  // tiles
+      auto pages_of = [&](int t) {
         const int pos = (walk.s.tile0 + t) * kTreeKeys + lane * a.box_rows;
         int page = -1;
-        if (lane < boxes && pos < walk.s.keys) {
+        if (pos < walk.s.keys) {
           page = row[pos >> a.page_shift];
-          if (page < 0 || page >= a.num_pages) {
-            atomicOr(&g_device_status, kStatusBadSeqlens);
-            page = static_cast<int>(a.num_pages);  // past the cache: the copy fills zeros
-          }
+          // past the cache: the copy fills zeros
+          if (page < 0 || page >= a.num_pages) page = static_cast<int>(a.num_pages);
         }
         return page;
       };
-      int page = page_of(walk.t0);
+      int pages = pages_of(walk.t0), next_pages = pages_of(walk.t0 + batch);
       for (int i = 0; ok && i < walk.nt; ++i, ++it) {
         const int t = walk.t0 + i;
-        const int next_page = i + 1 < walk.nt ? page_of(t + 1) : -1;
-        const bool copy = page >= 0;
+        const int in = i & (batch - 1);
+        if (in == 0 && i > 0) {
+          pages = next_pages;
+          next_pages = pages_of(t + batch);
+        }
+        const int page = __shfl_sync(~0u, pages, in * boxes + (lane & (boxes - 1)));
+        const bool copy = lane < boxes && page >= 0;
+        if (copy && page == a.num_pages) atomicOr(&g_device_status, kStatusBadSeqlens);
         const int n_copy = __popc(__ballot_sync(~0u, copy));
         const int r = ((walk.s.tile0 + t) * kTreeKeys + lane * a.box_rows) & (a.page_size - 1);
 #pragma unroll
@@ -707,7 +713,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
               tma_load_4d(dst + h * kTreeKeys * 128, kv ? &mv : &mk, f, h * 64, r, walk.hkv, page);
           }
         }
-        page = next_page;
       }
     }
     if (!ok) {
