@@ -134,8 +134,11 @@ struct TreeLayout {
   static constexpr int kRowsOff = kPOff + kBufs * kPBytes;
   static constexpr int kRowsBytes = (static_cast<int>(sizeof(TreeRows)) + 15) / 16 * 16;
   static constexpr int kMaxOff = kRowsOff + 2 * kRowsBytes;      // [4][kTreeRT][4] floats
-  static constexpr int kRefOff = kMaxOff + 4 * kTreeRT * 16;     // [4][kTreeRT] floats
-  static constexpr int kFacOff = kRefOff + 4 * kTreeRT * 4;      // [4][kTreeRT] floats
+  // what a piece leaves for its result, two pieces in turn (so that the
+  // warpgroups that do not write it out go on to the next)
+  static constexpr int kSumOff = kMaxOff + 4 * kTreeRT * 16;     // [2][4][kTreeRT][4] floats
+  static constexpr int kRefOff = kSumOff + 2 * 4 * kTreeRT * 16; // [2][4][kTreeRT] floats
+  static constexpr int kFacOff = kRefOff + 2 * 4 * kTreeRT * 4;  // [4][kTreeRT] floats
   static constexpr int kBucketOff = kFacOff + 4 * kTreeRT * 4;   // [kTreeBuckets] bytes
   static constexpr int kT5Off = kBucketOff + (BIAS ? kTreeBuckets : 0);  // [2][kTreeT5Slice] floats
   static constexpr int kMiscOff = kT5Off + (BIAS ? 2 * kTreeT5Slice * 4 : 0);
@@ -150,7 +153,7 @@ struct TreeLayout {
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;  // K and V in turn: even
   static constexpr int kSmem = kRingOff + kSlots * kTile;
   static constexpr int kOCol = kBufs * kN;                  // the O^T after the S buffers
-  static constexpr int kCols = kOCol + kTurns * kN;
+  static constexpr int kCols = kOCol + 2 * kTurns * kN;     // ... of two pieces
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kSlots >= 4 && kSmem <= kBudget, "shared memory budget");
   static_assert(kCols <= 512, "tensor memory budget");
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
             tc_fence_after();
             const uint64_t vd = dv + (slot_off(item) >> 4);
             const uint64_t pd = dp + ((L::kPOff + x * L::kPBytes) >> 4);
-            const uint32_t o = tmem + L::kOCol + (it % TN) * L::kN;
+            const uint32_t o = tmem + L::kOCol + ((u & 1) * TN + it % TN) * L::kN;
             const bool add = i >= TN;
 #pragma unroll
             for (int k = 0; k < kTreeKeys / kStep; ++k)
@@ -803,12 +806,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t turn = wg / RG;          // takes the tiles it = turn (mod TN)
     const int row0 = wg % RG * RT;          // first row of this thread's scores
-    const uint32_t t_o = tmem + lanes + L::kOCol + turn * L::kN + row0;
     constexpr uint32_t kTileThreads = 128 * RG;  // that work on one tile
     const uint32_t b_tile = RG == 1 ? 1 + wg : kTreeBarTurn + turn;
     float* wmax = reinterpret_cast<float*>(smem + L::kMaxOff);    // [4][RT][4 warps]
     float* mine = wmax + wg * RT * 4;
-    float* refs = reinterpret_cast<float*>(smem + L::kRefOff);    // [4][RT]
     float* facs = reinterpret_cast<float*>(smem + L::kFacOff);    // [4][RT]: what the last rescaling took
     // After a wait that ran out the warps go on without waiting, through the
     // same barriers, so that no thread is left at one.
@@ -825,6 +826,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     while (walk.next(a)) {
       const TreeSeq& s = walk.s;
       const TreeRows* info = reinterpret_cast<const TreeRows*>(smem + L::kRowsOff + (u & 1) * L::kRowsBytes);
+      const uint32_t t_all = tmem + lanes + L::kOCol + (u & 1) * TN * L::kN;  // the piece's O
+      const uint32_t t_o = t_all + turn * L::kN + row0;                       // this warpgroup's
+      float* refs = reinterpret_cast<float*>(smem + L::kRefOff) + (u & 1) * 4 * RT;  // [4][RT]
+      float* sums = reinterpret_cast<float*>(smem + L::kSumOff) + (u & 1) * 16 * RT; // [4][RT][4 warps]
       if (u == 0) {
         TreeRows* first = reinterpret_cast<TreeRows*>(smem + L::kRowsOff);
         tree_load_queries<D, FMT, R, BIAS>(a, walk, warp, kTreeSoftWarps, lane, smem + L::kQOff, first);
@@ -1143,7 +1148,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
 
       // ---- the piece's result: row sums over the warpgroup's keys, then O
       const float total = by_halves<RT>(l, lane, [](float x, float y) { return x + y; });
-      if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = total;
+      if ((lane & (32 / RT - 1)) == 0) sums[(wg * RT + lane / (32 / RT)) * 4 + (warp & 3)] = total;
       // the last P V of this warpgroup's O
       if (!fresh) values_done(it - 1 - ((it - 1 - turn) & (TN - 1)));
       constexpr uint32_t kMeet = TN == 1 ? 128 : kTreeSoftWarps * 32;  // threads whose results meet
@@ -1154,7 +1159,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
 
       const bool whole = walk.t0 == 0 && walk.nt == s.tiles;
       const int slot = walk.t0 == 0 ? 1 : 0;  // 0: began in an earlier CTA
-      const int out0 = wg * RO;               // first row that this thread writes
+      // first row that this thread writes; at 16 rows two warpgroups do, in turn
+      const int out0 = (R == 16 ? wg ^ ((u & 1) << 1) : wg) * RO;
       const int n_rows = min(R, s.n * a.G - walk.block * R) - out0;  // from there on, may exceed RO
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + out0;
       const int sets = min(walk.nt, TN);      // that had tiles, from the first tile's on
@@ -1174,15 +1180,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           const int t = (it - walk.nt + k) & (TN - 1);
           const int at = (t * RG + row / RT) * RT + row % RT;  // in the warpgroups' arrays
           float o2[8];
-          tmem_ld_cols<8>(tmem + lanes + L::kOCol + t * L::kN + row, o2);
+          tmem_ld_cols<8>(t_all + t * L::kN + row, o2);
           if constexpr (E4) {
             float rest[8];
-            tmem_ld_cols<8>(tmem + lanes + L::kOCol + t * L::kN + R + row, rest);
+            tmem_ld_cols<8>(t_all + t * L::kN + R + row, rest);
             fma_rows<8>(rest, 1.f / kWeightRest, o2);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float4 l4 = *reinterpret_cast<const float4*>(wmax + (at + j) * 4);
+            const float4 l4 = *reinterpret_cast<const float4*>(sums + (at + j) * 4);
             const float r2 = refs[at + j];
             const float top = fmaxf(rr[j], r2);
             const float f1 = fast_exp2(rr[j] - top), f2 = fast_exp2(r2 - top);
@@ -1217,8 +1223,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           }
         }
       }
+      // (the sums, references and O of this piece are written again two pieces
+      // on, after the meeting at the next one's end)
       tc_fence_before();
-      named_barrier(b_meet, kMeet);  // O, the sums and the references are read
+      __syncwarp();
       if (lane == 0) mbar_arrive(q_free(u & 1));
       ++u;
     }
