@@ -225,17 +225,23 @@ cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const CUtensor
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // a (sequence, head) of one tile cannot span CTAs
-  if (a.width * a.page_size <= kTreeKeys) return cudaSuccess;
+  if (a.width * a.page_size <= kTreeKeys || grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((a.max_nodes * a.Hq + kTreeJoinWarps - 1) / kTreeJoinWarps, a.B);
-  cfg.blockDim = dim3(kTreeJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, R>, a, grid);
+  if (a.B <= 32) {
+    cfg.gridDim = dim3((a.max_nodes * a.Hq + kTreeJoinWarps - 1) / kTreeJoinWarps, a.B);
+    cfg.blockDim = dim3(kTreeJoinWarps * 32);
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, R>, a, grid);
+  }
+  const int rows = std::min(a.max_nodes * a.G, R);  // of a block at most
+  cfg.gridDim = dim3((rows + kTreeCutWarps - 1) / kTreeCutWarps, grid - 1);
+  cfg.blockDim = dim3(kTreeCutWarps * 32);
+  return cudaLaunchKernelEx(&cfg, tree_join_cuts_kernel<D, R>, a, grid);
 }
 
 // Query rows of one product: the smallest of 16, 32 and 64 that holds a

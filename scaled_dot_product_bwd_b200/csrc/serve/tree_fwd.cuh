@@ -230,6 +230,109 @@ struct TreeWalk {
 // A CTA's part of a line of `total` (which the host keeps below 2^31 - 2^16).
 __device__ __forceinline__ int tree_share(int total, int ctas) { return (total + ctas - 1) / ctas; }
 
+// Where the part of a CTA begins: `left` tiles and piece costs from `off` in
+// sequence b on (nothing: left = 0).
+struct TreeSpot {
+  int left, per, cost;
+  int b, off;
+  TreeSeq s;
+};
+
+// The part of CTA `cta` of `ctas`, into shared memory, by one warp: up to 32
+// sequences, a lane each.
+template <int R>
+__device__ __forceinline__ void tree_locate(const TreeArgs& a, int cta, int ctas, int lane, TreeSpot* out) {
+  TreeSeq s{};
+  if (lane < a.B) s = tree_seq<R>(a, lane);
+  const int tiles = __reduce_add_sync(~0u, lane < a.B ? s.units(a.Hkv, 0) : 0);
+  const int pieces = __reduce_add_sync(~0u, lane < a.B ? s.rb * a.Hkv : 0);
+  const int cost = tree_piece_cost(tiles, ctas);
+  const int total = tiles + cost * pieces;
+  const int per = tree_share(total, ctas);
+  const int from = static_cast<int>(min(static_cast<int64_t>(per) * cta, static_cast<int64_t>(total)));
+  if (lane == 0) {
+    out->left = min(total - from, per);
+    out->per = per;
+    out->cost = cost;
+  }
+  const int units = lane < a.B ? s.units(a.Hkv, cost) : 0;
+  int upto = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (upto - units <= from && from < upto) {
+    out->b = lane;
+    out->off = from - (upto - units);
+    out->s = s;
+  }
+}
+
+// The same for any number of sequences, by all NW warps of a block (`totals`:
+// 2 * NW ints of shared memory; it may be read once all of the block are
+// through a barrier).  Each warp adds up a range of its own, then each goes
+// through the one range that holds the place.  Out of line: inlined it would
+// hold up the setup of those that do not come here.
+template <int R, int NW>
+__device__ __noinline__ void tree_locate_many(const TreeArgs& a, int cta, int ctas, int warp, int lane, int* totals,
+                                              TreeSpot* out) {
+  const int range = ((a.B + NW - 1) / NW + 31) / 32 * 32;
+  int tiles = 0, pieces = 0;
+  for (int b = warp * range + lane; b < min(a.B, (warp + 1) * range); b += 32) {
+    const TreeSeq s = tree_seq<R>(a, b);
+    tiles += s.units(a.Hkv, 0);
+    pieces += s.rb * a.Hkv;
+  }
+  tiles = __reduce_add_sync(~0u, tiles);
+  pieces = __reduce_add_sync(~0u, pieces);
+  if (lane == 0) {
+    totals[2 * warp] = tiles;
+    totals[2 * warp + 1] = pieces;
+  }
+  __syncthreads();
+  const int mine_t = lane < NW ? totals[2 * lane] : 0, mine_p = lane < NW ? totals[2 * lane + 1] : 0;
+  tiles = __reduce_add_sync(~0u, mine_t);
+  pieces = __reduce_add_sync(~0u, mine_p);
+  const int cost = tree_piece_cost(tiles, ctas);
+  const int total = tiles + cost * pieces;
+  const int per = tree_share(total, ctas);
+  const int from = static_cast<int>(min(static_cast<int64_t>(per) * cta, static_cast<int64_t>(total)));
+  if (threadIdx.x == 0) {
+    out->left = min(total - from, per);
+    out->per = per;
+    out->cost = cost;
+  }
+  int upto = mine_t + cost * mine_p;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const uint32_t holds = __ballot_sync(~0u, lane < NW && from < upto);
+  const int w = holds ? __ffs(holds) - 1 : NW;
+  if (w != warp) return;  // one warp stays, or none: nothing left for this CTA
+  int base = __shfl_sync(~0u, upto - (mine_t + cost * mine_p), w);
+  for (int b0 = w * range; b0 < min(a.B, (w + 1) * range); b0 += 32) {
+    const int b = b0 + lane;
+    TreeSeq s{};
+    if (b < a.B) s = tree_seq<R>(a, b);
+    const int units = b < a.B ? s.units(a.Hkv, cost) : 0;
+    int end = base + units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, end - base, o);
+      if (lane >= o) end += y;
+    }
+    if (end - units <= from && from < end) {
+      out->b = b;
+      out->off = from - (end - units);
+      out->s = s;
+    }
+    base = __shfl_sync(~0u, end, 31);
+  }
+}
+
 // ------------------------------------------------- operands of the products
 // Shared-memory matrix descriptor of a layout: 0 plain, 2 128-byte swizzle,
 // 4 64-byte swizzle.  A K-major operand steps 8 rows by sbo; an MN-major one
@@ -576,11 +679,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   uint32_t* dirty = reinterpret_cast<uint32_t*>(misc + 80);   // [4 turns][4] bits of keys
-  int* start_left = reinterpret_cast<int*>(misc + 12);
-  int* start_b = reinterpret_cast<int*>(misc + 40);
-  int* start_off = reinterpret_cast<int*>(misc + 44);
-  int* start_cost = reinterpret_cast<int*>(misc + 8);
-  TreeSeq* start_seq = reinterpret_cast<TreeSeq*>(misc + 48);  // 28 bytes
+  TreeSpot* spot = reinterpret_cast<TreeSpot*>(misc + 16);  // 48 bytes
 
   if (warp == kTreeIssueS) {
     if (lane == 0) {
@@ -609,51 +708,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   } else if (warp == kTreeProducer) {
-    // the line of tiles: its length, and where this CTA's part begins
-    TreeSeq s{};
-    int tiles = 0, pieces = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane;
-      if (b < a.B) {
-        s = tree_seq<R>(a, b);
-        tiles += s.units(a.Hkv, 0);
-        pieces += s.rb * a.Hkv;
-      }
-    }
-    tiles = __reduce_add_sync(~0u, tiles);
-    pieces = __reduce_add_sync(~0u, pieces);
-    const int cost = tree_piece_cost(tiles, gridDim.x);
-    const int total = tiles + cost * pieces;
-    const int per = tree_share(total, gridDim.x);
-    const int from = min(per * static_cast<int>(blockIdx.x), total);
-    if (lane == 0) {
-      *start_left = min(total - from, per);
-      *start_cost = cost;
-    }
-    int base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane;
-      if (a.B > 32 && b < a.B) s = tree_seq<R>(a, b);  // else the first pass's are at hand
-      const int units = b < a.B ? s.units(a.Hkv, cost) : 0;
-      int upto = units;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += y;
-      }
-      const int before = base + upto - units;
-      if (b < a.B && before <= from && from < before + units) {
-        *start_b = b;
-        *start_off = from - before;
-        *start_seq = s;
-      }
-      base += __shfl_sync(~0u, upto, 31);
-      if (base > from) break;
-    }
+    if (a.B <= 32) tree_locate<R>(a, blockIdx.x, gridDim.x, lane, spot);
   } else if (BIAS != 0 && warp < kTreeSoftWarps && a.t5_table) {
     for (int i = tid; i < kTreeBuckets; i += kTreeSoftWarps * 32)
       smem[L::kBucketOff + i] = static_cast<uint8_t>(t5_bucket(i - kTreeNear, a.t5));
   }
+  if (a.B > 32)
+    tree_locate_many<R, kTreeThreads / 32>(a, blockIdx.x, gridDim.x, warp, lane,
+                                           reinterpret_cast<int*>(smem + L::kRingOff), spot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -661,11 +723,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{abort_flag, a.wait_limit_ns};
   TreeWalk<R> walk;
-  walk.left = *start_left;
-  walk.b = *start_b;
-  walk.off = *start_off;
-  walk.s = *start_seq;
-  walk.cost = *start_cost;
+  walk.left = spot->left;
+  walk.cost = spot->cost;
+  walk.b = spot->b;
+  walk.off = spot->off;
+  walk.s = spot->s;
   walk.units = walk.s.units(a.Hkv, walk.cost);
 
   if (warp == kTreeProducer) {
@@ -825,7 +887,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     };
     while (walk.next(a)) {
       const TreeSeq& s = walk.s;
-      const TreeRows* info = reinterpret_cast<const TreeRows*>(smem + L::kRowsOff + (u & 1) * L::kRowsBytes);
       const uint32_t t_all = tmem + lanes + L::kOCol + (u & 1) * TN * L::kN;  // the piece's O
       const uint32_t t_o = t_all + turn * L::kN + row0;                       // this warpgroup's
       float* refs = reinterpret_cast<float*>(smem + L::kRefOff) + (u & 1) * 4 * RT;  // [4][RT]
@@ -842,6 +903,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       } else {
         wait(q_full(u & 1), (u >> 1) & 1);
       }
+      // (after an abort: the first buffer, which has been filled and holds
+      // addresses of this call)
+      const TreeRows* info =
+          reinterpret_cast<const TreeRows*>(smem + L::kRowsOff + (ok ? (u & 1) * L::kRowsBytes : 0));
       float ref[RT], l[RT];
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
@@ -944,7 +1009,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
                 int at[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                  at[j] = buckets[max(key_pos - info->pos[row0 + j0 + j], -kTreeNear) + kTreeNear];
+                  at[j] = buckets[min(max(key_pos - info->pos[row0 + j0 + j], -kTreeNear), 63) + kTreeNear];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sc[j0 + j] += slice[at[j] * a.G + info->head[row0 + j0 + j] - head0];
               }
@@ -953,7 +1018,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
 #pragma unroll
               for (int j = 0; j < RT; ++j) {
                 const int rel = key_pos - info->pos[row0 + j];
-                const int k = rel < -kTreeNear ? t5_bucket(rel, a.t5) : buckets[rel + kTreeNear];
+                const int k = rel < -kTreeNear ? t5_bucket(rel, a.t5) : buckets[min(rel, 63) + kTreeNear];
                 sc[j] += bias_to_log2(a.t5_table[k * a.Hq + info->head[row0 + j]]);
               }
             }
@@ -1167,7 +1232,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       // (rolled: straight-line code that runs once per piece would wait for
       // its instructions longer than it runs)
 #pragma unroll 1
-      for (int j0 = 0; j0 < min(RO, n_rows); j0 += 8) {
+      for (int j0 = 0; ok && j0 < min(RO, n_rows); j0 += 8) {
         const int row = out0 + j0;
         float o[8], sum[8], rr[8];
 #pragma unroll
@@ -1239,51 +1304,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   }
 }
 
-// Joins the pieces of (row, head)s that span CTAs, in the CTAs' order.  One
-// warp per query row and head; the lanes first weigh up to 32 pieces at once,
-// then add them, D / 32 columns each.
-constexpr int kTreeJoinWarps = 4;
-
-template <int D, int R>
-__global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a,
-                                                                       int ctas) {
+// One warp joins the pieces of query row `in` of a (sequence, head, row block)
+// that CTAs c0 .. c1 have parts of, in their order.  The lanes first weigh up
+// to 32 pieces at once, then add them, D / 32 columns each.
+template <int D, int R, int U>
+__device__ __forceinline__ void tree_join_row(const TreeArgs& a, int lane, int c0, int c1, int in, int row, int h) {
   constexpr int W = D / 32;
-  const int b = blockIdx.y;
-  const int lane = threadIdx.x & 31;
-  const int x = blockIdx.x * kTreeJoinWarps + (threadIdx.x >> 5);  // node * Hq + head
-  // all that the lengths decide, while the pieces are still being computed
-  const TreeSeq s = tree_seq<R>(a, b);
-  int tiles = 0, pieces = 0, tiles_before = 0, pieces_before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    if (b0 + lane >= a.B) continue;
-    const TreeSeq other = tree_seq<R>(a, b0 + lane);
-    const int t = other.units(a.Hkv, 0), p = other.rb * a.Hkv;
-    tiles += t;
-    pieces += p;
-    if (b0 + lane < b) {
-      tiles_before += t;
-      pieces_before += p;
-    }
-  }
-  tiles = __reduce_add_sync(~0u, tiles);
-  pieces = __reduce_add_sync(~0u, pieces);
-  tiles_before = __reduce_add_sync(~0u, tiles_before);
-  pieces_before = __reduce_add_sync(~0u, pieces_before);
-  const int n = x / a.Hq, h = x - n * a.Hq;
-  const int hkv = h / a.G;
-  const int r = n * a.G + (h - hkv * a.G);
-  const int block = r / R, in = r - block * R;
-  int c0 = 0, c1 = 0;
-  if (n < s.n) {
-    const int cost = tree_piece_cost(tiles, ctas);
-    const int per = tree_share(tiles + cost * pieces, ctas);
-    const int first = tiles_before + cost * pieces_before + (hkv * s.rb + block) * (cost + s.tiles) + cost;
-    c0 = first / per;
-    c1 = (first + s.tiles - 1) / per;
-  }
-  // (every thread waits, so that what follows this kernel follows the first too)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c0 == c1) return;
   float ref = -FLT_MAX, l = 0.f, acc[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) acc[i] = 0.f;
@@ -1303,7 +1329,7 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
 #pragma unroll
     for (int i = 0; i < W; ++i) acc[i] *= f_old;
     const int count = min(32, c1 - base + 1);
-#pragma unroll 16
+#pragma unroll U
     for (int j = 0; j < count; ++j) {
       const int cj = base + j;
       const float w = __shfl_sync(~0u, f, j);
@@ -1322,13 +1348,92 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
     }
   }
   const float inv = l > 0.f || isnan(l) ? 1.f / l : 0.f;
-  __nv_bfloat16* dst = a.o + static_cast<int64_t>(s.row0 + n) * a.o_t + static_cast<int64_t>(h) * a.o_h + lane * W;
+  __nv_bfloat16* dst = a.o + static_cast<int64_t>(row) * a.o_t + static_cast<int64_t>(h) * a.o_h + lane * W;
   if constexpr (W == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + s.row0 + n] = (ref + log2f(l)) * kLn2;
+  if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + row] = (ref + log2f(l)) * kLn2;
+}
+
+// Up to 32 sequences: a warp per (node, head), which finds where its piece of
+// the line lies.
+constexpr int kTreeJoinWarps = 4;
+
+template <int D, int R>
+__global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a,
+                                                                       int ctas) {
+  const int b = blockIdx.y;
+  const int lane = threadIdx.x & 31;
+  const int x = blockIdx.x * kTreeJoinWarps + (threadIdx.x >> 5);  // node * Hq + head
+  // all that the lengths decide, while the pieces are still being computed
+  const TreeSeq s = tree_seq<R>(a, b);
+  int tiles = 0, pieces = 0;
+  if (lane < a.B) {
+    const TreeSeq other = tree_seq<R>(a, lane);
+    tiles = other.units(a.Hkv, 0);
+    pieces = other.rb * a.Hkv;
+  }
+  const int tiles_before = __reduce_add_sync(~0u, lane < b ? tiles : 0);
+  const int pieces_before = __reduce_add_sync(~0u, lane < b ? pieces : 0);
+  tiles = __reduce_add_sync(~0u, tiles);
+  pieces = __reduce_add_sync(~0u, pieces);
+  const int n = x / a.Hq, h = x - n * a.Hq;
+  const int hkv = h / a.G;
+  const int r = n * a.G + (h - hkv * a.G);
+  const int block = r / R, in = r - block * R;
+  int c0 = 0, c1 = 0;
+  if (n < s.n) {
+    const int cost = tree_piece_cost(tiles, ctas);
+    const int per = tree_share(tiles + cost * pieces, ctas);
+    const int first = tiles_before + cost * pieces_before + (hkv * s.rb + block) * (cost + s.tiles) + cost;
+    c0 = first / per;
+    c1 = (first + s.tiles - 1) / per;
+  }
+  // (every thread waits, so that what follows this kernel follows the first too)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 != c1) tree_join_row<D, R, 16>(a, lane, c0, c1, in, s.row0 + n, h);
+}
+
+// More sequences: most of their pieces lie inside one CTA's part of the line,
+// and each warp of the form above would go through all lengths for nothing.
+// Here blockIdx.y + 1 names a CTA; if its part begins inside a piece that began
+// in the CTA before, that piece is joined, a warp per query row.  Measured with
+// the search of the lengths in one warp and the form above against this: 1000
+// sequences of 1 node over 500 keys 633 -> 578 us, 256 of 8 nodes over 1000 keys
+// 255 -> 217, 256 of 1 node 193 -> 195, 64 of 1 node 64 -> 67.
+// (32 registers and no more: a block has to find room beside the first
+// kernel's, to be waiting when it ends.)
+constexpr int kTreeCutWarps = 4;
+
+template <int D, int R>
+__global__ void __launch_bounds__(kTreeCutWarps * 32, 16) tree_join_cuts_kernel(const __grid_constant__ TreeArgs a,
+                                                                           int ctas) {
+  __shared__ int totals[2 * kTreeCutWarps];
+  __shared__ TreeSpot spot;
+  const int cut = blockIdx.y + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int in = blockIdx.x * kTreeCutWarps + warp;  // row of the block
+  tree_locate_many<R, kTreeCutWarps>(a, cut, ctas, warp, lane, totals, &spot);
+  __syncthreads();
+  int c0 = 0, c1 = 0, row = 0, h = 0;
+  if (spot.left > 0) {
+    const TreeSeq& s = spot.s;
+    const int span = spot.cost + s.tiles;
+    const int seg = spot.off / span;
+    const int done = spot.off - seg * span - spot.cost;  // its tiles before the cut
+    const int hkv = seg / s.rb;
+    const int r = (seg - hkv * s.rb) * R + in;
+    if (done > 0 && done <= spot.per && r < s.n * a.G) {  // begun in CTA cut - 1
+      c0 = cut - 1;
+      c1 = cut + (s.tiles - done - 1) / spot.per;
+      row = s.row0 + r / a.G;
+      h = hkv * a.G + r % a.G;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 != c1) tree_join_row<D, R, 4>(a, lane, c0, c1, in, row, h);
 }
 
 }  // namespace sdpa
