@@ -208,7 +208,7 @@ sdpa_status_t sdpa_tree_fwd(const sdpa_tree* tree, const sdpa_kv_cache* cache, c
  * Weights, sums and comparisons are float64, so a tie is a tie of the given
  * numbers.  Without children this samples from target[0].
  *   target, draft: device float32 [B, N, V], element strides *_b, *_n (V
- *     contiguous); N = 1: draft may be NULL.  1 <= N <= 64, 1 <= V < 2^31.
+ *     contiguous); N = 1: draft may be NULL.  1 <= N <= 64, 1 <= V < 2^30.
  *   tokens, parents: device int32 [B, N] contiguous; tokens[0], parents[0] and
  *     u_accept[0] are not read; parents NULL: a chain (parents[n] = n - 1).
  *     A token outside [0, V) is never accepted and removes draft[at] from w as

@@ -527,7 +527,7 @@ sdpa_status_t sdpa_tree_fwd(const sdpa_tree* t, const sdpa_kv_cache* cache, cons
 sdpa_status_t sdpa_spec_verify(const sdpa_verify* s, int32_t* path, int32_t* accepted,
                                int32_t* next_token, void* stream) {
   if (!s || s->B < 1 || s->N < 1 || s->V < 1) return SDPA_ERR_INVALID_ARG;
-  if (s->N > kVerifyMaxNodes || s->V >= (1ll << 31) || s->B > (1ll << 24)) return SDPA_ERR_UNSUPPORTED;
+  if (s->N > kVerifyMaxNodes || s->V >= (1ll << 30) || s->B > (1ll << 24)) return SDPA_ERR_UNSUPPORTED;
   if (!s->target || !s->u_sample || !path || !accepted || !next_token) return SDPA_ERR_INVALID_ARG;
   if (s->N > 1 && (!s->draft || !s->tokens || !s->u_accept)) return SDPA_ERR_INVALID_ARG;
   const void* ptrs[] = {s->target, s->draft, s->tokens, s->parents, s->u_accept, s->u_sample,

@@ -84,6 +84,9 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
   // every warp's sum of the cluster, by two passes in turn
   __shared__ double sums[2][kVerifyMaxCluster * kVerifyWarps];
 
+  // (a CTA's shared memory may be written to once it has started: arrived at
+  // here, waited for after the nodes' loads)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (tid < kVerifyMaxNodes) kids[tid] = 0;
   __syncthreads();
   if (tid < 64) {
@@ -113,6 +116,7 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
     if (lane == 0) first_ok[warp] = w;
   }
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   const unsigned long long ok_first = first_ok[0] | (static_cast<unsigned long long>(first_ok[1]) << 32);
 
   const int chunk = (a.V + C - 1) / C;

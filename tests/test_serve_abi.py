@@ -220,3 +220,9 @@ def test_binding_refuses_host_tensors():
                  lambda: serve.sdpa_spec_verify(torch.zeros(1, 1, 9), None, None, None, None, torch.zeros(1))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_verify_refuses_a_vocabulary_whose_indices_could_wrap(lib):
+    for v in (1 << 30, (1 << 31) - 1):
+        s = _verify(V=v, target_n=v, target_b=4 * v, draft_n=v, draft_b=4 * v)
+        assert lib.sdpa_spec_verify(ctypes.byref(s), FAKE, FAKE, FAKE, None) == 2
