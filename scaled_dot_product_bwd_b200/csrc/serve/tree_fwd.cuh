@@ -53,6 +53,7 @@
 
 namespace sdpa {
 
+constexpr uint64_t kTreeDrainNs = 1000000000ull;  // for what is in flight when a wait has run out
 constexpr int kTreeMaxCtas = 148;   // one per SM; the workspace is sized for it
 constexpr int kTreeMaxNodes = 64;
 constexpr int kTreeMaxRows = 64;    // query rows of one product
@@ -783,7 +784,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     if (!ok) {
       // a wait that ran out ends the CTA: let the copies in flight land first
       volatile int never = 0;
-      const WaitCtl ign{&never, a.wait_limit_ns};
+      const WaitCtl ign{&never, max(a.wait_limit_ns, kTreeDrainNs)};
       for (uint32_t j = item > NS ? item - NS : 0; j < item; ++j) mbar_wait(full(j % NS), (j / NS) & 1, ign);
     }
   } else if (warp == kTreeQuery) {
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       }
       // every MMA issued is done before tensor memory is freed
       volatile int never = 0;
-      const WaitCtl ign{&never, a.wait_limit_ns};
+      const WaitCtl ign{&never, max(a.wait_limit_ns, kTreeDrainNs)};
       mma_commit(drain(is_s ? 0 : 1));
       mbar_wait(drain(is_s ? 0 : 1), 0, ign);
     }
@@ -994,6 +995,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
             for (int j = 0; j < RT; ++j)
               sc[j] += bias_to_log2(-info->bias[row0 + j] *
                                     fabsf(static_cast<float>(key_pos - info->pos[row0 + j])));
+          } else if (!ok) {
+            // (after an abort the rows may be another piece's: no lookups by them)
           } else if (key0 + kTreeKeys - 1 - s.ctx <= a.t5.one_lo_max) {
             // every distance of the tile in the last bucket
 #pragma unroll
