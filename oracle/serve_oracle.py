@@ -104,7 +104,7 @@ def t5_bucket(rel, num_buckets=32, max_distance=128, bidirectional=False):
 
 
 def tree_attention(q, k, v, ctx, mask=None, window_left=-1, alibi_slopes=None, t5_table=None,
-                   t5_bidirectional=False, scale=None):
+                   t5_bidirectional=False, scale=None, t5_num_buckets=32, t5_max_distance=128):
     """One sequence's nodes q [n, Hq, d] over rows k, v [ctx + n, Hkv, d]; mask: n integers (bit
     j: sees node j), None: a chain.  Returns O, LSE [n, Hq], and per entry the sum of
     weight * |v| and the largest sum of |q k| of a row (for tolerances)."""
@@ -133,7 +133,7 @@ def tree_attention(q, k, v, ctx, mask=None, window_left=-1, alibi_slopes=None, t
                 s = s - float(alibi_slopes[h]) * np.abs(rel[i, on])
             if t5_table is not None:
                 s = s + np.asarray(t5_table, dtype=np.float64)[
-                    t5_bucket(rel[i, on], bidirectional=t5_bidirectional), h]
+                    t5_bucket(rel[i, on], t5_num_buckets, t5_max_distance, t5_bidirectional), h]
             top = s.max()
             p = np.exp(s - top)
             lse[i, h] = top + math.log(p.sum())

@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <stdexcept>
 #include <string>
 
@@ -59,6 +60,15 @@ double number(PyObject* o, const char* name) {
     refuse(std::string(name) + " must be a number");
   }
   return v;
+}
+
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be a bool");
+  }
+  return v != 0;
 }
 
 // Every tensor on one GPU, the current one; its current stream.
@@ -217,12 +227,12 @@ PyObject* rope(PyObject* const* a) {
     strides(ok, r.ko_b, r.ko_l, r.ko_h);
     r.Hkv = k->size(dims - 2);
   }
-  if (q.numel() != 0) {
+  if (r.B != 0 && r.L != 0) {
     r.offset = integer(a[6], "offset");
     r.freqs = freqs.data_ptr<double>();
     r.rot = static_cast<int32_t>(std::min<int64_t>(2 * freqs.numel(), 1 << 20));
-    r.interleaved = PyObject_IsTrue(a[7]);
-    r.inverse = PyObject_IsTrue(a[8]);
+    r.interleaved = truth(a[7], "interleaved");
+    r.inverse = truth(a[8], "inverse");
     r.amplitude = static_cast<float>(number(a[9], "amplitude"));
     check(sdpa_rope(&r, q.data_ptr(), k ? k->data_ptr() : nullptr, oq.data_ptr(), k ? ok.data_ptr() : nullptr, stream),
           "sdpa_rope");
@@ -316,8 +326,8 @@ PyObject* tree(PyObject* const* a) {
     const int64_t nb = integer(a[12], "t5_num_buckets");
     bias.ptr = vec<float>(*t5, "t5_table", at::kFloat, {nb, t.Hq});
     bias.num_buckets = static_cast<int32_t>(nb);
-    bias.max_distance = static_cast<int32_t>(std::min<int64_t>(integer(a[13], "t5_max_distance"), 1 << 30));
-    bias.bidirectional = PyObject_IsTrue(a[14]);
+    bias.max_distance = static_cast<int32_t>(std::clamp<int64_t>(integer(a[13], "t5_max_distance"), 0, 1 << 30));
+    bias.bidirectional = truth(a[14], "t5_bidirectional");
   } else if (slopes) {
     bias.kind = SDPA_BIAS_ALIBI;
     bias.ptr = vec<float>(*slopes, "alibi_slopes", at::kFloat, {t.Hq});

@@ -624,3 +624,96 @@ def test_generation_steps(kv):
     # a prompt chunk over its cached prefix equals the whole prompt's attention
     whole, _ = sdpa_fwd(*(x[None] for x in (randn(g, total, hq, d), kc, vc)), causal=True)
     assert torch.isfinite(whole.float()).all()
+
+
+# ------------------------------------------------- larger batches, odd calls
+@pytest.mark.parametrize("T,hkv,d,page", [(50, 40, 128, 16), (33, 17, 64, 32), (9, 33, 64, 128), (2100, 5, 64, 16)])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_append_and_gather_head_counts(T, hkv, d, page, kv):
+    test_append_and_gather(T, hkv, d, page, kv)
+
+
+MANY = {
+    "33": dict(lens=[7 * i % 100 for i in range(33)], counts=[1] * 33, hq=4, hkv=2, d=64, page=16),
+    "64_long_one": dict(lens=[20] * 20 + [15000] + [130] * 43, counts=[1] * 64, hq=4, hkv=1, d=128, page=64),
+    "70_trees": dict(lens=[53 * i % 400 for i in range(70)], counts=[i % 6 for i in range(70)], hq=8, hkv=2, d=64, page=32),
+    "300": dict(lens=[31 * i % 257 for i in range(300)], counts=[(i + 1) % 3 for i in range(300)], hq=4, hkv=4, d=64, page=16),
+    "700_one_node_each_third": dict(lens=[5] * 700, counts=[int(i % 3 == 0) for i in range(700)], hq=2, hkv=1, d=64, page=16),
+    "40_empty": dict(lens=[0] * 40, counts=[0] * 39 + [2], hq=2, hkv=2, d=64, page=16),
+}
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("name", list(MANY))
+def test_tree_many_sequences(name, kv):
+    cache, q, args, mask, seqs, cu, masks = tree_setup(kv=kv, extra_rows=1, **MANY[name])
+    o, lse = sdpa_tree_fwd(q, tree_mask=mask, **args, **cache)
+    check_tree(o, lse, q, seqs, cu, kv, masks)
+    again = sdpa_tree_fwd(q, tree_mask=mask, **args, **cache)
+    assert torch.equal(o[:cu[-1]], again[0][:cu[-1]]) and torch.equal(lse[:, :cu[-1]], again[1][:, :cu[-1]])
+    assert sdpa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_tree_many_row_blocks(kv):
+    """64 nodes of 32 query heads over one KV head: 2048 rows against the same keys."""
+    cache, q, args, mask, seqs, cu, masks = tree_setup([300, 5], [64, 64], 32, 1, 64, 16, kv)
+    o, lse = sdpa_tree_fwd(q, tree_mask=mask, window_left=120, **args, **cache)
+    check_tree(o, lse, q, seqs, cu, kv, masks, window_left=120)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("buckets,distance,bidir,ctx,hq,hkv", [
+    (128, 200, False, 1500, 16, 1),     # a table of 2048 entries per KV head
+    (32, 5000, False, 6000, 4, 2),      # buckets that go on behind the tabulated distances
+    (128, 3000, True, 4000, 16, 1),     # both
+    (4, 3, False, 200, 2, 2), (2, 2, False, 200, 2, 2), (6, 100000, True, 1200, 2, 1)])
+def test_tree_t5_tables(buckets, distance, bidir, ctx, hq, hkv, kv):
+    cache, q, args, mask, seqs, cu, masks = tree_setup([ctx, 40], [5, 9], hq, hkv, 64, 32, kv)
+    t = torch.randn(buckets, hq, generator=torch.Generator().manual_seed(buckets))
+    kw = dict(t5_num_buckets=buckets, t5_max_distance=distance, t5_bidirectional=bidir)
+    o, lse = sdpa_tree_fwd(q, tree_mask=mask, t5_table=t.to(DEV), **kw, **args, **cache)
+    check_tree(o, lse, q, seqs, cu, kv, masks, t5_table=t.numpy(), **kw)
+
+
+def test_tree_e4m3_offsets_past_32_bits():
+    """Three pages of e4m3 rows 2^31 + 4096 elements apart, their scales 2^32 bytes apart."""
+    hkv, page, d, far = 2, 32, 64, 2 ** 31 + 4096
+    codes = torch.empty(2, 2 * far + hkv * page * d, device=DEV, dtype=torch.uint8)
+    scales = torch.empty(2, 2 ** 33 + hkv * page, device=DEV, dtype=torch.uint8)
+    rows = lambda i: codes[i].as_strided((3, hkv, page, d), (far, page * d, d, 1)).view(torch.float8_e4m3fn)
+    sc = lambda i: scales[i].as_strided((3, hkv, page), (2 ** 32, page, 1))
+    cache = dict(k_cache=rows(0), v_cache=rows(1), k_scale=sc(0), v_scale=sc(1))
+    g = torch.Generator().manual_seed(5)
+    n = 90
+    table = torch.tensor([[2, 0, 1]], device=DEV, dtype=torch.int32)
+    flat = table[0].long().repeat_interleave(page)[:n] * page + torch.arange(n, device=DEV) % page
+    k, v, q = randn(g, n, hkv, d), randn(g, n, hkv, d), randn(g, 1, 4, d)
+    sdpa_cache_append(k, v, flat, **cache)
+    i32 = lambda *x: torch.tensor(x, device=DEV, dtype=torch.int32)
+    kg, vg = sdpa_cache_gather(page_table=table, cu_seqlens=i32(0, n), total=n, **cache)
+    o, lse = sdpa_tree_fwd(q, page_table=table, ctx_lens=i32(n - 1), cu_nodes=i32(0, 1), max_nodes=1, **cache)
+    # (the rows read back are exact: test_append_and_gather; here against the rows written, 2^-4 off at most)
+    assert ((kg.double() - k.double()).abs() <= 2.0 ** -4 * k.double().abs() + 2.0 ** -10 * 2.0 ** -5).all()
+    check_tree(o, lse, q, [(f64(kg), f64(vg), n - 1)], [0, 1], "e4m3")
+
+
+def test_verify_large_vocabulary_and_batch():
+    g = torch.Generator().manual_seed(31)
+    for B, N, V in ((2, 3, 200003), (600, 2, 130), (1, 2, 32769)):
+        check_verify(*draw_tree(g, B, N, V))
+
+
+def test_odd_arguments_are_refused():
+    q = torch.randn(1, 2, 0, 64, device=DEV).bfloat16()
+    k = torch.randn(1, 2, 2, 64, device=DEV).bfloat16()
+    freqs, _ = sdpa_rope_frequencies(64)
+    with pytest.raises(SdpaError):
+        sdpa_rope(q, k, freqs)                                  # no query head, yet keys to turn
+    for name in ("interleaved", "inverse"):
+        with pytest.raises(ValueError):
+            sdpa_rope(k, None, freqs, **{name: torch.zeros(2)})
+    cache, q, args, *_ = tree_setup([40], [2], 2, 2, 64, 16, "bf16")
+    for far in (-2 ** 32 + 200, -1, 0, 8):
+        with pytest.raises(SdpaError):
+            sdpa_tree_fwd(q, t5_table=torch.zeros(32, 2, device=DEV), t5_max_distance=far, **args, **cache)
