@@ -92,7 +92,7 @@ def _bind_flags():
     return (["-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
             + [x for i in inc for x in ("-isystem" if "sdpa" not in i and i != INCLUDE else "-I", i)],
-            ["-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            ["-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch", "-ltorch_cpu", "-lc10",
              "-lc10_cuda", "-L" + PKG, "-l:libsdpa_serve_b200.so", "-Wl,-rpath,$ORIGIN"])
 
 

@@ -554,6 +554,7 @@ sdpa_status_t sdpa_spec_verify(const sdpa_verify* s, int32_t* path, int32_t* acc
   a.path = path;
   a.accepted = accepted;
   a.next_token = next_token;
+  a.wait_limit_ns = g_wait_limit_ns;
   // a CTA of the cluster per 4096 entries of the vocabulary, up to eight
   int cluster = 1;
   while (cluster < kVerifyMaxCluster && cluster * 4096ll < s->V) cluster *= 2;

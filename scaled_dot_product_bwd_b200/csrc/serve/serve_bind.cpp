@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -111,8 +112,10 @@ T* vec(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayR
   return static_cast<T*>(t.data_ptr());
 }
 
+// An output of a call whose arguments are on the GPU (straight from the
+// allocator: the dispatcher would take as long as a kernel's launch).
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-  return at::empty(shape, like.options().dtype(type).memory_format(at::MemoryFormat::Contiguous));
+  return at::detail::empty_cuda(shape, type, like.device(), at::MemoryFormat::Contiguous);
 }
 
 struct Cache {

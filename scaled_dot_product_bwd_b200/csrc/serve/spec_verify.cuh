@@ -36,6 +36,7 @@ struct VerifyArgs {
   int32_t* path;
   int32_t* accepted;
   int32_t* next_token;
+  uint64_t wait_limit_ns;
 };
 
 constexpr int kVerifyThreads = 512;
@@ -57,6 +58,41 @@ __device__ __forceinline__ double verify_weight(float p, float q, int m, const d
   return t;
 }
 
+// x to `sum` of CTA `to` of the cluster, counted by its barrier `bar`.
+__device__ __forceinline__ void verify_send(uint32_t sum, uint32_t bar, int to, double x) {
+  asm volatile(
+      "{\n\t.reg .b32 s, b;\n\t"
+      "mapa.shared::cluster.u32 s, %0, %2;\n\t"
+      "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.f64 [s], %3, [b];\n\t}" ::"r"(sum),
+      "r"(bar), "r"(to), "d"(x)
+      : "memory");
+}
+
+// Waits for a phase of `bar` that other CTAs complete; false (and a status) at the limit.
+__device__ __forceinline__ bool verify_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t k = 0;; ++k) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((k & 63u) == 0) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > limit_ns) {
+        atomicOr(&g_device_status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(~0u, x, s);
@@ -68,6 +104,10 @@ __device__ __forceinline__ double warp_sum(double x) {
 // threads' registers (kVerifyHeld entries each), so a node's p and q are read
 // once for all its rejections; else every pass reads them again and computes
 // the weights from the earlier sums.
+// Sums travel as stores that complete on the receiving CTA's mbarrier, one
+// barrier per parity of the passes: a warp sends its sum of pass p + 1 once it
+// has read those of pass p, so none of pass p + 2 arrives before all of pass p
+// are read.
 template <bool HELD>
 __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const VerifyArgs a) {
   namespace cg = cooperative_groups;
@@ -83,10 +123,18 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
   __shared__ double inv[kVerifyMaxNodes + 1];
   // every warp's sum of the cluster, by two passes in turn
   __shared__ double sums[2][kVerifyMaxCluster * kVerifyWarps];
+  __shared__ __align__(8) uint64_t bars[2];
 
-  // (a CTA's shared memory may be written to once it has started: arrived at
-  // here, waited for after the nodes' loads)
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (tid == 0) {
+    mbar_init(smem_u32(bars), 1);
+    mbar_init(smem_u32(bars + 1), 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  // (a CTA's shared memory may be written to once it has started and its
+  // barriers stand: arrived at here, waited for after the nodes' loads)
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  const float u_sample = a.u_sample[b];  // (early: nothing waits for it at the end)
   if (tid < kVerifyMaxNodes) kids[tid] = 0;
   __syncthreads();
   if (tid < 64) {
@@ -126,6 +174,7 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
                                       static_cast<int64_t>(rank) * chunk + static_cast<int64_t>(warp) * seg));
   const int hi = min(cta_hi, lo + seg);
   int passes = 0;
+  bool ok = true;  // no wait has run out
 
   // HELD: entry lo + lane + 32 i of target[at] (then of what is left of it)
   // and of draft[at]
@@ -166,9 +215,11 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
       }
     }
     acc = warp_sum(acc);
-    double* mine = sums[passes & 1];
-    if (lane < C) *cluster.map_shared_rank(mine + rank * kVerifyWarps + warp, lane) = acc;
-    cluster.sync();
+    const double* mine = sums[passes & 1];
+    const uint32_t bar = smem_u32(bars + (passes & 1));
+    if (tid == 0) mbar_expect_tx(bar, C * kVerifyWarps * 8);
+    if (lane < C) verify_send(smem_u32(mine + rank * kVerifyWarps + warp), bar, lane, acc);
+    if (ok) ok = __all_sync(~0u, verify_wait(bar, (passes >> 1) & 1, a.wait_limit_ns));
     // all warps of the cluster add the same numbers in the same order
     double total = 0.0;
 #pragma unroll
@@ -180,22 +231,22 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
     return warp_sum(total);
   };
 
-  // every thread of the cluster walks alike
+  // every thread of the cluster walks alike (until a wait runs out)
   int at = 0, m = 0, n_acc = 0;
   unsigned long long left = a.N > 1 ? kids[0] : 0ull;
   if (rank == 0 && tid == 0) a.path[static_cast<int64_t>(b) * a.N] = 0;
   double total = 0.0;
-  while (left) {
+  while (left && ok) {
     const int n = __ffsll(static_cast<long long>(left)) - 1;
     left &= left - 1;
-    bool ok;
+    bool taken;
     if (m == 0) {
-      ok = (ok_first >> n) & 1ull;
+      taken = (ok_first >> n) & 1ull;
     } else {
       const double w = verify_weight(px[n], qx[n], m, inv) * inv[m];
-      ok = static_cast<double>(ux[n]) * qx[n] < w;
+      taken = static_cast<double>(ux[n]) * qx[n] < w;
     }
-    if (ok) {
+    if (taken) {
       at = n;
       m = 0;
       left = kids[n];
@@ -205,11 +256,17 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
       total = sum_pass(at, ++m);
       // (inv[m] was last read before the pass's barrier)
       if (tid == 0) inv[m] = total > 0.0 ? 1.0 / total : 0.0;
-      __syncthreads();
+      ok = __syncthreads_and(ok);
     }
   }
   if (m > 0 && !(total > 0.0)) m = 0;  // nothing left: the target itself
-  if (m == 0) total = sum_pass(at, 0);
+  if (m == 0 && ok) total = sum_pass(at, 0);
+  if (!ok) {
+    // stay until no other CTA can send here any more (one that has left counts
+    // as arrived); one whose waits all ended has all that was sent to it
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+    return;
+  }
   if (rank == 0) {
     for (int i = n_acc + 1 + tid; i < a.N; i += kVerifyThreads)
       a.path[static_cast<int64_t>(b) * a.N + i] = -1;
@@ -219,8 +276,8 @@ __global__ void __launch_bounds__(kVerifyThreads) spec_verify_kernel(const Verif
   // the warp piece in which the cumulative weight first exceeds u * total;
   // where rounding (or u = 1) leaves none, the last piece with any weight.
   // Every warp scans all pieces' sums, four neighbours to a lane.
-  const double aim = static_cast<double>(a.u_sample[b]) * total;
-  const double* last_sums = sums[(passes - 1) & 1];
+  const double aim = static_cast<double>(u_sample) * total;
+  const double* last_sums = sums[(passes + 1) & 1];
   constexpr int kPer = kVerifyMaxCluster * kVerifyWarps / 32;
   double part[kPer], mine = 0.0;
 #pragma unroll
