@@ -8,7 +8,13 @@
 // the scale by at most 2^-10 of it).
 //
 // Both kernels are bound by DRAM (append, e4m3: 2 bytes read and 1 written
-// per element; gather the reverse).  A row is spread over the lanes of a part
+// per element; gather the reverse).  Measured: append of 32 k rows of 8 heads of
+// 128 as e4m3 41 us, 4.8 TB/s (73 % of a copy's rate; eight rows in flight per
+// thread instead of four 43 us; CTAs that stay and walk the rows with the next
+// rows' places read ahead 49 us); gather of 485 MB, two thirds of it written,
+// 104 us, 4.7 TB/s (a plain fill of this GPU's memory reaches 3.8 TB/s, at which
+// the written part alone takes 85 us); calls of a few rows 3 - 5 us, latency.
+// A row is spread over the lanes of a part
 // of a warp in 16-byte pieces, so its maximum is a few shuffles and every
 // access is a full vector.
 #pragma once
@@ -85,7 +91,7 @@ struct AppendArgs {
 // thread keeps one 16-byte piece of one head (several when the heads are
 // many) and goes through the rows, four in flight.
 constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 64;  // at most
+constexpr int kCacheRows = 32;  // at most
 
 struct CacheCells {
   int64_t off[kCacheRows];    // of the row in the cache, elements; < 0: none
