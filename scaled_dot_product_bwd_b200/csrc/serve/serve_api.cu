@@ -247,12 +247,13 @@ cudaError_t launch_tree(const TreeArgs& a, const CUtensorMap& mk, const CUtensor
   return cudaLaunchKernelEx(&cfg, tree_join_cuts_kernel<D, R>, a, grid);
 }
 
-// Query rows of one product: the smallest of 16, 32 and 64 that holds a
+// Query rows of one product: the smallest of 8, 16, 32 and 64 that holds a
 // sequence's, 64 (and several blocks) beyond.
 template <int D, int FMT, int BIAS>
 cudaError_t dispatch_tree_rows(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                                cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.max_nodes) * a.G;
+  if (rows <= 8) return launch_tree<D, FMT, 8, BIAS>(a, mk, mv, st);
   if (rows <= 16) return launch_tree<D, FMT, 16, BIAS>(a, mk, mv, st);
   if (rows <= 32) return launch_tree<D, FMT, 32, BIAS>(a, mk, mv, st);
   return launch_tree<D, FMT, 64, BIAS>(a, mk, mv, st);

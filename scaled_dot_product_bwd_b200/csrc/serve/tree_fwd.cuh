@@ -35,12 +35,14 @@
 //    there), a query warp that lays the next piece's rows out as an operand,
 //    an issuing thread each for S and for P V, and four softmax warpgroups
 //    of 16 rows.  The softmax's chain of waits per tile (~700 cycles) is what
-//    one warpgroup would pay again and again, so at 16 rows the four take
+//    one warpgroup would pay again and again, so up to 16 rows the four take
 //    turns by tile, each with an O of its own; at 32 two pairs do; at 64 they
-//    share every tile by rows.
+//    share every tile by rows.  Up to 8 rows a thread does 8, not 16 (e4m3
+//    d = 64 49 -> 44 us, 1000 sequences of 500 bf16 keys 579 -> 484; bf16
+//    d = 64 53 -> 54).
 // Measured (32 query, 8 KV heads; 6.56 TB/s is a copy's rate):
 //   16 sequences of 8192 keys, one node: bf16 d = 128 90 us (5.9 TB/s, 91 %),
-//     d = 64 53 us (77 %); e4m3 d = 128 57 us (72 %), d = 64 49 us (42 %:
+//     d = 64 53 us (77 %); e4m3 d = 128 55 us (76 %), d = 64 44 us (47 %:
 //     bound by a tile's chain of steps, not by its bytes)
 //   32 ragged sequences of up to 16 k keys, e4m3: 121 us (86 %)
 //   16 ragged trees of 16 nodes over up to 8 k keys, bf16: 73 us (73 %; 64 rows,
@@ -74,7 +76,7 @@ constexpr int kTreeKeys = 128;      // keys per tile
 constexpr int kTreeSoftWarps = 16;
 constexpr int kTreeProducer = 16, kTreeIssueS = 17, kTreeIssueO = 18, kTreeQuery = 19;  // the other warps
 constexpr int kTreeThreads = 20 * 32;
-constexpr int kTreeRT = 16;         // rows of a softmax thread
+constexpr int kTreeRT = 16;         // rows of a softmax thread (8 where there are no more)
 // Named barriers: 1 .. 4 a softmax warpgroup, 5 all four, 6 + turn those of one tile.
 constexpr uint32_t kTreeBarAll = 5, kTreeBarTurn = 6;
 // A (sequence, head, row block) costs its first CTA about three tiles more (its
@@ -136,10 +138,11 @@ struct TreeLayout {
   static constexpr int kLine = kRowBytes / kHalves;         // bytes of a swizzled row
   static constexpr int kTile = kTreeKeys * kRowBytes;       // bytes of a slot: a tile of K or of V
   static constexpr int kParts = kE4m3 ? 2 : 1;              // of queries and weights
-  static constexpr int kN = kParts * R;                     // columns of S and of O^T
+  static constexpr int kN = kParts * R < 16 ? 16 : kParts * R;  // columns of S and of O^T (16: the fewest)
   static constexpr int kQBytes = kN * kRowBytes;
   static constexpr int kPBytes = kN * kTreeKeys * kCell;
-  static constexpr int kGroups = R / kTreeRT;               // softmax warpgroups that share a tile
+  static constexpr int kRT = R < kTreeRT ? R : kTreeRT;     // rows of a softmax thread
+  static constexpr int kGroups = R / kRT;                   // softmax warpgroups that share a tile
   static constexpr int kTurns = 4 / kGroups;                // ... and how many such sets there are
   static constexpr int kBufs = kTurns > 2 ? kTurns : 2;     // of S and of the weights
   static constexpr int kRO = R / 4 > 8 ? R / 4 : 8;         // rows a warpgroup writes out
@@ -584,7 +587,7 @@ __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeW
       const int r = (p0 + f * nw) * kPass + sub;
       if ((p0 + f * nw) * kPass >= R) break;
       if (FMT == kCacheBf16) {
-        *reinterpret_cast<uint4*>(dst + L::at(r, c, R)) = x[f];
+        *reinterpret_cast<uint4*>(dst + L::at(r, c, L::kN)) = x[f];
         continue;
       }
       // the row by a power of two that puts its largest element in [128, 256)
@@ -611,9 +614,9 @@ __device__ __forceinline__ void tree_load_queries(const TreeArgs& a, const TreeW
       }
       // a row that is not finite gives what float32 gives: NaN
       if (m >= 0x7f80u) hi[0] = hi[1] = hi[2] = hi[3] = 0x7f7fu;
-      *reinterpret_cast<uint2*>(dst + L::at(r, c >> 1, 2 * R) + (c & 1) * 8) =
+      *reinterpret_cast<uint2*>(dst + L::at(r, c >> 1, L::kN) + (c & 1) * 8) =
           make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-      *reinterpret_cast<uint2*>(dst + L::at(R + r, c >> 1, 2 * R) + (c & 1) * 8) =
+      *reinterpret_cast<uint2*>(dst + L::at(R + r, c >> 1, L::kN) + (c & 1) * 8) =
           make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       // the other way round: 2^(e - 134)
       if (c == 0)
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
   using L = TreeLayout<D, FMT, R, BIAS>;
   constexpr bool E4 = L::kE4m3;
   constexpr int NS = L::kSlots;
-  constexpr int RT = kTreeRT;
+  constexpr int RT = L::kRT;
   constexpr int RO = L::kRO;
   constexpr int TN = L::kTurns, NB = L::kBufs, RG = L::kGroups;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -986,7 +989,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         float sc[RT];
         if constexpr (E4) {
           float rest[RT];
-          tmem_ld_two(tmem + lanes + x * L::kN + row0, tmem + lanes + x * L::kN + R + row0, sc, rest);
+          if constexpr (RT == 8) {
+            float both[16];
+            tmem_ld_cols<16>(tmem + lanes + x * L::kN, both);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+              sc[j] = both[j];
+              rest[j] = both[RT + j];
+            }
+          } else {
+            tmem_ld_two(tmem + lanes + x * L::kN + row0, tmem + lanes + x * L::kN + R + row0, sc, rest);
+          }
           fma_rows<RT>(rest, 1.f / kQueryRest, sc);
         } else {
           tmem_ld_cols<RT>(tmem + lanes + x * L::kN + row0, sc);
@@ -1141,11 +1154,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
             hi[j / 4] = h0 | h1 << 16;
             lo[j / 4] = e4m3x2_rest(sc[j], sc[j + 1], h0) | e4m3x2_rest(sc[j + 2], sc[j + 3], h1) << 16;
           }
+          if constexpr (RT == 8) *reinterpret_cast<uint4*>(pbuf) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
             const uint32_t* w = part ? lo : hi;
 #pragma unroll
-            for (int j = 0; j < RT / 4; j += 4)
+            for (int j = 0; j + 4 <= RT / 4; j += 4)
               *reinterpret_cast<uint4*>(pbuf + ((part * R + row0) / 16 + j / 4) * (kTreeKeys * 16)) =
                   make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
           }
@@ -1260,8 +1274,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
 
       const bool whole = walk.t0 == 0 && walk.nt == s.tiles;
       const int slot = walk.t0 == 0 ? 1 : 0;  // 0: began in an earlier CTA
-      // first row that this thread writes; at 16 rows two warpgroups do, in turn
-      const int out0 = (R == 16 ? wg ^ ((u & 1) << 1) : wg) * RO;
+      // first row that this thread writes; at 16 rows two warpgroups do, at 8
+      // one does, in turn
+      const int out0 = (R == 8 ? (wg + u) & 3 : R == 16 ? wg ^ ((u & 1) << 1) : wg) * RO;
       const int n_rows = min(R, s.n * a.G - walk.block * R) - out0;  // from there on, may exceed RO
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + out0;
       const int sets = min(walk.nt, TN);      // that had tiles, from the first tile's on

@@ -717,3 +717,16 @@ def test_odd_arguments_are_refused():
     for far in (-2 ** 32 + 200, -1, 0, 8):
         with pytest.raises(SdpaError):
             sdpa_tree_fwd(q, t5_table=torch.zeros(32, 2, device=DEV), t5_max_distance=far, **args, **cache)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nodes", [4, 5, 8, 9, 16, 17])
+def test_tree_row_counts(nodes, kv, d):
+    """8 to 34 query rows: each size of product, full and barely begun, plain and with T5 and a window."""
+    cache, q, args, mask, seqs, cu, masks = tree_setup([400, 129], [nodes, 1], 4, 2, d, 16, kv)
+    o, lse = sdpa_tree_fwd(q, tree_mask=mask, **args, **cache)
+    check_tree(o, lse, q, seqs, cu, kv, masks)
+    kw, okw = bias_kw(dict(t5=True, window_left=150), 4)
+    o, lse = sdpa_tree_fwd(q, tree_mask=mask, **args, **cache, **kw)
+    check_tree(o, lse, q, seqs, cu, kv, masks, **okw)

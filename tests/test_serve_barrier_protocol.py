@@ -52,7 +52,7 @@ def tree_protocol(pieces, R, NS, seed, drop=None):
     """pieces: tiles of each; R: query rows of a product; NS: ring slots.  drop: a wait left out
     (to show that the model sees it)."""
     rng = random.Random(seed)
-    RG = R // 16
+    RG = max(R // 16, 1)
     TN = 4 // RG
     NB = max(TN, 2)
     ids = [(u, i) for u, nt in enumerate(pieces) for i in range(nt)]
@@ -192,7 +192,7 @@ def tree_protocol(pieces, R, NS, seed, drop=None):
             sums[(u & 1, g)] = u
             if TN > 1:
                 yield ("sync", "all")
-            writer = R > 16 or (g ^ ((u & 1) << 1)) < 2
+            writer = R > 16 or ((g + u) & 3 == 0 if R == 8 else (g ^ ((u & 1) << 1)) < 2)
             if writer:
                 for t in range(min(nt, TN)):
                     k = (it - nt + t) % TN
@@ -215,7 +215,7 @@ SHAPES = [[1], [2, 1, 1, 3], [1] * 9, [5, 4], [13], [3, 1, 7, 2, 6], [4, 1, 1, 1
 
 
 @pytest.mark.parametrize("NS", [4, 6, 12])
-@pytest.mark.parametrize("R", [16, 32, 64])
+@pytest.mark.parametrize("R", [8, 16, 32, 64])
 def test_tree_kernel_protocol(R, NS):
     for k, pieces in enumerate(SHAPES):
         for seed in range(12):
@@ -227,7 +227,7 @@ def test_tree_kernel_protocol(R, NS):
 def test_the_model_sees_a_missing_wait(drop):
     """Leaving a wait out of the model (not of the kernel) is noticed (scores that run ahead only
     where the ring has more slots than there are buffers of scores)."""
-    for R in (16, 32, 64):
+    for R in (8, 16, 32, 64):
         for seed in range(400):
             try:
                 explore(*tree_protocol([3, 1, 7, 2, 6], R, 4 if seed & 1 else 12, seed, drop), seed)
