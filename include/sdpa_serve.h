@@ -120,7 +120,7 @@ typedef struct sdpa_kv_cache {
  * is the smallest power of two 2^(e - 127), 1 <= e <= 254, with the row's
  * largest finite magnitude at most 448 of it (e = 127 for a row of zeros);
  * codes round to nearest even; infinities become +-448, NaN stays NaN.
- * slots: device int64 [T].  T = 0 does nothing.
+ * slots: device int64 [T].  T = 0 does nothing; T < 2^31.
  */
 sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const void* v,
                                 int64_t T, int64_t kv_t, int64_t kv_h, const int64_t* slots,
@@ -135,7 +135,7 @@ sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const
  * were, and so are rows whose page lies outside the table or the cache, which
  * sdpa_serve_read_device_status reports as SDPA_ERR_UNSUPPORTED.  An e4m3 value
  * times its scale is exact in bf16 (below bf16's smallest normal number, to
- * its rounding).
+ * its rounding).  B <= 65535, total < 2^30.
  */
 sdpa_status_t sdpa_cache_gather(const sdpa_kv_cache* cache, int64_t B, const int32_t* page_table,
                                 int64_t table_width, int64_t table_b, const int32_t* cu_seqlens,
@@ -171,6 +171,9 @@ sdpa_status_t sdpa_cache_gather(const sdpa_kv_cache* cache, int64_t B, const int
  * unspecified, and no memory outside the tensors is touched.
  * workspace: sdpa_tree_fwd_workspace_size() bytes, 256-byte aligned, contents
  * ignored on entry; calls that may overlap on the GPU need one each.
+ * B, Hq <= 65535; T < 2^30; table_width * page_size <= 2^30, and the batch's
+ * tiles of 128 keys over KV heads and blocks of 16 query rows are counted in 32
+ * bits: SDPA_ERR_UNSUPPORTED where they could pass that.
  * Deterministic: the split of the keys depends on the lengths and the GPU's
  * number of SMs alone, and sums are taken in a fixed order.
  */
