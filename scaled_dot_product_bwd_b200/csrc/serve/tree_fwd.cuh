@@ -1020,8 +1020,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
 #pragma unroll
           for (int j = 0; j < RT; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(info->scale + row0 + j);
-            f2_unpack(f2_fma(f2_mul(f2_pack(sc[j], sc[j + 1]), kf2), f2_pack(f.x, f.y), vx2), sc[j], sc[j + 1]);
-            f2_unpack(f2_fma(f2_mul(f2_pack(sc[j + 2], sc[j + 3]), kf2), f2_pack(f.z, f.w), vx2), sc[j + 2],
+            // the row's factor and the key's first: either with the sum of codes could leave float32
+            f2_unpack(f2_fma(f2_pack(sc[j], sc[j + 1]), f2_mul(f2_pack(f.x, f.y), kf2), vx2), sc[j], sc[j + 1]);
+            f2_unpack(f2_fma(f2_pack(sc[j + 2], sc[j + 3]), f2_mul(f2_pack(f.z, f.w), kf2), vx2), sc[j + 2],
                       sc[j + 3]);
           }
         } else {
