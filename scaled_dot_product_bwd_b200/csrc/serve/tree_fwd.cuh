@@ -19,9 +19,11 @@
 // query exactly (down to 2^-21 of its row's largest element) and a weight to
 // 2^-8 (or 2^-21 of the largest).  Over a bf16 cache a weight is rounded to
 // bf16 (2^-8), as in the framework's forward.  A key's scale multiplies its
-// scores; a value row's scale 2^e joins the exponent, weights being
-// 2^(s + e - r) with r near the maximum of s + e, so they stay in range
-// whatever the scales are, and l adds weight * 2^-e.
+// scores.  A value row's scale 2^e multiplies the weight that enters P V, and r
+// is near the maximum of s + e, so that what enters stays in range whatever the
+// scales are; l adds 2^(s - r).  Where r is so large that e would be rounded away
+// (every key under a bias of the type's lowest value), a row has a gain of its
+// own for P V.
 //
 // Bound by DRAM: a cached byte takes 2 to 128 FLOPs (1 to 64 rows).  What
 // costs is keeping enough loads in flight and every SM busy:
@@ -155,8 +157,9 @@ struct TreeLayout {
   // warpgroups that do not write it out go on to the next)
   static constexpr int kSumOff = kMaxOff + 4 * kTreeRT * 16;     // [2][4][kTreeRT][4] floats
   static constexpr int kRefOff = kSumOff + 2 * 4 * kTreeRT * 16; // [2][4][kTreeRT] floats
-  static constexpr int kFacOff = kRefOff + 2 * 4 * kTreeRT * 4;  // [4][kTreeRT] floats
-  static constexpr int kBucketOff = kFacOff + 4 * kTreeRT * 4;   // [kTreeBuckets] bytes
+  static constexpr int kFacOff = kRefOff + 2 * 4 * kTreeRT * 4;  // [4][kTreeRT] floats, e4m3: of l and of O
+  static constexpr int kGainOff = kFacOff + (kE4m3 ? 2 : 1) * 4 * kTreeRT * 4;     // [2][4][kTreeRT] floats (e4m3)
+  static constexpr int kBucketOff = kGainOff + (kE4m3 ? 2 * 4 * kTreeRT * 4 : 0);  // [kTreeBuckets] bytes
   static constexpr int kT5Off = kBucketOff + (BIAS ? kTreeBuckets : 0);  // [2][kTreeT5Slice] floats
   static constexpr int kMiscOff = kT5Off + (BIAS ? 2 * kTreeT5Slice * 4 : 0);
   static constexpr int kMaxSlots = 12;
@@ -523,8 +526,18 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t w) {
 constexpr float kQueryRest = 16.f, kWeightRest = 16.f;
 // Weights are 2^(s - r).  Over a bf16 cache r is a maximum that a later score
 // may outgrow by 2^8 before O is rescaled; over e4m3, whose largest value is
-// 448, r is set 7 below the maximum and outgrown at 2^8.7 = 416.
+// 448, r is set 7 below the maximum of s + e and outgrown at 2^8.7 = 416.  There
+// e counts from kLeastE on, so that l, whose terms are 2^-e as large, stays
+// finite over 2^17 keys.  Where that leaves a row's weights small, or r has less
+// than 3 bits below the point (from kManyDigits on), its weights are 2^(s - r)
+// times 2^e times a gain 2^-t, t found as r is, from s - r + e.
 constexpr float kTopBf16 = 0.f, kOverBf16 = 8.f, kTopE4m3 = 7.f, kOverE4m3 = 8.7f;
+constexpr float kLeastE = -103.f, kManyDigits = 0x1p20f, kMostGain = 0x1p120f;
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // All bits of the codes / bf16 halves in w that are infinite or NaN.
 template <int FMT>
@@ -911,7 +924,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     const uint32_t b_tile = RG == 1 ? 1 + wg : kTreeBarTurn + turn;
     float* wmax = reinterpret_cast<float*>(smem + L::kMaxOff);    // [4][RT][4 warps]
     float* mine = wmax + wg * RT * 4;
-    float* facs = reinterpret_cast<float*>(smem + L::kFacOff);    // [4][RT]: what the last rescaling took
+    float* facs = reinterpret_cast<float*>(smem + L::kFacOff);    // [4][RT]: what the last rescaling took of l
+    float* facs_o = facs + (E4 ? 4 * kTreeRT : 0);                // ... and of O
     // After a wait that ran out the warps go on without waiting, through the
     // same barriers, so that no thread is left at one.
     bool ok = true;
@@ -930,6 +944,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
       const uint32_t t_o = t_all + turn * L::kN + row0;                       // this warpgroup's
       float* refs = reinterpret_cast<float*>(smem + L::kRefOff) + (u & 1) * 4 * RT;  // [4][RT]
       float* sums = reinterpret_cast<float*>(smem + L::kSumOff) + (u & 1) * 16 * RT; // [4][RT][4 warps]
+      float* gains = reinterpret_cast<float*>(smem + L::kGainOff) + (u & 1) * 4 * RT; // [4][RT] (e4m3)
       if (u == 0) {
         TreeRows* first = reinterpret_cast<TreeRows*>(smem + L::kRowsOff);
         tree_load_queries<D, FMT, R, BIAS>(a, walk, warp, kTreeSoftWarps, lane, smem + L::kQOff, first);
@@ -953,6 +968,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         l[j] = 0.f;
       }
       bool fresh = true;  // no tile of the piece in this warpgroup's O yet
+      bool gained = false;  // some row's gain is not 1 (e4m3)
       // e4m3: the scales of this thread's key, read one tile ahead: its page
       // at the tile's start, the bytes at its end
       uint32_t k_byte = 127, v_byte = 127;
@@ -1008,22 +1024,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free(x));
 
-        // scores in log2 units, plus the exponent of the key's value scale
-        float v_inv = 1.f;
+        // scores in log2 units
+        float e = 0.f;  // exponent of the key's value scale
         if constexpr (E4) {
           const float kf = e8m0_float(k_byte);
-          const int ve = static_cast<int>(v_byte);
-          v_inv = e8m0_float(static_cast<uint32_t>(max(254 - ve, 0)));
+          e = fmaxf(static_cast<float>(static_cast<int>(v_byte) - 127), kLeastE);
           const uint64_t kf2 = f2_pack(kf, kf);
-          const float vx = static_cast<float>(ve - 127);
-          const uint64_t vx2 = f2_pack(vx, vx);
 #pragma unroll
           for (int j = 0; j < RT; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(info->scale + row0 + j);
             // the row's factor and the key's first: either with the sum of codes could leave float32
-            f2_unpack(f2_fma(f2_pack(sc[j], sc[j + 1]), f2_mul(f2_pack(f.x, f.y), kf2), vx2), sc[j], sc[j + 1]);
-            f2_unpack(f2_fma(f2_pack(sc[j + 2], sc[j + 3]), f2_mul(f2_pack(f.z, f.w), kf2), vx2), sc[j + 2],
-                      sc[j + 3]);
+            f2_unpack(f2_mul(f2_pack(sc[j], sc[j + 1]), f2_mul(f2_pack(f.x, f.y), kf2)), sc[j], sc[j + 1]);
+            f2_unpack(f2_mul(f2_pack(sc[j + 2], sc[j + 3]), f2_mul(f2_pack(f.z, f.w), kf2)), sc[j + 2], sc[j + 3]);
           }
         } else {
           const uint64_t f2 = f2_pack(a.scale_log2, a.scale_log2);
@@ -1098,19 +1110,55 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           f2_unpack(f2_sub(f2_pack(sc[j], sc[j + 1]), f2_pack(ref[j], ref[j + 1])), d0, d1);
           over = fmax3(over, d0, d1);
         }
-        if (barrier_or(1 + wg, 128, over > (E4 ? kOverE4m3 : kOverBf16) || fresh)) {
-          const float top = by_halves<RT>(sc, lane, [](float x, float y) { return fmaxf(x, y); });
-          if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = top;
-          named_barrier(1 + wg, 128);
-          if ((warp & 3) == 0 && lane < RT) {
-            const float4 w4 = *reinterpret_cast<const float4*>(mine + lane * 4);
-            const float old = fresh ? -FLT_MAX : refs[wg * RT + lane];
-            const float m = fmaxf(fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) - (E4 ? kTopE4m3 : kTopBf16), old);
-            refs[wg * RT + lane] = m;
-            facs[wg * RT + lane] = fast_exp2(old - m);
+        if (barrier_or(1 + wg, 128, over + e > (E4 ? kOverE4m3 : kOverBf16) || fresh || gained)) {
+          const bool scribe = (warp & 3) == 0 && lane < RT;  // keeps row `lane`'s reference
+          const int at = wg * RT + lane;
+          auto rows_top = [&](const float (&y)[RT]) {  // for the scribes: their row's largest, less kTop
+            const float of_row = by_halves<RT>(y, lane, [](float x, float z) { return fmaxf(x, z); });
+            if ((lane & (32 / RT - 1)) == 0) mine[(lane / (32 / RT)) * 4 + (warp & 3)] = of_row;
+            named_barrier(1 + wg, 128);
+            const float4 w4 = *reinterpret_cast<const float4*>(mine + lane % RT * 4);
+            return fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) - (E4 ? kTopE4m3 : kTopBf16);
+          };
+          float top[RT];
+#pragma unroll
+          for (int j = 0; j < RT; j += 2) {
+            if constexpr (E4) f2_unpack(f2_add(f2_pack(sc[j], sc[j + 1]), f2_pack(e, e)), top[j], top[j + 1]);
+            else { top[j] = sc[j]; top[j + 1] = sc[j + 1]; }
+          }
+          const float m = rows_top(top);
+          const float true_e = static_cast<float>(static_cast<int>(v_byte) - 127);
+          bool wide = E4 && (gained || true_e < kLeastE);  // gains have to be looked at
+          if (scribe) {
+            const float old = fresh ? -FLT_MAX : refs[at];
+            const float r = fmaxf(m, old);
+            refs[at] = r;
+            facs[at] = fast_exp2(old - r);
+            if constexpr (E4) {
+              facs_o[at] = fast_exp2(old - r);
+              if (fresh) gains[at] = 1.f;
+              wide |= fabsf(r) >= kManyDigits && m > -INFINITY;
+            }
           }
           if (TN < NB && !fresh) values_done(it - TN);
-          named_barrier(1 + wg, 128);
+          if constexpr (E4) {
+            if (__builtin_expect(barrier_or(1 + wg, 128, wide), 0)) {
+#pragma unroll
+              for (int j = 0; j < RT; ++j) top[j] = (sc[j] - refs[wg * RT + j]) + true_e;
+              const float m = rows_top(top);
+              if (scribe) {
+                // (what is in O does not grow)
+                const float old = gains[at], most = fminf(old * fast_rcp(facs[at]), kMostGain);
+                const float gain = fminf(most, fabsf(refs[at]) >= kManyDigits || m < -1.f ? fast_exp2(-m) : 1.f);
+                gains[at] = gain;
+                if (gain != old) facs_o[at] = facs[at] * (gain * fast_rcp(old));
+                wide = gain != 1.f;
+              }
+              gained = barrier_or(1 + wg, 128, scribe && wide);
+            }
+          } else {
+            named_barrier(1 + wg, 128);
+          }
 #pragma unroll
           for (int j = 0; j < RT; j += 4) {
             const float4 r4 = *reinterpret_cast<const float4*>(refs + wg * RT + j);
@@ -1126,7 +1174,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
 #pragma unroll 1
             for (int j0 = 0; j0 < RT * L::kParts; j0 += 8) {
               const uint32_t t = t_o + (j0 < RT ? j0 : R + j0 - RT);
-              const float* f = facs + wg * RT + (j0 < RT ? j0 : j0 - RT);
+              const float* f = facs_o + wg * RT + (j0 < RT ? j0 : j0 - RT);
               float o[8];
               tmem_ld_cols<8>(t, o);
 #pragma unroll
@@ -1137,14 +1185,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
 
         uint8_t* pbuf = smem + L::kPOff + x * L::kPBytes + me * 16;
-        const uint64_t v_inv2 = f2_pack(v_inv, v_inv);
+        const float v_up = e8m0_float(v_byte);
+        const uint64_t up2 = f2_pack(v_up, v_up);
 #pragma unroll
         for (int j = 0; j < RT; j += 2) {
           f2_unpack(f2_sub(f2_pack(sc[j], sc[j + 1]), f2_pack(ref[j], ref[j + 1])), sc[j], sc[j + 1]);
           sc[j] = fast_exp2(sc[j]);
           sc[j + 1] = fast_exp2(sc[j + 1]);
-          const uint64_t p2 = f2_pack(sc[j], sc[j + 1]), l2 = f2_pack(l[j], l[j + 1]);
-          f2_unpack(E4 ? f2_fma(p2, v_inv2, l2) : f2_add(p2, l2), l[j], l[j + 1]);
+          const uint64_t p2 = f2_pack(sc[j], sc[j + 1]);
+          f2_unpack(f2_add(p2, f2_pack(l[j], l[j + 1])), l[j], l[j + 1]);
+          if constexpr (E4) f2_unpack(f2_mul(p2, up2), sc[j], sc[j + 1]);
+        }
+        if (E4 && __builtin_expect(gained, 0)) {
+#pragma unroll
+          for (int j = 0; j < RT; ++j) sc[j] *= gains[wg * RT + j];
         }
         // the weights: 16 bytes of one key's rows at a time
         if constexpr (E4) {
@@ -1302,6 +1356,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
             float rest[8];
             tmem_ld_cols<8>(t_all + t * L::kN + R + row, rest);
             fma_rows<8>(rest, 1.f / kWeightRest, o2);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o2[j] *= fast_rcp(gains[at + j]);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {

@@ -3,6 +3,8 @@ values, biases of the type's lowest value, value rows of zeros, many small weigh
 
 Bounds are test_gpu_serve.py's (its module docstring) unless a test says otherwise.
 """
+import math
+
 import pytest
 import torch
 
@@ -39,4 +41,63 @@ def test_keys_near_one_end_under_queries_near_the_other(nodes, q_size, k_size):
     q = (q * 2.0 ** q_size).bfloat16().to(DEV)
     cache, table, rows = filled(k * 2.0 ** k_size, v)
     o, lse = sdpa_tree_fwd(q, page_table=table, ctx_lens=i32(n - nodes), cu_nodes=i32(0, nodes), max_nodes=nodes, **cache)
+    check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
+
+
+# one piece per CTA where every sequence is the same: the whole line's tiles in one accumulator
+COPIES = 148
+
+
+def attend(q, cache, table, ctx, copies=1, **kw):
+    """O, LSE of nodes q [n, Hq, d] at ctx, as one sequence or as copies of it over the same pages."""
+    n = len(q)
+    o, lse = sdpa_tree_fwd(q.repeat(copies, 1, 1), page_table=table.repeat(copies, 1), ctx_lens=i32(*[ctx] * copies),
+                           cu_nodes=i32(*range(0, n * copies + 1, n)), max_nodes=n, **kw, **cache)
+    for c in range(1, copies):
+        assert torch.equal(o[:n], o[c * n:c * n + n]) and torch.equal(lse[:, :n], lse[:, c * n:c * n + n])
+    return o[:n], lse[:, :n]
+
+
+@pytest.mark.parametrize("low", [torch.finfo(torch.float32).min, -1e38, -1e8, -1e5, 0.0])
+@pytest.mark.parametrize("nodes,copies", [(1, 1), (16, 1), (40, 1), (1, COPIES), (40, COPIES)])
+def test_biases_that_leave_no_digits_for_the_scores(nodes, copies, low):
+    """Every key under the same bias, down to the type's lowest value, and equal scores (q = 0): the
+    mean of the values, whose scales differ by up to 2^7 from row to row."""
+    g = torch.Generator().manual_seed(nodes)
+    n, hq, d = 300 + nodes, 1, 64
+    k, v = torch.randn(n, hq, d, generator=g), torch.randn(n, hq, d, generator=g)
+    cache, table, rows = filled(k, v * torch.exp2(torch.randint(-4, 4, (n, hq, 1), generator=g).float()))
+    q = torch.zeros(nodes, hq, d, device=DEV).bfloat16()
+    o, _ = attend(q, cache, table, n - nodes, copies, t5_table=torch.full((32, hq), low, device=DEV), t5_bidirectional=False)
+    _, lse = attend(q, cache, table, n - nodes, copies)
+    check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
+
+
+@pytest.mark.parametrize("size", [-116, -100, -60, 60, 100, 120])
+@pytest.mark.parametrize("nodes", [1, 16, 40])
+def test_values_near_the_ends_of_the_range(nodes, size):
+    g = torch.Generator().manual_seed(nodes)
+    n, hq, d = 500 + nodes, 2, 64
+    k, v, q = (torch.randn(m, hq, d, generator=g) for m in (n, n, nodes))
+    q = q.bfloat16().to(DEV)
+    cache, table, rows = filled(k, v * 2.0 ** size)
+    o, lse = attend(q, cache, table, n - nodes)
+    check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
+
+
+@pytest.mark.parametrize("step", [8, -8])
+@pytest.mark.parametrize("nodes,copies", [(1, 1), (1, COPIES), (16, COPIES), (40, COPIES)])
+def test_scores_that_rise_as_the_values_fall(nodes, copies, step):
+    """From tile to tile weights rise (or fall) by 2^8 and the values' scales do the opposite: each tile
+    adds as much to O, while the sum of weights grows by 2^128."""
+    g = torch.Generator().manual_seed(nodes)
+    tiles, d = 17, 64
+    n = 128 * tiles + nodes
+    u = torch.randn(1, d, generator=g).bfloat16().float()
+    tile = (torch.arange(n) // 128)[:, None, None].float()
+    k = u * (step * math.log(2) * math.sqrt(d) / (u * u).sum()) * (tile - 8)
+    v = torch.randn(n, 1, d, generator=g) * torch.exp2(step * (8 - tile))
+    q = u.expand(nodes, 1, d).bfloat16().to(DEV)
+    cache, table, rows = filled(k, v)
+    o, lse = attend(q, cache, table, n - nodes, copies)
     check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
