@@ -527,12 +527,13 @@ constexpr float kQueryRest = 16.f, kWeightRest = 16.f;
 // Weights are 2^(s - r).  Over a bf16 cache r is a maximum that a later score
 // may outgrow by 2^8 before O is rescaled; over e4m3, whose largest value is
 // 448, r is set 7 below the maximum of s + e and outgrown at 2^8.7 = 416.  There
-// e counts from kLeastE on, so that l, whose terms are 2^-e as large, stays
-// finite over 2^17 keys.  Where that leaves a row's weights small, or r has less
-// than 3 bits below the point (from kManyDigits on), its weights are 2^(s - r)
-// times 2^e times a gain 2^-t, t found as r is, from s - r + e.
+// e counts from kLeastE to kMostE, so that l, whose terms are 2^-e as large,
+// stays finite over 2^17 keys and loses none above 2^-43 of the largest.  Where
+// that leaves a row's weights small or large, or r has less than 3 bits below
+// the point (from kManyDigits on), its weights are 2^(s - r) times 2^e times a
+// gain 2^-t, t found as r is, from s - r + e.
 constexpr float kTopBf16 = 0.f, kOverBf16 = 8.f, kTopE4m3 = 7.f, kOverE4m3 = 8.7f;
-constexpr float kLeastE = -103.f, kManyDigits = 0x1p20f, kMostGain = 0x1p120f;
+constexpr float kLeastE = -103.f, kMostE = 90.f, kManyDigits = 0x1p20f, kMostGain = 0x1p120f;
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1123,12 +1124,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           float top[RT];
 #pragma unroll
           for (int j = 0; j < RT; j += 2) {
-            if constexpr (E4) f2_unpack(f2_add(f2_pack(sc[j], sc[j + 1]), f2_pack(e, e)), top[j], top[j + 1]);
+            const float in = fminf(e, kMostE);
+            if constexpr (E4) f2_unpack(f2_add(f2_pack(sc[j], sc[j + 1]), f2_pack(in, in)), top[j], top[j + 1]);
             else { top[j] = sc[j]; top[j + 1] = sc[j + 1]; }
           }
           const float m = rows_top(top);
           const float true_e = static_cast<float>(static_cast<int>(v_byte) - 127);
-          bool wide = E4 && (gained || true_e < kLeastE);  // gains have to be looked at
+          bool wide = E4 && (gained || true_e < kLeastE || true_e > kMostE);  // gains have to be looked at
           if (scribe) {
             const float old = fresh ? -FLT_MAX : refs[at];
             const float r = fmaxf(m, old);
@@ -1149,7 +1151,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
               if (scribe) {
                 // (what is in O does not grow)
                 const float old = gains[at], most = fminf(old * fast_rcp(facs[at]), kMostGain);
-                const float gain = fminf(most, fabsf(refs[at]) >= kManyDigits || m < -1.f ? fast_exp2(-m) : 1.f);
+                const float gain = fminf(most, fabsf(refs[at]) >= kManyDigits || fabsf(m) > 1.f ? fast_exp2(-m) : 1.f);
                 gains[at] = gain;
                 if (gain != old) facs_o[at] = facs[at] * (gain * fast_rcp(old));
                 wide = gain != 1.f;

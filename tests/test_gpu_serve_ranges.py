@@ -79,10 +79,27 @@ def test_values_near_the_ends_of_the_range(nodes, size):
     g = torch.Generator().manual_seed(nodes)
     n, hq, d = 500 + nodes, 2, 64
     k, v, q = (torch.randn(m, hq, d, generator=g) for m in (n, n, nodes))
-    q = q.bfloat16().to(DEV)
     cache, table, rows = filled(k, v * 2.0 ** size)
-    o, lse = attend(q, cache, table, n - nodes)
-    check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
+    for steep in (1, 8):                         # weights of one size, and over 2^80
+        o, lse = attend((steep * q).bfloat16().to(DEV), cache, table, n - nodes)
+        check_tree(o, lse, (steep * q).bfloat16(), [(*rows, n - nodes)], [0, nodes], "e4m3")
+
+
+@pytest.mark.parametrize("nodes", [1, 16, 40])
+def test_many_small_weights_on_values_near_the_largest(nodes):
+    """One key of weight 1 and 2^16 of weight 2^-16, with values of 2^126 and -2^125: half of O's
+    weight lies 2^-16 below the largest."""
+    g = torch.Generator().manual_seed(nodes)
+    n, d = 65536 + nodes, 64
+    u = torch.randn(1, d, generator=g).bfloat16().float()
+    k, v = torch.zeros(n, 1, d), torch.full((n, 1, d), -2.0 ** 125)
+    k[3] = u * (16 * math.log(2) * math.sqrt(d) / (u * u).sum())
+    v[3] = 2.0 ** 126
+    q = u.expand(nodes, 1, d).bfloat16().to(DEV)
+    cache, table, rows = filled(k, v, page=256)
+    o, lse = attend(q, cache, table, n - nodes, COPIES)
+    check_tree(o[:1], lse[:, :1], q[:1], [(rows[0][:n - nodes + 1], rows[1][:n - nodes + 1], n - nodes)], [0, 1], "e4m3")
+    assert (o.double().abs() < 2.0 ** 125).all()
 
 
 @pytest.mark.parametrize("step", [8, -8])
