@@ -20,8 +20,8 @@
 // 2^-8 (or 2^-21 of the largest).  Over a bf16 cache a weight is rounded to
 // bf16 (2^-8), as in the framework's forward.  A key's scale multiplies its
 // scores.  A value row's scale 2^e multiplies the weight that enters P V, and r
-// is near the maximum of s + e, so that what enters stays in range whatever the
-// scales are; l adds 2^(s - r).  Where r is so large that e would be rounded away
+// is near the maximum of s + e (over keys whose value row is not all zeros), so
+// that what enters stays in range whatever the scales are; l adds 2^(s - r).  Where r is so large that e would be rounded away
 // (every key under a bias of the type's lowest value), a row has a gain of its
 // own for P V.
 //
@@ -695,6 +695,19 @@ __device__ __forceinline__ void tree_load_rows(const TreeArgs& a, const TreeWalk
   }
 }
 
+// Whether key `me` of a tile in the ring has e4m3 codes of zero alone.  (Out of
+// line: it runs where a scale stands out, and its instructions would otherwise
+// be fetched for every piece.)
+template <typename L>
+__device__ __noinline__ bool tree_row_of_zeros(const uint8_t* tile, int me) {
+  uint32_t some = 0;
+  for (int c = 0; c < L::kRowBytes / 16; ++c) {
+    const uint4 w = *reinterpret_cast<const uint4*>(tile + L::at(me, c, kTreeKeys));
+    some |= w.x | w.y | w.z | w.w;
+  }
+  return !(some & 0x7f7f7f7fu);
+}
+
 // ---------------------------------------------------------------- kernel
 template <int D, int FMT, int R, int BIAS>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
@@ -1121,16 +1134,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
             const float4 w4 = *reinterpret_cast<const float4*>(mine + lane % RT * 4);
             return fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) - (E4 ? kTopE4m3 : kTopBf16);
           };
+          float in = fminf(e, kMostE), true_e = static_cast<float>(static_cast<int>(v_byte) - 127);
+          if constexpr (E4) {
+            // a value row of zeros raises r no more than l needs: its weight in
+            // P V does not matter.  It is stored with a scale of 1 (byte 127);
+            // rows are looked at where one could be far above its neighbours
+            const bool there = key < s.keys;
+            const uint32_t hi = __reduce_max_sync(~0u, there ? v_byte : 0u);
+            const uint32_t lo = __reduce_min_sync(~0u, there ? v_byte : 255u);
+            if (__builtin_expect(hi >= 127u || hi > lo + 4u, 0)) {
+              const uint32_t item = 2 * it + 1;
+              wait(full(item % NS), (item / NS) & 1);
+              if (tree_row_of_zeros<L>(smem + slot_off(item), me)) {
+                in = kLeastE;
+                true_e = -INFINITY;
+              }
+            }
+          }
           float top[RT];
 #pragma unroll
           for (int j = 0; j < RT; j += 2) {
-            const float in = fminf(e, kMostE);
             if constexpr (E4) f2_unpack(f2_add(f2_pack(sc[j], sc[j + 1]), f2_pack(in, in)), top[j], top[j + 1]);
             else { top[j] = sc[j]; top[j + 1] = sc[j + 1]; }
           }
           const float m = rows_top(top);
-          const float true_e = static_cast<float>(static_cast<int>(v_byte) - 127);
-          bool wide = E4 && (gained || true_e < kLeastE || true_e > kMostE);  // gains have to be looked at
+          bool wide = E4 && (gained || (true_e < kLeastE && true_e > -INFINITY) || true_e > kMostE);  // gains have to be looked at
           if (scribe) {
             const float old = fresh ? -FLT_MAX : refs[at];
             const float r = fmaxf(m, old);
@@ -1146,8 +1174,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           if constexpr (E4) {
             if (__builtin_expect(barrier_or(1 + wg, 128, wide), 0)) {
 #pragma unroll
-              for (int j = 0; j < RT; ++j) top[j] = (sc[j] - refs[wg * RT + j]) + true_e;
-              const float m = rows_top(top);
+              for (int j = 0; j < RT; ++j) {
+                const float of_row = warp_max((sc[j] - refs[wg * RT + j]) + true_e);
+                if (lane == 0) mine[j * 4 + (warp & 3)] = of_row;
+              }
+              named_barrier(1 + wg, 128);
+              const float4 w4 = *reinterpret_cast<const float4*>(mine + lane % RT * 4);
+              const float m = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) - kTopE4m3;
               if (scribe) {
                 // (what is in O does not grow)
                 const float old = gains[at], most = fminf(old * fast_rcp(facs[at]), kMostGain);

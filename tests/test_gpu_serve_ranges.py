@@ -118,3 +118,34 @@ def test_scores_that_rise_as_the_values_fall(nodes, copies, step):
     cache, table, rows = filled(k, v)
     o, lse = attend(q, cache, table, n - nodes, copies)
     check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
+
+
+@pytest.mark.parametrize("size", [1.0, 0.1, 1e-4])
+@pytest.mark.parametrize("lead", [0.0, 8.0, 9.7, 11.0, 100.0])
+@pytest.mark.parametrize("nodes,copies", [(1, 1), (1, COPIES), (16, COPIES), (40, COPIES)])
+def test_value_rows_of_zeros(nodes, copies, lead, size):
+    """Value rows of zeros (stored with a scale of 1), one of them under the highest score: they add to
+    the sum of weights and take nothing from the other keys' weights."""
+    g = torch.Generator().manual_seed(nodes)
+    n, d = 4096 + nodes, 128
+    u = torch.randn(1, d, generator=g)
+    q = (u + 0.05 * torch.randn(nodes, 1, d, generator=g)).bfloat16().to(DEV)
+    k, v = torch.randn(n, 1, d, generator=g), size * torch.randn(n, 1, d, generator=g)
+    k[5] = u * (lead * math.sqrt(d) / (u * u).sum())
+    v[5] = v[700] = v[n - nodes - 1] = v[n - 1] = 0.0
+    cache, table, rows = filled(k, v, page=64)
+    o, lse = attend(q, cache, table, n - nodes, copies)
+    check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
+
+
+@pytest.mark.parametrize("nodes", [1, 16, 40])
+def test_values_of_zeros_alone(nodes):
+    g = torch.Generator().manual_seed(nodes)
+    n, d = 400 + nodes, 64
+    k, q = torch.randn(n, 1, d, generator=g), torch.randn(nodes, 1, d, generator=g).bfloat16().to(DEV)
+    cache, table, rows = filled(k, torch.zeros(n, 1, d))
+    for kw in (dict(), dict(alibi_slopes=torch.ones(1, device=DEV))):
+        o, lse = attend(q, cache, table, n - nodes, **kw)
+        assert (o == 0).all()
+        check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3",
+                   **{name: t.cpu().numpy() for name, t in kw.items()})
