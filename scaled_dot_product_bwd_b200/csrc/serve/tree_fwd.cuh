@@ -1308,12 +1308,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
                   else v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(src));
                 }
                 if (!isinf(v) && !isnan(v)) continue;
+                // (a row that sees the key gets it whatever its weight, as in a
+                // tile that all rows see)
+                const int nd = key0 + k - s.ctx;
+                const int pos = nd >= 0 ? s.ctx + info->depth[nd] : key0 + k;
+                const uint32_t sees = nd >= 0 ? info->seen[nd][row0 / 32] >> (row0 % 32) : ~0u;
                 const uint8_t* pk = smem + L::kPOff + x * L::kPBytes + k * 16;
 #pragma unroll
                 for (int j = 0; j < RT; ++j) {
+                  if (!((sees >> j) & 1u) || (a.wl >= 0 && info->pos[row0 + j] - pos > a.wl)) continue;
                   const int byte = (row0 + j) * L::kCell;
-                  const uint8_t* src = pk + (byte >> 4) * (kTreeKeys * 16) + (byte & 15);
-                  if (E4 ? *src != 0 : *reinterpret_cast<const uint16_t*>(src) != 0) sc[j] += v;
+                  sc[j] += E4 ? v : v * __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                                            pk + (byte >> 4) * (kTreeKeys * 16) + (byte & 15)));
                 }
               }
             named_barrier(b_tile, kTileThreads);

@@ -149,3 +149,38 @@ def test_values_of_zeros_alone(nodes):
         assert (o == 0).all()
         check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3",
                    **{name: t.cpu().numpy() for name, t in kw.items()})
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("gap", [1.0, 12.0, 40.0, 200.0])
+@pytest.mark.parametrize("ctx", [5, 128, 300])
+@pytest.mark.parametrize("window", [-1, 3])
+def test_nan_values_reach_their_viewers_whatever_their_weight(ctx, gap, window, kv):
+    """Values of NaN of a node `gap` nats below the other keys: NaN for the node that sees it, and for it alone."""
+    g = torch.Generator().manual_seed(5)
+    nodes, d = 3, 64
+    u = torch.randn(1, d, generator=g).bfloat16().float()
+    k, v = torch.zeros(ctx + nodes, 1, d), torch.randn(ctx + nodes, 1, d, generator=g)
+    k[ctx + 1] = -u * (gap * math.sqrt(d) / (u * u).sum())
+    v[ctx + 1] = float("nan")
+    cache, table, _ = filled(k, v, kv)
+    q = u.expand(nodes, 1, d).bfloat16().to(DEV)
+    mask = torch.tensor([0b001, 0b011, 0b101], device=DEV)
+    o, lse = attend(q, cache, table, ctx, tree_mask=mask, window_left=window)
+    assert torch.isnan(o[1]).all() and torch.isfinite(o[0]).all() and torch.isfinite(o[2]).all()
+    assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("gap", [1.0, 12.0, 40.0])
+def test_infinite_values_reach_their_viewers_whatever_their_weight(gap):
+    g = torch.Generator().manual_seed(6)
+    ctx, nodes, d = 70, 3, 64
+    u = torch.randn(1, d, generator=g).bfloat16().float()
+    k, v = torch.zeros(ctx + nodes, 1, d), torch.randn(ctx + nodes, 1, d, generator=g)
+    k[ctx + 1] = -u * (gap * math.sqrt(d) / (u * u).sum())
+    v[ctx + 1, :, ::2], v[ctx + 1, :, 1::2] = float("inf"), -float("inf")
+    cache, table, _ = filled(k, v, "bf16")
+    q = u.expand(nodes, 1, d).bfloat16().to(DEV)
+    o, _ = attend(q, cache, table, ctx, tree_mask=torch.tensor([0b001, 0b011, 0b101], device=DEV))
+    assert (o[1, :, ::2] == float("inf")).all() and (o[1, :, 1::2] == -float("inf")).all()
+    assert torch.isfinite(o[0]).all() and torch.isfinite(o[2]).all()
