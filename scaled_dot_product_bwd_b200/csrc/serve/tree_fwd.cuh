@@ -566,6 +566,12 @@ __device__ __forceinline__ float bias_to_log2(float b) {
   return isinf(x) && !isinf(b) ? copysignf(FLT_MAX, b) : x;
 }
 
+// LSE of a row with reference r and sum l (0: it sees nothing).  A reference at
+// the lowest value is a bias of the lowest value, which bias_to_log2 kept there.
+__device__ __forceinline__ float tree_lse(float r, float l) {
+  return r == -FLT_MAX && l > 0.f ? -FLT_MAX : (r + log2f(l)) * kLn2;
+}
+
 __device__ __forceinline__ float t5_bias_log2(const TreeArgs& a, int rel, int h) {
   return bias_to_log2(a.t5_table[t5_bucket(rel, a.t5) * a.Hq + h]);
 }
@@ -1415,7 +1421,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         for (int j = 0; j < 8; ++j) {
           if (whole) o[j] *= sum[j] > 0.f || isnan(sum[j]) ? 1.f / sum[j] : 0.f;
           if (me == j && j0 + j < n_rows) {
-            if (whole) a.lse[info->lse[row + j]] = (rr[j] + log2f(sum[j])) * kLn2;
+            if (whole) a.lse[info->lse[row + j]] = tree_lse(rr[j], sum[j]);
             else a.part_ml[part + j0 + j] = make_float2(rr[j], sum[j]);
           }
         }
@@ -1503,7 +1509,7 @@ __device__ __forceinline__ void tree_join_row(const TreeArgs& a, int lane, int c
                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + row] = (ref + log2f(l)) * kLn2;
+  if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + row] = tree_lse(ref, l);
 }
 
 // Up to 32 sequences: a warp per (node, head), which finds where its piece of

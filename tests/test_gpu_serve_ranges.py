@@ -184,3 +184,19 @@ def test_infinite_values_reach_their_viewers_whatever_their_weight(gap):
     o, _ = attend(q, cache, table, ctx, tree_mask=torch.tensor([0b001, 0b011, 0b101], device=DEV))
     assert (o[1, :, ::2] == float("inf")).all() and (o[1, :, 1::2] == -float("inf")).all()
     assert torch.isfinite(o[0]).all() and torch.isfinite(o[2]).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("ctx,nodes", [(40, 1), (3000, 1), (300, 16), (0, 1)])
+def test_lse_of_rows_whose_biases_are_the_lowest_value(ctx, nodes, kv):
+    """Such a row's LSE is that value (its scores and the count of its keys are far below its last
+    digit); a row hidden by -inf has -inf."""
+    g = torch.Generator().manual_seed(ctx)
+    n, hq, d = ctx + nodes, 2, 64
+    cache, table, _ = filled(torch.randn(n, hq, d, generator=g), torch.randn(n, hq, d, generator=g), kv)
+    q = torch.randn(nodes, hq, d, generator=g).bfloat16().to(DEV)
+    low = torch.finfo(torch.float32).min
+    t5 = torch.tensor([[low, -float("inf")]] * 32, device=DEV)
+    o, lse = attend(q, cache, table, ctx, t5_table=t5, t5_bidirectional=False)
+    assert (lse[0] == low).all() and torch.isfinite(o[:, 0]).all()
+    assert torch.isneginf(lse[1]).all() and (o[:, 1] == 0).all()
