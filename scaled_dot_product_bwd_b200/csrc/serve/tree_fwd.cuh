@@ -17,7 +17,7 @@
 // widened.  The other operand is split into two e4m3 parts x = x1 + x2 side
 // by side in the columns of one product: 4 + 4 significant bits hold a bf16
 // query exactly (down to 2^-21 of its row's largest element) and a weight to
-// 2^-8 (or 2^-21 of the largest).  Over a bf16 cache a weight is rounded to
+// 2^-8 (small ones: to 2^-20 of the largest, without bias).  Over a bf16 cache a weight is rounded to
 // bf16 (2^-8), as in the framework's forward.  A key's scale multiplies its
 // scores.  A value row's scale 2^e multiplies the weight that enters P V, and r
 // is near the maximum of s + e (over keys whose value row is not all zeros), so
@@ -547,12 +547,16 @@ __device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
                            : __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// The codes of what the codes `w` leave of two weights, times kWeightRest.
-__device__ __forceinline__ uint32_t e4m3x2_rest(float x0, float x1, uint32_t w) {
+// The codes of what the codes `w` leave of two weights, times kWeightRest, plus
+// the key's share `d` of the last step, between -1/2 and 1/2 of it.  Weights below
+// the last step (2^-20 of the largest) are many where a context is long: rounded
+// to nearest, all of one size would be lost or doubled together; with shares
+// spread evenly over the keys their sum is right.
+__device__ __forceinline__ uint32_t e4m3x2_rest(float x0, float x1, uint32_t w, __half2 d) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
-  // at most 448 * 16 in fp16: exact
-  const __half2 n = __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(-kWeightRest));
+  // at most 448 * 16 in fp16: exact (d is lost beside all but the smallest)
+  const __half2 n = __hfma2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(-kWeightRest), d);
   const float2 nf = __half22float2(n);
   float r0, r1;
   f2_unpack(f2_fma(f2_pack(x0, x1), f2_pack(kWeightRest, kWeightRest), f2_pack(nf.x, nf.y)), r0, r1);
@@ -1244,11 +1248,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         // the weights: 16 bytes of one key's rows at a time
         if constexpr (E4) {
           uint32_t hi[RT / 4], lo[RT / 4];
+          // van der Corput's sequence over the keys: 2^-9 is e4m3's last step
+          const __half2 d = __float2half2_rn(static_cast<float>(static_cast<int>(__brev(key))) * 0x1p-41f);
 #pragma unroll
           for (int j = 0; j < RT; j += 4) {
             const uint32_t h0 = e4m3x2(sc[j], sc[j + 1]), h1 = e4m3x2(sc[j + 2], sc[j + 3]);
             hi[j / 4] = h0 | h1 << 16;
-            lo[j / 4] = e4m3x2_rest(sc[j], sc[j + 1], h0) | e4m3x2_rest(sc[j + 2], sc[j + 3], h1) << 16;
+            lo[j / 4] = e4m3x2_rest(sc[j], sc[j + 1], h0, d) | e4m3x2_rest(sc[j + 2], sc[j + 3], h1, d) << 16;
           }
           if constexpr (RT == 8) *reinterpret_cast<uint4*>(pbuf) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
 #pragma unroll

@@ -5,11 +5,13 @@ Bounds are test_gpu_serve.py's (its module docstring) unless a test says otherwi
 """
 import math
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import serve_oracle as so
 from scaled_dot_product_bwd_b200 import sdpa_cache_append, sdpa_tree_fwd
-from test_gpu_serve import DEV, check_tree, make_cache, rows_of
+from test_gpu_serve import DEV, check_tree, f64, make_cache, rows_of, tree_tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +202,31 @@ def test_lse_of_rows_whose_biases_are_the_lowest_value(ctx, nodes, kv):
     o, lse = attend(q, cache, table, ctx, t5_table=t5, t5_bidirectional=False)
     assert (lse[0] == low).all() and torch.isfinite(o[:, 0]).all()
     assert torch.isneginf(lse[1]).all() and (o[:, 1] == 0).all()
+
+
+@pytest.mark.parametrize("below", [20.4, 21.0, 21.6, 23.0])
+@pytest.mark.parametrize("noise", [0.0, 1.0])
+@pytest.mark.parametrize("nodes", [1, 16, 40])
+def test_many_weights_below_the_last_step_of_the_weights(nodes, noise, below):
+    """32767 keys 2^-below of the largest weight each, all in one piece: together up to 2 % of O.
+
+    Each weight is off by at most 2^-20 of the largest, unbiased over the keys: for n keys a standard
+    deviation of at most sqrt(n) 2^-21, and six of them are allowed beside the roundings of the
+    module docstring of test_gpu_serve.py without its loss per key (2^-21 n, all of what is tested)."""
+    g = torch.Generator().manual_seed(nodes)
+    ctx, d = 32768, 64
+    n = ctx + nodes
+    u = torch.randn(1, d, generator=g).bfloat16().float()
+    k = noise * torch.randn(n, 1, d, generator=g)
+    k = k - (k @ u.T) * u / (u * u).sum() * 0.9
+    k[0] = u * (below * math.log(2) * math.sqrt(d) / (u * u).sum())
+    v = torch.ones(n, 1, d)
+    v[0, :, 1:] = 0
+    cache, table, rows = filled(k, v, page=256)
+    q = u.expand(nodes, 1, d).bfloat16().to(DEV)
+    o, _ = attend(q, cache, table, ctx, COPIES)
+    ro, _, spread, size = so.tree_attention(f64(q[:1]), rows[0][:ctx + 1], rows[1][:ctx + 1], ctx)
+    tol, _ = tree_tolerance(f64(q[:1]), rows[0], rows[1], ro, spread, size, "e4m3")
+    tol += (6 * math.sqrt(n) * 2.0 ** -21 - 2.0 ** -21 * n) * np.abs(rows[1]).max()
+    err = np.abs(f64(o[:1]) - ro)
+    assert (err <= tol).all(), (float(err.max()), float(ro[..., 1:].min()))
