@@ -166,8 +166,9 @@ sdpa_status_t sdpa_cache_gather(const sdpa_kv_cache* cache, int64_t B, const int
  * included; so may one that some nodes see: it reaches those alone.
  * Sequences whose cu_nodes, ctx_lens or pages do not fit (n outside
  * 0 .. max_nodes, rows outside T, ctx_lens[b] < 0, ctx_lens[b] + n positions
- * more than the table's width holds, a page outside the cache) are reported
- * by sdpa_serve_read_device_status as SDPA_ERR_UNSUPPORTED; their outputs are
+ * more than the table's width holds, a page outside the cache that holds a key
+ * inside the window of a node at ctx_lens[b]) are reported by
+ * sdpa_serve_read_device_status as SDPA_ERR_UNSUPPORTED; their outputs are
  * unspecified, and no memory outside the tensors is touched.
  * workspace: sdpa_tree_fwd_workspace_size() bytes, 256-byte aligned, contents
  * ignored on entry; calls that may overlap on the GPU need one each.

@@ -836,7 +836,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
         const int page = __shfl_sync(~0u, pages, in * boxes + (lane & (boxes - 1)));
         const bool copy = lane < boxes && page >= 0;
-        if (copy && page == a.num_pages) atomicOr(&g_device_status, kStatusBadSeqlens);
+        // (a page behind every node's window may be gone)
+        if (copy && page == a.num_pages &&
+            (a.wl < 0 || (walk.s.tile0 + t) * kTreeKeys + (lane + 1) * a.box_rows > walk.s.ctx - a.wl))
+          atomicOr(&g_device_status, kStatusBadSeqlens);
         const int n_copy = __popc(__ballot_sync(~0u, copy));
         const int r = ((walk.s.tile0 + t) * kTreeKeys + lane * a.box_rows) & (a.page_size - 1);
 #pragma unroll

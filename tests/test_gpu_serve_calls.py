@@ -1,0 +1,35 @@
+"""GPU tests of calls that a serving program makes: tables whose pages are gone, ties after
+a rejection, prompt chunks over a cached prefix."""
+import pytest
+import torch
+
+from scaled_dot_product_bwd_b200 import sdpa_read_device_status, sdpa_tree_fwd
+from test_gpu_serve import tree_setup
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("window", [100, 0])
+def test_pages_behind_the_window_may_be_gone(page, window, kv):
+    """Pages that hold no key inside any node's window are not reported, whatever the table says;
+    those that hold one are."""
+    lens, counts = [1000, 300, 2000], [3, 1, 17]
+    cache, q, args, mask, *_ = tree_setup(lens, counts, 4, 2, 64, page, kv)
+    want = sdpa_tree_fwd(q, tree_mask=mask, window_left=window, **args, **cache)
+    assert sdpa_read_device_status() == 0
+    table = args["page_table"].clone()
+    for b, (ctx, gone) in enumerate(zip(lens, (-1, 1 << 30, -7))):
+        table[b, :(ctx - window) // page] = gone
+    got = sdpa_tree_fwd(q, tree_mask=mask, window_left=window, **{**args, "page_table": table}, **cache)
+    assert sdpa_read_device_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for b, ctx in enumerate(lens):
+        bad = table.clone()
+        bad[b, (ctx - window) // page] = -1
+        sdpa_tree_fwd(q, tree_mask=mask, window_left=window, **{**args, "page_table": bad}, **cache)
+        assert sdpa_read_device_status() == 2
+    table[0, 0] = -1
+    sdpa_tree_fwd(q, tree_mask=mask, **{**args, "page_table": table}, **cache)    # no window: needed
+    assert sdpa_read_device_status() == 2
