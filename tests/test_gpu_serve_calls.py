@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from scaled_dot_product_bwd_b200 import sdpa_read_device_status, sdpa_tree_fwd
-from test_gpu_serve import tree_setup
+from test_gpu_serve import check_verify, tree_setup
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,25 @@ def test_pages_behind_the_window_may_be_gone(page, window, kv):
     table[0, 0] = -1
     sdpa_tree_fwd(q, tree_mask=mask, **{**args, "page_table": table}, **cache)    # no window: needed
     assert sdpa_read_device_status() == 2
+
+
+@pytest.mark.parametrize("vocab", [4, 4000, 40000])
+def test_a_tie_after_a_rejection_is_a_rejection(vocab):
+    """The second child's u q(x) equals (p - q)(x) / Z exactly, with a Z that is no power of two; next
+    to it on either side; and so the third child's after a second rejection."""
+    def spread(*at):
+        row = torch.zeros(vocab, dtype=torch.float64)
+        for x, value in zip((0, vocab // 2, vocab - 2, vocab - 1), at):
+            row[x] = value
+        return row
+    t, z = 1125 / 65536, 4800 / 65536            # t / Z = 15 / 64 = 0.375 * 0.625
+    p = spread(0.625 + t, 0.125 + z - t, 0.0, 0.0)
+    q = spread(0.625, 0.125, 0.125, 0.125)
+    assert (p.float().double() == p).all() and (q.float().double() == q).all()
+    n = 4
+    target, draft = p.float().repeat(1, n, 1), q.float().repeat(1, n, 1)
+    tokens = torch.tensor([[0, vocab - 1, 0, 0]], dtype=torch.int32)
+    parents = torch.tensor([[-1, 0, 0, 0]], dtype=torch.int32)
+    for u in (0.375, 0.375 - 2.0 ** -25, 0.375 + 2.0 ** -24):
+        for third in (0.0, 0.5):
+            check_verify(target, draft, tokens, parents, torch.tensor([[0.0, 0.5, u, third]]), torch.tensor([0.3]))
