@@ -38,9 +38,6 @@ def _deps():
     return out
 
 
-STAMP_PATH = LIB_PATH + ".stamp"
-
-
 def _source_hash(flags) -> str:
     import hashlib
     h = hashlib.sha256(" ".join(flags).encode())
@@ -50,14 +47,6 @@ def _source_hash(flags) -> str:
             with open(d, "rb") as fh:
                 h.update(fh.read())
     return h.hexdigest()
-
-
-def up_to_date(flags=()) -> bool:
-    """The library exists and was built from exactly these sources and flags."""
-    if not (os.path.exists(LIB_PATH) and os.path.exists(STAMP_PATH)):
-        return False
-    with open(STAMP_PATH) as fh:
-        return fh.read().strip() == _source_hash(flags)
 
 
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-gencode", "arch=compute_100a,code=sm_100a",
@@ -131,9 +120,17 @@ def _build_serve(verbose: bool, force: bool):
           nvcc + ["-I", INCLUDE, "-I", CSRC, os.path.join(SERVE_CSRC, "serve_api.cu")], verbose, force)
     flags, libs = _bind_flags()
     src = os.path.join(SERVE_CSRC, "serve_bind.cpp")
-    deps = [src, os.path.join(INCLUDE, "sdpa.h"), os.path.join(INCLUDE, "sdpa_serve.h")]
-    _make(SERVE_BIND_PATH, _hash(deps, flags + libs),
+    _make(SERVE_BIND_PATH, _bind_stamp(flags + libs),
           [shutil.which("g++") or "g++"] + flags + [src] + libs, verbose, force)
+
+
+def _bind_stamp(flags) -> str:
+    """Of the marshalling module: its sources and flags, and the torch and Python whose
+    headers and ABI it is compiled against (an upgrade in place changes no path)."""
+    import torch
+    deps = [os.path.join(SERVE_CSRC, "serve_bind.cpp"), os.path.join(INCLUDE, "sdpa.h"),
+            os.path.join(INCLUDE, "sdpa_serve.h")]
+    return _hash(deps, flags + [torch.__version__, str(torch.version.git_version), sys.version])
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
