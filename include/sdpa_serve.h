@@ -129,8 +129,12 @@ sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const
 /*
  * Reads the first cu_seqlens[b + 1] - cu_seqlens[b] positions of every
  * sequence b back as packed bf16 K and V [total, Hkv, d] (element strides
- * kv_t, kv_h), the operands of sdpa_fwd_varlen: one prompt chunk attends to
- * its cached prefix that way.  page_table: device int32 [B][table_width],
+ * kv_t, kv_h), the operands of sdpa_fwd_varlen.  A prompt chunk of more than 64
+ * tokens attends to its cached prefix that way: with its own rows in the cache
+ * too, and window_right = prefix length in place of the causal mask.  That mask
+ * is the whole batch's, and sdpa_fwd_varlen counts the chunk's positions from 0:
+ * so a call takes sequences of one prefix length, without a left window and
+ * without T5, ALiBi or REL biases.  page_table: device int32 [B][table_width],
  * row stride table_b.  Rows from cu_seqlens[B] to total are left as they
  * were, and so are rows whose page lies outside the table or the cache, which
  * sdpa_serve_read_device_status reports as SDPA_ERR_UNSUPPORTED.  An e4m3 value

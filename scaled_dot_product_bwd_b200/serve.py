@@ -164,7 +164,8 @@ def sdpa_cache_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None)
 def sdpa_cache_gather(k_cache, v_cache, page_table, cu_seqlens, total, k_scale=None, v_scale=None,
                       k=None, v=None):
     """The cached sequences as packed bf16 (k, v) [total, Hkv, d], sequence b's first
-    cu_seqlens[b + 1] - cu_seqlens[b] positions at its rows (see sdpa_cache_gather)."""
+    cu_seqlens[b + 1] - cu_seqlens[b] positions at its rows: the keys and values over which
+    sdpa_fwd_varlen attends from a prompt's next chunk (see sdpa_cache_gather for its limits)."""
     return (_bind or _load_bind()).gather(k_cache, v_cache, k_scale, v_scale, page_table,
                                           cu_seqlens, total, k, v)
 

@@ -3,8 +3,9 @@ a rejection, prompt chunks over a cached prefix."""
 import pytest
 import torch
 
-from scaled_dot_product_bwd_b200 import sdpa_read_device_status, sdpa_tree_fwd
-from test_gpu_serve import check_verify, tree_setup
+from scaled_dot_product_bwd_b200 import (sdpa_cache_append, sdpa_cache_gather, sdpa_fwd, sdpa_fwd_varlen,
+                                         sdpa_read_device_status, sdpa_tree_fwd)
+from test_gpu_serve import DEV, check_verify, make_cache, randn, tree_setup
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,31 @@ def test_a_tie_after_a_rejection_is_a_rejection(vocab):
     for u in (0.375, 0.375 - 2.0 ** -25, 0.375 + 2.0 ** -24):
         for third in (0.0, 0.5):
             check_verify(target, draft, tokens, parents, torch.tensor([[0.0, 0.5, u, third]]), torch.tensor([0.3]))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("prefix,chunk", [(75, 100), (1000, 129), (1, 200)])
+def test_a_prompt_chunk_over_its_cached_prefix_is_the_whole_prompt(prefix, chunk, kv):
+    """Two sequences of one prefix length: their chunks over the rows read back equal those rows of
+    causal attention over the whole prompt, over the same keys.  Both are bf16 results within the
+    attention tests' 1e-2 (1 + |O|) of the definition."""
+    g = torch.Generator().manual_seed(prefix)
+    hq, hkv, d, page, n = 8, 2, 128, 16, prefix + chunk
+    pages = -(-n // page)
+    cache = make_cache(2 * pages + 1, hkv, page, d, kv)
+    table = torch.randperm(2 * pages + 1, generator=g)[:2 * pages].view(2, pages).int().to(DEV)
+    pos = torch.arange(n, device=DEV)
+    q = randn(g, 2, n, hq, d)
+    for b in range(2):
+        slots = table[b].long()[pos // page] * page + pos % page
+        for part in (slice(0, prefix), slice(prefix, n)):
+            rows = len(slots[part])
+            sdpa_cache_append(randn(g, rows, hkv, d), randn(g, rows, hkv, d), slots[part].contiguous(), **cache)
+    i32 = lambda *x: torch.tensor(x, device=DEV, dtype=torch.int32)
+    k, v = sdpa_cache_gather(page_table=table, cu_seqlens=i32(0, n, 2 * n), total=2 * n, **cache)
+    whole, whole_lse = sdpa_fwd(q, k.view(2, n, hkv, d), v.view(2, n, hkv, d), causal=True)
+    o, lse = sdpa_fwd_varlen(q[:, prefix:].reshape(2 * chunk, hq, d), k, v, i32(0, chunk, 2 * chunk), i32(0, n, 2 * n),
+                             chunk, n, window_right=prefix)
+    want, want_lse = whole[:, prefix:].reshape(2 * chunk, hq, d).float(), whole_lse[:, :, prefix:]
+    assert ((o.float() - want).abs() <= 2e-2 * (1 + want.abs())).all()
+    assert ((lse.view(hq, 2, chunk).transpose(0, 1) - want_lse).abs() <= 2e-3).all()
