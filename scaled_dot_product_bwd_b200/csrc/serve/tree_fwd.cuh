@@ -705,9 +705,11 @@ __device__ __forceinline__ void tree_load_rows(const TreeArgs& a, const TreeWalk
   }
 }
 
-// Whether key `me` of a tile in the ring has e4m3 codes of zero alone.  (Out of
-// line: it runs where a scale stands out, and its instructions would otherwise
-// be fetched for every piece.)
+// What follows runs for unusual values alone and is kept out of line: in line,
+// its instructions would be fetched for every piece (256 sequences of 8 nodes
+// over e4m3 301 us, so 282).
+
+// Whether key `me` of a tile in the ring has e4m3 codes of zero alone.
 template <typename L>
 __device__ __noinline__ bool tree_row_of_zeros(const uint8_t* tile, int me) {
   uint32_t some = 0;
@@ -716,6 +718,87 @@ __device__ __noinline__ bool tree_row_of_zeros(const uint8_t* tile, int me) {
     some |= w.x | w.y | w.z | w.w;
   }
   return !(some & 0x7f7f7f7fu);
+}
+
+// New gains of a warpgroup's rows, from the scores `sc` of a thread's key under
+// the new references with the exponent `e` of its value scale; whether any is
+// not 1.  By all of the warpgroup.
+template <int RT>
+__device__ __noinline__ bool tree_renew_gains(const float* sc, float e, const float* refs, float* gains,
+                                              const float* facs, float* facs_o, float* mine, int wg, int warp,
+                                              int lane) {
+  for (int j = 0; j < RT; ++j) {
+    const float top = warp_max((sc[j] - refs[wg * RT + j]) + e);
+    if (lane == 0) mine[j * 4 + (warp & 3)] = top;
+  }
+  named_barrier(1 + wg, 128);
+  bool gained = false;
+  if ((warp & 3) == 0 && lane < RT) {
+    const int at = wg * RT + lane;
+    const float4 w4 = *reinterpret_cast<const float4*>(mine + lane * 4);
+    const float m = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) - kTopE4m3;
+    // (what is in O does not grow)
+    const float old = gains[at], most = fminf(old * fast_rcp(facs[at]), kMostGain);
+    const float gain = fminf(most, fabsf(refs[at]) >= kManyDigits || fabsf(m) > 1.f ? fast_exp2(-m) : 1.f);
+    gains[at] = gain;
+    if (gain != old) facs_o[at] = facs[at] * (gain * fast_rcp(old));
+    gained = gain != 1.f;
+  }
+  return barrier_or(1 + wg, 128, gained);
+}
+
+// Takes infinite and NaN values of keys hidden from some row out of a tile of V
+// (`odd`: this thread's key has some), and gives what the rows that see such a
+// key then miss.  By all threads of the tile.
+template <int D, int FMT, int R, int BIAS>
+__device__ __noinline__ void tree_take_out(int wl, int ctx, int key0, const TreeRows* info, uint8_t* vrows,
+                                           const uint8_t* weights, uint32_t* bits, uint32_t odd, uint32_t b_tile,
+                                           int row0, int warp, int lane, float* missing) {
+  using L = TreeLayout<D, FMT, R, BIAS>;
+  constexpr bool E4 = L::kE4m3;
+  constexpr uint32_t kTileThreads = 128 * L::kGroups;
+  const int me = (warp & 3) * 32 + lane;
+  const uint32_t some = __ballot_sync(~0u, odd != 0);
+  if (lane == 0 && some) atomicOr(&bits[warp & 3], some);
+  named_barrier(b_tile, kTileThreads);
+  for (int j = 0; j < L::kRT; ++j) missing[j] = 0.f;
+  for (int k4 = 0; k4 < 4; ++k4)
+    for (uint32_t left = bits[k4]; left; left &= left - 1) {
+      const int k = k4 * 32 + __ffs(left) - 1;
+      float v = 0.f;
+      if (me < D) {
+        const int byte = me * L::kCell;
+        const uint8_t* src = vrows + L::at(k, byte >> 4, kTreeKeys) + (byte & 15);
+        if (E4) v = (*src & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : 0.f;
+        else v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(src));
+      }
+      if (!isinf(v) && !isnan(v)) continue;
+      // (a row that sees the key gets it whatever its weight, as in a tile that
+      // all rows see)
+      const int nd = key0 + k - ctx;
+      const int pos = nd >= 0 ? ctx + info->depth[nd] : key0 + k;
+      const uint32_t sees = nd >= 0 ? info->seen[nd][row0 / 32] >> (row0 % 32) : ~0u;
+      const uint8_t* pk = weights + k * 16;
+      for (int j = 0; j < L::kRT; ++j) {
+        if (!((sees >> j) & 1u) || (wl >= 0 && info->pos[row0 + j] - pos > wl)) continue;
+        const int byte = (row0 + j) * L::kCell;
+        missing[j] += E4 ? v : v * __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                                       pk + (byte >> 4) * (kTreeKeys * 16) + (byte & 15)));
+      }
+    }
+  named_barrier(b_tile, kTileThreads);
+  if (row0 == 0 && me < 4) bits[me] = 0;
+  if (odd != 0) {
+    for (int c = 0; c < L::kRowBytes / 16; ++c) {
+      uint4* p = reinterpret_cast<uint4*>(vrows + L::at(me, c, kTreeKeys));
+      uint4 w = *p;
+      w.x &= ~nonfinite_bits<FMT>(w.x);
+      w.y &= ~nonfinite_bits<FMT>(w.y);
+      w.z &= ~nonfinite_bits<FMT>(w.z);
+      w.w &= ~nonfinite_bits<FMT>(w.w);
+      *p = w;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- kernel
@@ -1185,24 +1268,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           }
           if (TN < NB && !fresh) values_done(it - TN);
           if constexpr (E4) {
-            if (__builtin_expect(barrier_or(1 + wg, 128, wide), 0)) {
+            if (barrier_or(1 + wg, 128, wide)) {
+              float cold[RT];
 #pragma unroll
-              for (int j = 0; j < RT; ++j) {
-                const float of_row = warp_max((sc[j] - refs[wg * RT + j]) + true_e);
-                if (lane == 0) mine[j * 4 + (warp & 3)] = of_row;
-              }
-              named_barrier(1 + wg, 128);
-              const float4 w4 = *reinterpret_cast<const float4*>(mine + lane % RT * 4);
-              const float m = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) - kTopE4m3;
-              if (scribe) {
-                // (what is in O does not grow)
-                const float old = gains[at], most = fminf(old * fast_rcp(facs[at]), kMostGain);
-                const float gain = fminf(most, fabsf(refs[at]) >= kManyDigits || fabsf(m) > 1.f ? fast_exp2(-m) : 1.f);
-                gains[at] = gain;
-                if (gain != old) facs_o[at] = facs[at] * (gain * fast_rcp(old));
-                wide = gain != 1.f;
-              }
-              gained = barrier_or(1 + wg, 128, scribe && wide);
+              for (int j = 0; j < RT; ++j) cold[j] = sc[j];
+              gained = tree_renew_gains<RT>(cold, true_e, refs, gains, facs, facs_o, mine, wg, warp, lane);
             }
           } else {
             named_barrier(1 + wg, 128);
@@ -1277,6 +1347,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
         if constexpr (E4) find_scales(i + TN);
         bool mend = false;
+        float missing[RT];  // what the rows of this thread miss in its column of O
         if (masked) {
           // 0 * NaN is NaN: rows behind the sequence's end are zeroed (they hold
           // anything), and an infinite or NaN value of a key hidden from some
@@ -1303,54 +1374,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           }
           mend = barrier_or(b_tile, kTileThreads, odd != 0);
           if (mend) {
-            uint32_t* bits = dirty + turn * 4;
-            const uint32_t some = __ballot_sync(~0u, odd != 0);
-            if (lane == 0 && some) atomicOr(&bits[warp & 3], some);
-            named_barrier(b_tile, kTileThreads);
-            // sc becomes what the rows of this thread miss in its column of O
-#pragma unroll
-            for (int j = 0; j < RT; ++j) sc[j] = 0.f;
-#pragma unroll 1
-            for (int k4 = 0; k4 < 4; ++k4)
-#pragma unroll 1
-              for (uint32_t left = bits[k4]; left; left &= left - 1) {
-                const int k = k4 * 32 + __ffs(left) - 1;
-                float v = 0.f;
-                if (me < D) {
-                  const int byte = me * L::kCell;
-                  const uint8_t* src = vrows + L::at(k, byte >> 4, kTreeKeys) + (byte & 15);
-                  if (E4) v = (*src & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : 0.f;
-                  else v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(src));
-                }
-                if (!isinf(v) && !isnan(v)) continue;
-                // (a row that sees the key gets it whatever its weight, as in a
-                // tile that all rows see)
-                const int nd = key0 + k - s.ctx;
-                const int pos = nd >= 0 ? s.ctx + info->depth[nd] : key0 + k;
-                const uint32_t sees = nd >= 0 ? info->seen[nd][row0 / 32] >> (row0 % 32) : ~0u;
-                const uint8_t* pk = smem + L::kPOff + x * L::kPBytes + k * 16;
-#pragma unroll
-                for (int j = 0; j < RT; ++j) {
-                  if (!((sees >> j) & 1u) || (a.wl >= 0 && info->pos[row0 + j] - pos > a.wl)) continue;
-                  const int byte = (row0 + j) * L::kCell;
-                  sc[j] += E4 ? v : v * __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-                                            pk + (byte >> 4) * (kTreeKeys * 16) + (byte & 15)));
-                }
-              }
-            named_barrier(b_tile, kTileThreads);
-            if (row0 == 0 && me < 4) bits[me] = 0;
-            if (odd != 0) {
-#pragma unroll 1
-              for (int c = 0; c < kPieces; ++c) {
-                uint4* p = reinterpret_cast<uint4*>(vrows + L::at(me, c, kTreeKeys));
-                uint4 w = *p;
-                w.x &= ~nonfinite_bits<FMT>(w.x);
-                w.y &= ~nonfinite_bits<FMT>(w.y);
-                w.z &= ~nonfinite_bits<FMT>(w.z);
-                w.w &= ~nonfinite_bits<FMT>(w.w);
-                *p = w;
-              }
-            }
+            tree_take_out<D, FMT, R, BIAS>(a.wl, s.ctx, key0, info, vrows, smem + L::kPOff + x * L::kPBytes,
+                                           dirty + turn * 4, odd, b_tile, row0, warp, lane, missing);
           }
         }
         fence_async_shared();
@@ -1360,12 +1385,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         fresh = false;
         if (mend) {
           values_done(it);
-#pragma unroll
+#pragma unroll 1
           for (int j0 = 0; j0 < RT; j0 += 8) {
             float o[8];
             tmem_ld_cols<8>(t_o + j0, o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] += sc[j0 + j];
+            for (int j = 0; j < 8; ++j) o[j] += missing[j0 + j];
             tmem_st_cols<8>(t_o + j0, o);
           }
           tc_fence_before();
@@ -1426,13 +1451,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
             rr[j] = top;
           }
         }
+        // one logarithm a thread, of row + me (eight in line cost 1000 sequences a
+        // fifth of their time in instruction fetches: 502 us, 402)
+        float my_r = 0.f, my_sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (whole) o[j] *= sum[j] > 0.f || isnan(sum[j]) ? 1.f / sum[j] : 0.f;
-          if (me == j && j0 + j < n_rows) {
-            if (whole) a.lse[info->lse[row + j]] = tree_lse(rr[j], sum[j]);
-            else a.part_ml[part + j0 + j] = make_float2(rr[j], sum[j]);
+          if (me == j) {
+            my_r = rr[j];
+            my_sum = sum[j];
           }
+        }
+        if (me < 8 && j0 + me < n_rows) {
+          if (whole) a.lse[info->lse[row + me]] = tree_lse(my_r, my_sum);
+          else a.part_ml[part + j0 + me] = make_float2(my_r, my_sum);
         }
         if (me < D) {
 #pragma unroll
