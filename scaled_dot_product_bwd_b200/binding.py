@@ -501,7 +501,7 @@ def sdpa_read_device_status() -> int:
 def sdpa_set_wait_limit_ns(ns: int):
     from . import serve
     load_library().sdpa_set_wait_limit_ns(int(ns))
-    serve.load_serve_library().sdpa_serve_set_wait_limit_ns(int(ns))
+    serve.set_wait_limit_ns(int(ns))
 
 
 def sdpa_debug_wait_timeout():

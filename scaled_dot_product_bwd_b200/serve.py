@@ -64,6 +64,7 @@ class Verify(ctypes.Structure):
 
 _lib = None
 _bind = None
+_wait_limit_ns = None    # set before the library was loaded
 
 
 def load_serve_library(path: str | None = None) -> ctypes.CDLL:
@@ -102,6 +103,8 @@ def load_serve_library(path: str | None = None) -> ctypes.CDLL:
     lib.sdpa_serve_set_wait_limit_ns.restype = None
     if path is None:
         _lib = lib
+        if _wait_limit_ns is not None:
+            lib.sdpa_serve_set_wait_limit_ns(_wait_limit_ns)
     return lib
 
 
@@ -117,15 +120,23 @@ def _load_bind():
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_serve", loader))
         loader.exec_module(mod)
         mod.set_error((SdpaError, torch.OutOfMemoryError))
+        load_serve_library()
         _bind = mod
     return _bind
 
 
 def read_device_status(stream) -> int:
     """The serving kernels' status on `stream`'s device (0 while the library is not loaded)."""
-    if _lib is None and _bind is None:
-        return 0
-    return int(load_serve_library().sdpa_serve_read_device_status(stream))
+    return 0 if _lib is None else int(_lib.sdpa_serve_read_device_status(stream))
+
+
+def set_wait_limit_ns(ns: int):
+    """The wait limit of the serving kernels, now or (a program that only trains need not have
+    the library) as soon as it is loaded."""
+    global _wait_limit_ns
+    _wait_limit_ns = ns
+    if _lib is not None:
+        _lib.sdpa_serve_set_wait_limit_ns(ns)
 
 
 def sdpa_rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, original_length=0,

@@ -1,0 +1,48 @@
+"""Attention calls do without the serving library (no GPU needed)."""
+import pytest
+
+from scaled_dot_product_bwd_b200 import binding, serve
+from scaled_dot_product_bwd_b200.build import build
+
+
+class Function:
+    """A library's function, which remembers its last arguments."""
+    def __init__(self):
+        self.got = None
+
+    def __call__(self, *args):
+        self.got = args
+
+
+class Library:
+    """Any name is a function."""
+    def __getattr__(self, name):
+        self.__dict__[name] = f = Function()
+        return f
+
+
+@pytest.fixture
+def unloaded(monkeypatch):
+    build()
+    for name in ("_lib", "_bind", "_wait_limit_ns"):
+        monkeypatch.setattr(serve, name, None, raising=False)
+    yield monkeypatch
+    binding.load_library().sdpa_set_wait_limit_ns(2000000000)
+
+
+def test_the_wait_limit_is_set_without_the_serving_library(unloaded, tmp_path):
+    unloaded.setattr(serve, "SERVE_LIB_PATH", str(tmp_path / "missing.so"))
+    binding.sdpa_set_wait_limit_ns(2000000000)
+    assert serve.read_device_status(None) == 0
+    with pytest.raises(RuntimeError):
+        serve.load_serve_library()
+
+
+def test_the_wait_limit_reaches_a_library_loaded_later(unloaded):
+    binding.sdpa_set_wait_limit_ns(1500000000)
+    library = Library()
+    unloaded.setattr(serve.ctypes, "CDLL", lambda path: library)
+    serve.load_serve_library()
+    assert library.sdpa_serve_set_wait_limit_ns.got == (1500000000,)
+    binding.sdpa_set_wait_limit_ns(1600000000)
+    assert library.sdpa_serve_set_wait_limit_ns.got == (1600000000,)
