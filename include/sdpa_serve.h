@@ -31,8 +31,8 @@ extern "C" {
  * launch; Hkv = 0: q alone (k and k_out ignored).  Strides in elements,
  * multiples of 8, inputs and outputs each their own.  q_out may be q itself
  * with the same strides (and k_out k): in place; other overlap is not allowed.
- *   positions: device int32 [B, L] with row stride pos_b (L contiguous), any
- *     sign; NULL: position offset + l.
+ *   positions: device int32 [B, L] with row stride pos_b (L contiguous; 0: one
+ *     row for all sequences), any sign; NULL: position offset + l.
  *   freqs: device float64 [rot / 2], radians per position
  *     (sdpa_rope_frequencies).  The angle is formed and reduced in float64, so
  *     positions of a long context lose nothing; the rest is float32 with one
@@ -135,7 +135,7 @@ sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const
  * is the whole batch's, and sdpa_fwd_varlen counts the chunk's positions from 0:
  * so a call takes sequences of one prefix length, without a left window and
  * without T5, ALiBi or REL biases.  page_table: device int32 [B][table_width],
- * row stride table_b.  Rows from cu_seqlens[B] to total are left as they
+ * row stride table_b (0: one row for all).  Rows from cu_seqlens[B] to total are left as they
  * were, and so are rows whose page lies outside the table or the cache, which
  * sdpa_serve_read_device_status reports as SDPA_ERR_UNSUPPORTED.  An e4m3 value
  * times its scale is exact in bf16 (below bf16's smallest normal number, to
@@ -188,7 +188,7 @@ typedef struct sdpa_tree {
   int64_t o_t, o_h; /* element strides of o */
   const int32_t* cu_nodes;   /* device [B + 1] */
   const int32_t* ctx_lens;   /* device [B] */
-  const int32_t* page_table; /* device [B][table_width], row stride table_b */
+  const int32_t* page_table; /* device [B][table_width], row stride table_b (0: one for all) */
   int64_t table_width, table_b;
   const int64_t* tree_mask;  /* device [T] or NULL */
   int64_t window_left;

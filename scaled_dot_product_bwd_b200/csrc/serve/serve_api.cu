@@ -97,6 +97,9 @@ bool good_stride(int64_t v, int64_t multiple) {
   return v > 0 && v % multiple == 0 && v < (1ll << 38);
 }
 
+// Row stride of a matrix that is only read: rows side by side, or one for all.
+bool row_step(int64_t v, int64_t width) { return v == 0 || v >= width; }
+
 // ------------------------------------------------------------------ rotary
 template <int D>
 cudaError_t launch_rope(const RopeArgs& a, int mode, cudaStream_t st) {
@@ -195,7 +198,7 @@ sdpa_status_t check_tree(const sdpa_tree* t, const sdpa_kv_cache* c, CacheView& 
   if (t->max_nodes > kTreeMaxNodes || t->B > 65535 || t->Hq > 65535 || t->T >= (1ll << 30))
     return SDPA_ERR_UNSUPPORTED;
   if (!t->cu_nodes || !t->ctx_lens || !t->page_table || t->table_width < 1 ||
-      t->table_b < t->table_width)
+      !row_step(t->table_b, t->table_width))
     return SDPA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(t->cu_nodes) & 3u) || (reinterpret_cast<uintptr_t>(t->ctx_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(t->page_table) & 3u) || (reinterpret_cast<uintptr_t>(t->tree_mask) & 7u))
@@ -279,7 +282,7 @@ sdpa_status_t sdpa_rope(const sdpa_rope_desc* r, const void* q, const void* k, v
     return SDPA_ERR_UNSUPPORTED;
   if (!std::isfinite(r->amplitude)) return SDPA_ERR_INVALID_ARG;
   if (!r->freqs || (reinterpret_cast<uintptr_t>(r->freqs) & 7u) ||
-      (reinterpret_cast<uintptr_t>(r->positions) & 3u) || (r->positions && r->B > 1 && r->pos_b < r->L))
+      (reinterpret_cast<uintptr_t>(r->positions) & 3u) || (r->positions && r->B > 1 && !row_step(r->pos_b, r->L)))
     return SDPA_ERR_INVALID_ARG;
   if (!q || !q_out || !aligned16(q) || !aligned16(q_out)) return SDPA_ERR_INVALID_ARG;
   const int64_t sq[] = {r->q_b, r->q_l, r->q_h, r->qo_b, r->qo_l, r->qo_h};
@@ -411,7 +414,7 @@ sdpa_status_t sdpa_cache_gather(const sdpa_kv_cache* cache, int64_t B, const int
   GatherArgs a{};
   const sdpa_status_t st = check_cache(cache, a.c);
   if (st != SDPA_OK) return st;
-  if (B < 1 || total < 0 || !page_table || table_width < 1 || table_b < table_width || !cu_seqlens ||
+  if (B < 1 || total < 0 || !page_table || table_width < 1 || !row_step(table_b, table_width) || !cu_seqlens ||
       (reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
     return SDPA_ERR_INVALID_ARG;
   if (B > 65535 || total >= (1ll << 30) || table_width >= (1ll << 31)) return SDPA_ERR_UNSUPPORTED;

@@ -4,8 +4,9 @@ import pytest
 import torch
 
 from scaled_dot_product_bwd_b200 import (sdpa_cache_append, sdpa_cache_gather, sdpa_fwd, sdpa_fwd_varlen,
-                                         sdpa_read_device_status, sdpa_tree_fwd)
-from test_gpu_serve import DEV, check_verify, make_cache, randn, tree_setup
+                                         sdpa_read_device_status, sdpa_rope, sdpa_rope_frequencies,
+                                         sdpa_spec_verify, sdpa_tree_fwd)
+from test_gpu_serve import DEV, check_verify, draw_tree, make_cache, randn, tree_setup
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,80 @@ def test_a_prompt_chunk_over_its_cached_prefix_is_the_whole_prompt(prefix, chunk
     want, want_lse = whole[:, prefix:].reshape(2 * chunk, hq, d).float(), whole_lse[:, :, prefix:]
     assert ((o.float() - want).abs() <= 2e-2 * (1 + want.abs())).all()
     assert ((lse.view(hq, 2, chunk).transpose(0, 1) - want_lse).abs() <= 2e-3).all()
+
+
+def test_one_row_of_positions_or_pages_for_all_sequences():
+    g = torch.Generator().manual_seed(1)
+    freqs, _ = sdpa_rope_frequencies(64)
+    q = randn(g, 3, 20, 2, 64)
+    pos = torch.arange(20, device=DEV, dtype=torch.int32) * 7
+    assert torch.equal(sdpa_rope(q, None, freqs, pos.expand(3, 20))[0], sdpa_rope(q, None, freqs, pos.repeat(3, 1))[0])
+    cache, q, args, mask, *_ = tree_setup([40, 40, 17], [2, 2, 2], 2, 2, 64, 16, "bf16")
+    table = args["page_table"][:1]
+    one, each = ({**args, "page_table": t} for t in (table.expand(3, -1), table.repeat(3, 1)))
+    a, b = sdpa_tree_fwd(q, tree_mask=mask, **one, **cache), sdpa_tree_fwd(q, tree_mask=mask, **each, **cache)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    cu = torch.tensor([0, 40, 45, 62], device=DEV, dtype=torch.int32)
+    a, b = (sdpa_cache_gather(page_table=x["page_table"], cu_seqlens=cu, total=62, **cache) for x in (one, each))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_two_streams_at_once(kv):
+    """Calls of different sizes on two streams, whose kernels may run side by side: the same bits."""
+    cases = []
+    for seed, (lens, counts) in enumerate((([3000, 100, 5], [7, 1, 16]), ([800] * 40, [1] * 40))):
+        cache, q, args, mask, *_ = tree_setup(lens, counts, 8, 2, 128, 64, kv, seed=seed)
+        t, d, x, p, ua, us = (y.to(DEV) for y in draw_tree(torch.Generator().manual_seed(seed), 4, 9, 9000))
+        def call(cache=cache, q=q, args=args, mask=mask, v=(t, d, x, p, ua, us)):
+            return *sdpa_tree_fwd(q, tree_mask=mask, **args, **cache), *sdpa_spec_verify(*v)
+        cases.append((call, call()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (call, _) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(call())
+    torch.cuda.synchronize()
+    for i, (_, want) in enumerate(cases):
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_generation_step_in_a_graph(kv):
+    """Rotation, write, attention, read-back and verification captured together and replayed with
+    other inputs: what the calls give one by one."""
+    g = torch.Generator().manual_seed(3)
+    hq, hkv, d, page, n, ctx = 8, 2, 128, 16, 6, 90
+    freqs, amp = sdpa_rope_frequencies(d, scaling="yarn", factor=4.0, original_length=64)
+    cache = make_cache(8, hkv, page, d, kv)
+    table = torch.tensor([[5, 0, 7, 2, 1, 3, 6]], device=DEV, dtype=torch.int32)
+    i32 = lambda *x: torch.tensor(x, device=DEV, dtype=torch.int32)
+    slot = lambda pos: table[0].long()[pos // page] * page + pos % page
+    sdpa_cache_append(randn(g, ctx, hkv, d), randn(g, ctx, hkv, d), slot(torch.arange(ctx, device=DEV)), **cache)
+    q, k, v = randn(g, n, hq, d), randn(g, n, hkv, d), randn(g, n, hkv, d)
+    pos, slots = i32(*range(ctx, ctx + n)), slot(ctx + torch.arange(n, device=DEV))
+    cu, ctx_lens, all_rows = i32(0, n), i32(ctx), i32(0, ctx + n)
+    tree = [t.to(DEV) for t in draw_tree(g, 1, n, 500, chain=True)]
+
+    def step():
+        rq, rk = sdpa_rope(q, k, freqs, pos, amplitude=amp)
+        sdpa_cache_append(rk, v, slots, **cache)
+        o, lse = sdpa_tree_fwd(rq, page_table=table, ctx_lens=ctx_lens, cu_nodes=cu, max_nodes=n, **cache)
+        return rq, o, lse, *sdpa_cache_gather(page_table=table, cu_seqlens=all_rows, total=ctx + n, **cache), \
+            *sdpa_spec_verify(*tree)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in range(3):
+        g = torch.Generator().manual_seed(100 + seed)
+        for t in (q, k, v):
+            t.copy_(randn(g, *t.shape))
+        for t, new in zip(tree, draw_tree(g, 1, n, 500, chain=True)):
+            t.copy_(new)
+        graph.replay()
+        kept = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(kept, step()))

@@ -1,4 +1,4 @@
-"""Attention calls do without the serving library (no GPU needed)."""
+"""Attention calls do without the serving library, and checks of its arguments (no GPU needed)."""
 import pytest
 
 from scaled_dot_product_bwd_b200 import binding, serve
@@ -46,3 +46,18 @@ def test_the_wait_limit_reaches_a_library_loaded_later(unloaded):
     assert library.sdpa_serve_set_wait_limit_ns.got == (1500000000,)
     binding.sdpa_set_wait_limit_ns(1600000000)
     assert library.sdpa_serve_set_wait_limit_ns.got == (1600000000,)
+
+
+def test_a_row_stride_of_zero_passes_the_checks_and_one_below_the_width_does_not():
+    """Past the stride, what follows in the checks refuses: a missing workspace, a missing output."""
+    import ctypes
+
+    from test_serve_abi import FAKE, NULL, _cache, _rope, _tree
+    lib = serve.load_serve_library()
+    c = _cache()
+    for step, code in ((0, 3), (4, 1)):
+        t = _tree(table_b=step)
+        assert lib.sdpa_tree_fwd(ctypes.byref(t), ctypes.byref(c), FAKE, None, 0.1, FAKE, FAKE, NULL, 0, None) == code
+        assert (lib.sdpa_tree_fwd_workspace_size(ctypes.byref(t), ctypes.byref(c)) > 0) == (step == 0)
+    r = _rope(pos_b=0)
+    assert lib.sdpa_rope(ctypes.byref(r), FAKE, FAKE, FAKE, NULL, None) == 1      # (for k_out)
