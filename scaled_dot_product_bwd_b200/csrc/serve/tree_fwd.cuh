@@ -565,15 +565,18 @@ __device__ __forceinline__ uint32_t e4m3x2_rest(float x0, float x1, uint32_t w, 
 
 // b * log2(e) of a bias b, kept finite where b is: a bias of the type's lowest
 // value then still orders below every other score instead of hiding its key.
+// It stays above the reference -FLT_MAX of a row that has seen no key, so that
+// the first such key is seen to outgrow it.
+constexpr float kLowest = -0x1.fffffcp127f;
 __device__ __forceinline__ float bias_to_log2(float b) {
   const float x = b * kLog2e;
-  return isinf(x) && !isinf(b) ? copysignf(FLT_MAX, b) : x;
+  return isinf(b) ? x : fminf(fmaxf(x, kLowest), -kLowest);
 }
 
-// LSE of a row with reference r and sum l (0: it sees nothing).  A reference at
-// the lowest value is a bias of the lowest value, which bias_to_log2 kept there.
+// LSE of a row with reference r and sum l (0: it sees nothing).  A reference of
+// kLowest is a bias of the lowest value.
 __device__ __forceinline__ float tree_lse(float r, float l) {
-  return r == -FLT_MAX && l > 0.f ? -FLT_MAX : (r + log2f(l)) * kLn2;
+  return r == kLowest ? -FLT_MAX : (r + log2f(l)) * kLn2;
 }
 
 __device__ __forceinline__ float t5_bias_log2(const TreeArgs& a, int rel, int h) {

@@ -230,3 +230,25 @@ def test_many_weights_below_the_last_step_of_the_weights(nodes, noise, below):
     tol += (6 * math.sqrt(n) * 2.0 ** -21 - 2.0 ** -21 * n) * np.abs(rows[1]).max()
     err = np.abs(f64(o[:1]) - ro)
     assert (err <= tol).all(), (float(err.max()), float(ro[..., 1:].min()))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -20])
+@pytest.mark.parametrize("nodes,copies", [(1, 1), (1, COPIES), (16, COPIES), (40, COPIES)])
+def test_the_lowest_bias_after_tiles_that_a_row_does_not_see(nodes, copies, size, kv):
+    """Far keys hidden by a bias of -inf, near ones under the type's lowest value: the near ones' mean
+    (q = 0), whose weights the tiles before have left no reference for."""
+    g = torch.Generator().manual_seed(nodes)
+    ctx, d = 1000, 64
+    n = ctx + nodes
+    v = size * torch.randn(n, 1, d, generator=g) * torch.exp2(torch.randint(-3, 4, (n, 1, 1), generator=g).float())
+    cache, table, rows = filled(torch.randn(n, 1, d, generator=g), v, kv)
+    q = torch.zeros(nodes, 1, d, device=DEV).bfloat16()
+    t5 = torch.full((32, 1), torch.finfo(torch.float32).min)
+    t5[28:] = -float("inf")
+    o, _ = attend(q, cache, table, ctx, copies, t5_table=t5.to(DEV), t5_bidirectional=False)
+    t5[:28] = 0.0                                # (the same weights for the float64 definition)
+    ro, _, spread, size = so.tree_attention(f64(q), *rows, ctx, t5_table=t5.numpy())
+    tol, _ = tree_tolerance(f64(q), *rows, ro, spread, size, kv)
+    err = np.abs(f64(o) - ro)
+    assert (err <= tol).all(), float((err / tol).max())
