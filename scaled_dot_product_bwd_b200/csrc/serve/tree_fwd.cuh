@@ -157,8 +157,8 @@ struct TreeLayout {
   // warpgroups that do not write it out go on to the next)
   static constexpr int kSumOff = kMaxOff + 4 * kTreeRT * 16;     // [2][4][kTreeRT][4] floats
   static constexpr int kRefOff = kSumOff + 2 * 4 * kTreeRT * 16; // [2][4][kTreeRT] floats
-  static constexpr int kFacOff = kRefOff + 2 * 4 * kTreeRT * 4;  // [4][kTreeRT] floats, e4m3: of l and of O
-  static constexpr int kGainOff = kFacOff + (kE4m3 ? 2 : 1) * 4 * kTreeRT * 4;     // [2][4][kTreeRT] floats (e4m3)
+  static constexpr int kFacOff = kRefOff + 2 * 4 * kTreeRT * 4;  // [4][kTreeRT] floats, e4m3: three times
+  static constexpr int kGainOff = kFacOff + (kE4m3 ? 3 : 1) * 4 * kTreeRT * 4;     // [2][4][kTreeRT] floats (e4m3)
   static constexpr int kBucketOff = kGainOff + (kE4m3 ? 2 * 4 * kTreeRT * 4 : 0);  // [kTreeBuckets] bytes
   static constexpr int kT5Off = kBucketOff + (BIAS ? kTreeBuckets : 0);  // [2][kTreeT5Slice] floats
   static constexpr int kMiscOff = kT5Off + (BIAS ? 2 * kTreeT5Slice * 4 : 0);
@@ -527,13 +527,13 @@ constexpr float kQueryRest = 16.f, kWeightRest = 16.f;
 // Weights are 2^(s - r).  Over a bf16 cache r is a maximum that a later score
 // may outgrow by 2^8 before O is rescaled; over e4m3, whose largest value is
 // 448, r is set 7 below the maximum of s + e and outgrown at 2^8.7 = 416.  There
-// e counts from kLeastE to kMostE, so that l, whose terms are 2^-e as large,
-// stays finite over 2^17 keys and loses none above 2^-43 of the largest.  Where
-// that leaves a row's weights small or large, or r has less than 3 bits below
-// the point (from kManyDigits on), its weights are 2^(s - r) times 2^e times a
-// gain 2^-t, t found as r is, from s - r + e.
+// e counts from kLeastE to kMostE: r then moves by at most 2^97 for the values'
+// sake, and l, whose terms are 2^-e as large, loses nothing above 2^-29 of the
+// largest when it does.  Where that leaves a row's weights small or large, or r
+// has less than 3 bits below the point (from kManyDigits on), its weights are
+// 2^(s - r) times 2^e times a gain 2^-t, t found as r is, from s - r + e.
 constexpr float kTopBf16 = 0.f, kOverBf16 = 8.f, kTopE4m3 = 7.f, kOverE4m3 = 8.7f;
-constexpr float kLeastE = -103.f, kMostE = 90.f, kManyDigits = 0x1p20f, kMostGain = 0x1p120f;
+constexpr float kLeastE = -45.f, kMostE = 45.f, kManyDigits = 0x1p20f, kMostGain = 0x1p120f;
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -725,11 +725,11 @@ __device__ __noinline__ bool tree_row_of_zeros(const uint8_t* tile, int me) {
 
 // New gains of a warpgroup's rows, from the scores `sc` of a thread's key under
 // the new references with the exponent `e` of its value scale; whether any is
-// not 1.  By all of the warpgroup.
+// not 1 (`had`: whether one was).  By all of the warpgroup.
 template <int RT>
-__device__ __noinline__ bool tree_renew_gains(const float* sc, float e, const float* refs, float* gains,
-                                              const float* facs, float* facs_o, float* mine, int wg, int warp,
-                                              int lane) {
+__device__ __noinline__ bool tree_renew_gains(const float* sc, float e, bool had, const float* refs, float* gains,
+                                              const float* facs, float* facs_o, float* peaks, float* mine, int wg,
+                                              int warp, int lane) {
   for (int j = 0; j < RT; ++j) {
     const float top = warp_max((sc[j] - refs[wg * RT + j]) + e);
     if (lane == 0) mine[j * 4 + (warp & 3)] = top;
@@ -740,11 +740,16 @@ __device__ __noinline__ bool tree_renew_gains(const float* sc, float e, const fl
     const int at = wg * RT + lane;
     const float4 w4 = *reinterpret_cast<const float4*>(mine + lane * 4);
     const float m = fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)) - kTopE4m3;
-    // (what is in O does not grow)
-    const float old = gains[at], most = fminf(old * fast_rcp(facs[at]), kMostGain);
-    const float gain = fminf(most, fabsf(refs[at]) >= kManyDigits || fabsf(m) > 1.f ? fast_exp2(-m) : 1.f);
+    // the largest m that O holds weights of, under the new r: the gain lifts O
+    // by 2^80 at most, so that it stays finite
+    const float held = fmaxf((had ? peaks[at] : 0.f) + __log2f(facs[at]), m);
+    const float old = gains[at];
+    float gain = fabsf(refs[at]) >= kManyDigits || fabsf(m) > 1.f ? fast_exp2(-m) : 1.f;
+    if (m == -INFINITY) gain = old;
+    gain = fminf(fminf(gain, fast_exp2(80.f - held)), kMostGain);
+    peaks[at] = held;
     gains[at] = gain;
-    if (gain != old) facs_o[at] = facs[at] * (gain * fast_rcp(old));
+    if (gain != old) facs_o[at] = facs[at] * gain * fast_rcp(old);
     gained = gain != 1.f;
   }
   return barrier_or(1 + wg, 128, gained);
@@ -1039,6 +1044,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
     float* mine = wmax + wg * RT * 4;
     float* facs = reinterpret_cast<float*>(smem + L::kFacOff);    // [4][RT]: what the last rescaling took of l
     float* facs_o = facs + (E4 ? 4 * kTreeRT : 0);                // ... and of O
+    float* peaks = facs_o + 4 * kTreeRT;                          // [4][RT] of rows with gains (e4m3)
     // After a wait that ran out the warps go on without waiting, through the
     // same barriers, so that no thread is left at one.
     bool ok = true;
@@ -1223,7 +1229,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
           f2_unpack(f2_sub(f2_pack(sc[j], sc[j + 1]), f2_pack(ref[j], ref[j + 1])), d0, d1);
           over = fmax3(over, d0, d1);
         }
-        if (barrier_or(1 + wg, 128, over + e > (E4 ? kOverE4m3 : kOverBf16) || fresh || gained)) {
+        if (barrier_or(1 + wg, 128, over + e > (E4 ? kOverE4m3 : kOverBf16) || fresh || gained ||
+                                        (E4 && v_byte < 127 + static_cast<int>(kLeastE)))) {
           const bool scribe = (warp & 3) == 0 && lane < RT;  // keeps row `lane`'s reference
           const int at = wg * RT + lane;
           auto rows_top = [&](const float (&y)[RT]) {  // for the scribes: their row's largest, less kTop
@@ -1275,7 +1282,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
               float cold[RT];
 #pragma unroll
               for (int j = 0; j < RT; ++j) cold[j] = sc[j];
-              gained = tree_renew_gains<RT>(cold, true_e, refs, gains, facs, facs_o, mine, wg, warp, lane);
+              gained = tree_renew_gains<RT>(cold, true_e, gained, refs, gains, facs, facs_o, peaks, mine, wg, warp, lane);
             }
           } else {
             named_barrier(1 + wg, 128);

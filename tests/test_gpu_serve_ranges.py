@@ -252,3 +252,20 @@ def test_the_lowest_bias_after_tiles_that_a_row_does_not_see(nodes, copies, size
     tol, _ = tree_tolerance(f64(q), *rows, ro, spread, size, kv)
     err = np.abs(f64(o) - ro)
     assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("sizes", [(0.0, 2.0 ** 100), (2.0 ** 100, 0.0), (2.0 ** -110, 2.0 ** 100), (2.0 ** 110, 2.0 ** -110),
+                                   (0.0, 2.0 ** -110), (2.0 ** -40, 2.0 ** 60), (0.0, 1.0, 2.0 ** 90, 2.0 ** -90)])
+@pytest.mark.parametrize("nodes,copies", [(1, 1), (1, COPIES), (16, COPIES), (40, COPIES)])
+def test_values_of_one_size_after_values_of_another(nodes, copies, sizes):
+    """Each size for some tiles, scores alike: every key counts in the sum of weights, whatever its value."""
+    g = torch.Generator().manual_seed(nodes)
+    d, run = 64, 640
+    n = run * len(sizes) + nodes
+    v = torch.randn(n, 1, d, generator=g)
+    for i in range(n):
+        v[i] *= sizes[min(i // run, len(sizes) - 1)]
+    cache, table, rows = filled(torch.randn(n, 1, d, generator=g), v)
+    q = torch.randn(nodes, 1, d, generator=g).bfloat16().to(DEV)
+    o, lse = attend(q, cache, table, n - nodes, copies)
+    check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
