@@ -37,7 +37,7 @@ extern "C" {
  *     (sdpa_rope_frequencies).  The angle is formed and reduced in float64, so
  *     positions of a long context lose nothing; the rest is float32 with one
  *     rounding to bf16.
- *   d in {64, 128}; rot even, 2 <= rot <= d; B * L < 2^31.
+ *   d in {64, 128}; rot even, 2 <= rot <= d; 1 <= B * L < 2^31.
  */
 typedef struct sdpa_rope_desc {
   int64_t B, L, Hq, Hkv, d;
@@ -89,7 +89,7 @@ sdpa_status_t sdpa_rope_frequencies(int32_t rot, double base, int32_t scaling, d
  *   SDPA_CACHE_BF16: bf16 rows; the scales are ignored.
  *   SDPA_CACHE_E4M3: 8-bit rows (e4m3, no infinities, largest value 448) with
  *     one power-of-two scale per row and head: value = code * 2^(e - 127), e
- *     a byte of k_scale / v_scale [num_pages][Hkv][page_size] (strides
+ *     a byte 0 .. 254 of k_scale / v_scale [num_pages][Hkv][page_size] (strides
  *     scale_stride_page, scale_stride_head, multiples of 16; rows contiguous;
  *     16-byte aligned).  A power of two costs an e4m3 code nothing (its
  *     relative step is the same in every binade) and makes scaling exact both
@@ -176,11 +176,20 @@ sdpa_status_t sdpa_cache_gather(const sdpa_kv_cache* cache, int64_t B, const int
  * unspecified, and no memory outside the tensors is touched.
  * workspace: sdpa_tree_fwd_workspace_size() bytes, 256-byte aligned, contents
  * ignored on entry; calls that may overlap on the GPU need one each.
- * B, Hq <= 65535; T < 2^30; table_width * page_size <= 2^30, and the batch's
+ * 1 <= B, Hq <= 65535; 1 <= T < 2^30 (a batch without rows is refused, as by
+ * sdpa_fwd); table_width * page_size <= 2^30, and the batch's
  * tiles of 128 keys over KV heads and blocks of 16 query rows are counted in 32
  * bits: SDPA_ERR_UNSUPPORTED where they could pass that.
  * Deterministic: the split of the keys depends on the lengths and the GPU's
  * number of SMs alone, and sums are taken in a fixed order.
+ * Accuracy: scores, maxima, sums and O are float32.  A weight enters the product
+ * with V rounded to bf16 over a bf16 cache (half a step, 2^-9 of it), as in
+ * sdpa_fwd, and as two e4m3 parts over an e4m3 cache: to 2^-8 of it, or to 2^-20
+ * of the largest weight times value scale of its row, rounded without bias over
+ * the keys, whichever is more.  What a key adds to LSE is not rounded.  A bf16
+ * query's elements are exact over e4m3 down to 2^-21 of their row's largest (and
+ * 2^-132).  A score's bias near the type's lowest value leaves no digits for the
+ * score, as in float32.
  */
 typedef struct sdpa_tree {
   int64_t B, T, max_nodes, Hq;
@@ -221,7 +230,7 @@ sdpa_status_t sdpa_tree_fwd(const sdpa_tree* tree, const sdpa_kv_cache* cache, c
  *     u_accept[0] are not read; parents NULL: a chain (parents[n] = n - 1).
  *     A token outside [0, V) is never accepted and removes draft[at] from w as
  *     any rejected one; a parent >= n makes n no node.  Both are reported by
- *     sdpa_serve_read_device_status as SDPA_ERR_UNSUPPORTED.
+ *     sdpa_serve_read_device_status as SDPA_ERR_UNSUPPORTED.  B >= 1.
  *   u_accept [B, N], u_sample [B]: device float32, in [0, 1).
  * Outputs: path int32 [B, N]: the accepted nodes from node 0 on, then -1;
  * accepted int32 [B]: how many after node 0; next_token int32 [B].  If all

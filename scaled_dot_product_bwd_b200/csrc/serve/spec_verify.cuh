@@ -15,9 +15,10 @@
 // sequence's passes, so one sequence is not left to one SM's loads, and the
 // partial sums travel through distributed shared memory inside one launch.
 // All sums are float64 in a fixed order.
-// Measured at 32000 tokens: a chain of 5 nodes 5.7 us, 32 trees of 16 nodes
-// 14.7 us (with cluster barriers instead of counted stores 16.2; with node 0's
-// rows read ahead of the nodes' numbers the same).
+// Measured at 32000 tokens: a chain of 5 nodes 6.1 us, 32 trees of 16 nodes
+// 16.2 us (tried when they took 14.7: cluster barriers instead of counted stores
+// 16.2, node 0's rows read ahead of the nodes' numbers the same); 8 trees of 16
+// nodes at 128256 tokens, whose passes read the rows again, 53 us.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -17,13 +17,14 @@
 // widened.  The other operand is split into two e4m3 parts x = x1 + x2 side
 // by side in the columns of one product: 4 + 4 significant bits hold a bf16
 // query exactly (down to 2^-21 of its row's largest element) and a weight to
-// 2^-8 (small ones: to 2^-20 of the largest, without bias).  Over a bf16 cache a weight is rounded to
-// bf16 (2^-8), as in the framework's forward.  A key's scale multiplies its
-// scores.  A value row's scale 2^e multiplies the weight that enters P V, and r
-// is near the maximum of s + e (over keys whose value row is not all zeros), so
-// that what enters stays in range whatever the scales are; l adds 2^(s - r).  Where r is so large that e would be rounded away
-// (every key under a bias of the type's lowest value), a row has a gain of its
-// own for P V.
+// 2^-8 (small ones: to 2^-20 of the largest, without bias over the keys).  Over
+// a bf16 cache a weight is rounded to bf16 (2^-8), as in the framework's forward.
+// A key's scale multiplies its scores.  A value row's scale 2^e multiplies the
+// weight that enters P V, and r is near the maximum of s + e (over keys whose
+// value row is not all zeros), so that what enters stays in range whatever the
+// scales are; l adds 2^(s - r).  Where e is beyond +-45, or r so large that e
+// would be rounded away (every key under a bias of the type's lowest value), a
+// row has a gain of its own for P V, renewed with every tile.
 //
 // Bound by DRAM: a cached byte takes 2 to 128 FLOPs (1 to 64 rows).  What
 // costs is keeping enough loads in flight and every SM busy:
@@ -39,19 +40,21 @@
 //    of 16 rows.  The softmax's chain of waits per tile (~700 cycles) is what
 //    one warpgroup would pay again and again, so up to 16 rows the four take
 //    turns by tile, each with an O of its own; at 32 two pairs do; at 64 they
-//    share every tile by rows.  Up to 8 rows a thread does 8, not 16 (e4m3
-//    d = 64 49 -> 44 us, 1000 sequences of 500 bf16 keys 579 -> 484; bf16
-//    d = 64 53 -> 54).
+//    share every tile by rows.  Up to 8 rows a thread does 8, not 16 (when it
+//    came: e4m3 d = 64 49 -> 44 us, 1000 sequences of 500 bf16 keys 579 -> 484;
+//    bf16 d = 64 53 -> 54).
 // Measured (32 query, 8 KV heads; 6.56 TB/s is a copy's rate):
-//   16 sequences of 8192 keys, one node: bf16 d = 128 90 us (5.9 TB/s, 91 %),
-//     d = 64 53 us (77 %); e4m3 d = 128 55 us (76 %), d = 64 44 us (47 %:
-//     bound by a tile's chain of steps, not by its bytes)
-//   32 ragged sequences of up to 16 k keys, e4m3: 121 us (86 %)
-//   16 ragged trees of 16 nodes over up to 8 k keys, bf16: 73 us (73 %; 64 rows,
+//   16 sequences of 8192 keys, one node: bf16 d = 128 88 us (6.1 TB/s, 93 %),
+//     d = 64 51 us (80 %); e4m3 d = 128 54 us (77 %), d = 64 43 us (48 %:
+//     bound by a tile's chain of steps, not by its bytes); 16 nodes: bf16 101 us
+//     (81 %), e4m3 121 us (34 %: softmax instructions)
+//   32 ragged sequences of up to 16 k keys, e4m3: 113 us (92 %)
+//   16 ragged trees of 16 nodes over up to 8 k keys, bf16: 71 us (75 %; 64 rows,
 //     2 to 3 pieces per CTA whose queries and results cost about 3 tiles each)
-//   8 trees of 64 nodes over 2000 keys, 12 heads of 64, T5: 33 us (18 %: per
+//   8 trees of 64 nodes over 2000 keys, 12 heads of 64, T5: 31 us (19 %: per
 //     piece and softmax instructions)
-//   one sequence of 4096 keys: 13 us (setup 1.2, queries 1.8, tiles, result 1.2,
+//   1000 sequences of 500 keys, one node, bf16: 402 us (78 %)
+//   one sequence of 4096 keys: 12.5 us (setup 1.2, queries 1.8, tiles, result 1.2,
 //     joining kernel 3: a chain of latencies)
 // The same with mma.sync and rows as tile rows: 150, 105, 50 us (32 sequences,
 // 16 trees, 8 trees).
@@ -1605,10 +1608,12 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(const __
 // More sequences: most of their pieces lie inside one CTA's part of the line,
 // and each warp of the form above would go through all lengths for nothing.
 // Here blockIdx.y + 1 names a CTA; if its part begins inside a piece that began
-// in the CTA before, that piece is joined, a warp per query row.  Measured with
-// the search of the lengths in one warp and the form above against this: 1000
-// sequences of 1 node over 500 keys 633 -> 578 us, 256 of 8 nodes over 1000 keys
-// 255 -> 217, 256 of 1 node 193 -> 195, 64 of 1 node 64 -> 67.
+// in the CTA before, that piece is joined, a warp per query row.  The form above
+// ends at the 32 sequences that one warp's lanes hold; a loop over more of them in
+// each warp, with the search of the lengths in one warp, against this, when it
+// came: 1000 sequences of 1 node over 500 keys 633 -> 578 us, 256 of 8 nodes over
+// 1000 keys 255 -> 217, 256 of 1 node 193 -> 195, 64 of 1 node 64 -> 67: one form
+// for all that are more, though up to some 256 single nodes it gains nothing.
 // (32 registers and no more: a block has to find room beside the first
 // kernel's, to be waiting when it ends.)
 constexpr int kTreeCutWarps = 4;
