@@ -1316,7 +1316,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_fwd_kernel(
         }
 
         uint8_t* pbuf = smem + L::kPOff + x * L::kPBytes + me * 16;
-        const float v_up = e8m0_float(v_byte);
+        const float v_up = e8m0_float(min(v_byte, 254u));  // (finite, also of a hidden row that holds anything)
         const uint64_t up2 = f2_pack(v_up, v_up);
 #pragma unroll
         for (int j = 0; j < RT; j += 2) {

@@ -269,3 +269,26 @@ def test_values_of_one_size_after_values_of_another(nodes, copies, sizes):
     q = torch.randn(nodes, 1, d, generator=g).bfloat16().to(DEV)
     o, lse = attend(q, cache, table, n - nodes, copies)
     check_tree(o, lse, q, [(*rows, n - nodes)], [0, nodes], "e4m3")
+
+
+@pytest.mark.parametrize("byte", [255, 254, 0, 127])
+@pytest.mark.parametrize("codes", [0x7F, 0x00, 0x7E])
+@pytest.mark.parametrize("nodes", [1, 5, 40])
+def test_hidden_rows_may_hold_any_codes_and_scales(nodes, codes, byte):
+    """Keys behind the window, a node that none sees and the rest of the last page."""
+    g = torch.Generator().manual_seed(nodes)
+    ctx, d, page = 500, 64, 64
+    n = ctx + nodes + 1
+    k, v = torch.randn(n, 1, d, generator=g), torch.randn(n, 1, d, generator=g)
+    cache, table, rows = filled(k, v, page=page)
+    q = torch.randn(nodes + 1, 1, d, generator=g).bfloat16().to(DEV)
+    words = [(2 << i) - 1 for i in range(nodes)] + [(1 << nodes) - 1]       # a chain; the last node sees it alone
+    mask = torch.tensor(words, device=DEV)
+    wild = list(range(ctx - 100)) + list(range(n - 1, cache["k_cache"].shape[0] * page))
+    at = torch.tensor(wild, device=DEV)
+    for name in ("k", "v"):
+        cache[name + "_cache"].view(torch.uint8)[at // page, 0, at % page] = codes
+        cache[name + "_scale"][at // page, 0, at % page] = byte
+    got = attend(q, cache, table, ctx, tree_mask=mask, window_left=100)
+    assert torch.isfinite(got[0]).all()
+    check_tree(*got, q, [(*rows, ctx)], [0, nodes + 1], "e4m3", words, window_left=100)
