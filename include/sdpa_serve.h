@@ -113,7 +113,9 @@ typedef struct sdpa_kv_cache {
 /*
  * Writes T rows of bf16 K and V [T, Hkv, d] (element strides kv_t, kv_h,
  * multiples of 8, the same for both; d contiguous) into the cache, row t at
- * slots[t] = page * page_size + row in the page.  A negative slot skips its
+ * slots[t] = page * page_size + row in the page.  v NULL: K alone (and V alone,
+ * with strides of its own, by a second call that gives the cache's v and
+ * v_scale as its k and k_scale).  A negative slot skips its
  * row (padding); a slot past the cache is skipped and reported by
  * sdpa_serve_read_device_status as SDPA_ERR_UNSUPPORTED.  Two rows of one call must
  * not name the same slot (its contents would be unspecified).  e4m3: the scale

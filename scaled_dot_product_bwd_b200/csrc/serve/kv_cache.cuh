@@ -86,8 +86,8 @@ struct AppendArgs {
   int rows;  // per CTA, <= kCacheRows
 };
 
-// Both kernels: a CTA takes `rows` rows of K (blockIdx.y = 0) or V with all
-// heads.  Its first threads find where each row lies in the cache; then a
+// Both kernels: a CTA takes `rows` rows of K (blockIdx.y = 0) or V (1, where
+// there is one) with all heads.  Its first threads find where each row lies in the cache; then a
 // thread keeps one 16-byte piece of one head (several when the heads are
 // many) and goes through the rows, four in flight.
 constexpr int kCacheThreads = 256;

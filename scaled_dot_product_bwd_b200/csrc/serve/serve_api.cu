@@ -382,8 +382,8 @@ sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const
   if (st != SDPA_OK) return st;
   if (T < 0) return SDPA_ERR_INVALID_ARG;
   if (T == 0) return SDPA_OK;
-  if (!k || !v || !aligned16(k) || !aligned16(v) || !slots ||
-      (reinterpret_cast<uintptr_t>(slots) & 7u) || !good_stride(kv_t, 8) || !good_stride(kv_h, 8))
+  if (!k || !aligned16(k) || !aligned16(v) || !slots || (reinterpret_cast<uintptr_t>(slots) & 7u) ||
+      !good_stride(kv_t, 8) || !good_stride(kv_h, 8))
     return SDPA_ERR_INVALID_ARG;
   if (T >= (1ll << 31)) return SDPA_ERR_UNSUPPORTED;
   a.k = static_cast<const __nv_bfloat16*>(k);
@@ -394,7 +394,7 @@ sdpa_status_t sdpa_cache_append(const sdpa_kv_cache* cache, const void* k, const
   a.slots = slots;
   a.rows = cache_rows(T);
   if (!a.rows) return SDPA_ERR_CUDA;
-  const dim3 g(static_cast<unsigned>((T + a.rows - 1) / a.rows), 2);
+  const dim3 g(static_cast<unsigned>((T + a.rows - 1) / a.rows), v ? 2 : 1);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->format == SDPA_CACHE_E4M3;
   if (cache->d == 128) {

@@ -249,12 +249,24 @@ PyObject* append(PyObject* const* a) {
   const at::Tensor &k = need(a[4], "k"), &v = need(a[5], "v"), &slots = need(a[6], "slots");
   void* stream = stream_of({cache.k, cache.v, cache.ks, cache.vs, &k, &v, &slots});
   rows(k, "k", 3);
-  alike(v, "v", k);
+  rows(v, "v", 3);
+  shaped(v, "v", k.sizes());
   const int64_t T = k.size(0);
   if (k.size(1) != cache.c.Hkv || k.size(2) != cache.c.d) refuse("k does not fit the cache's heads");
-  check(sdpa_cache_append(&cache.c, k.data_ptr(), v.data_ptr(), T, step(k, 0), step(k, 1),
-                          vec<int64_t>(slots, "slots", at::kLong, {T}), stream),
+  const int64_t* at = vec<int64_t>(slots, "slots", at::kLong, {T});
+  const bool alike = step(k, 0) == step(v, 0) && step(k, 1) == step(v, 1);
+  // (two calls: what the second would refuse is refused before the first)
+  if (!alike && (reinterpret_cast<uintptr_t>(v.data_ptr()) % 16 || step(v, 0) <= 0 || step(v, 0) % 8 ||
+                 step(v, 1) <= 0 || step(v, 1) % 8))
+    check(SDPA_ERR_INVALID_ARG, "sdpa_cache_append");
+  check(sdpa_cache_append(&cache.c, k.data_ptr(), alike ? v.data_ptr() : nullptr, T, step(k, 0), step(k, 1), at, stream),
         "sdpa_cache_append");
+  if (!alike) {  // V by itself, as the K of its part of the cache
+    sdpa_kv_cache values = cache.c;
+    values.k = cache.c.v;
+    values.k_scale = cache.c.v_scale;
+    check(sdpa_cache_append(&values, v.data_ptr(), nullptr, T, step(v, 0), step(v, 1), at, stream), "sdpa_cache_append");
+  }
   Py_RETURN_NONE;
 }
 

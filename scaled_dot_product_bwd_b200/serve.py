@@ -168,8 +168,8 @@ def sdpa_rope(q, k, freqs, positions=None, *, offset=0, interleaved=False, inver
 
 def sdpa_cache_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
     """Rows k, v [T, Hkv, d] into the cache at slots int64 [T] (page * page_size + row;
-    negative: skipped), quantised if the cache is e4m3 (see sdpa_cache_append).  v has k's
-    strides: slices of one fused QKV buffer go together, with k rotated in place (out_k=k)."""
+    negative: skipped), quantised if the cache is e4m3 (see sdpa_cache_append).  Where k and v differ
+    in strides (a rotated k, and v still a slice of a fused buffer) that is two launches."""
     (_bind or _load_bind()).append(k_cache, v_cache, k_scale, v_scale, k, v, slots)
 
 

@@ -3,7 +3,7 @@ a rejection, prompt chunks over a cached prefix."""
 import pytest
 import torch
 
-from scaled_dot_product_bwd_b200 import (sdpa_cache_append, sdpa_cache_gather, sdpa_fwd, sdpa_fwd_varlen,
+from scaled_dot_product_bwd_b200 import (SdpaError, sdpa_cache_append, sdpa_cache_gather, sdpa_fwd, sdpa_fwd_varlen,
                                          sdpa_read_device_status, sdpa_rope, sdpa_rope_frequencies,
                                          sdpa_spec_verify, sdpa_tree_fwd)
 from test_gpu_serve import DEV, check_verify, draw_tree, make_cache, randn, tree_setup
@@ -162,3 +162,34 @@ def test_a_generation_step_in_a_graph(kv):
         graph.replay()
         kept = [t.clone() for t in out]
         assert all(torch.equal(a, b) for a, b in zip(kept, step()))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [1, 5, 700])
+def test_append_of_a_rotated_key_and_a_slice_of_a_fused_buffer(T, kv):
+    """K fresh from the rotation, V and slots as they are: what an append of copies gives."""
+    g = torch.Generator().manual_seed(T)
+    hq, hkv, d, page = 4, 2, 64, 16
+    freqs, _ = sdpa_rope_frequencies(d)
+    qkv = randn(g, T, hq + 2 * hkv, d)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    _, k = sdpa_rope(q, k, freqs)
+    assert T == 1 or k.stride() != v.stride()
+    pages = T // page + 2
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    slots[:1] = -1 if T > 1 else slots[:1]
+    a, b = make_cache(pages, hkv, page, d, kv), make_cache(pages, hkv, page, d, kv)
+    sdpa_cache_append(k, v, slots.to(DEV), **a)
+    sdpa_cache_append(k, v.contiguous(), slots.to(DEV), **b)
+    raw = lambda t: t.view(torch.int16 if t.dtype == torch.bfloat16 else torch.uint8)
+    for name in a:
+        assert a[name] is None or torch.equal(raw(a[name]), raw(b[name])), name
+    for bad in (v.float(), v[:, :1], v[:0] if T > 1 else v[:, :, :32]):
+        with pytest.raises(ValueError):
+            sdpa_cache_append(k, bad, slots.to(DEV), **a)
+    # refused before K is written: a base off by 8 bytes, rows of one stride of 0
+    odd = torch.zeros(T, 2 * hkv, d + 8, device=DEV, dtype=torch.bfloat16)[:, :hkv, 4:4 + d]
+    for bad in (odd, v[:1, :1].expand(T, hkv, d)):
+        with pytest.raises(SdpaError):
+            sdpa_cache_append(torch.full_like(k, 5.0), bad, slots.to(DEV), **a)
+    assert torch.equal(raw(a["k_cache"]), raw(b["k_cache"]))

@@ -61,3 +61,14 @@ def test_a_row_stride_of_zero_passes_the_checks_and_one_below_the_width_does_not
         assert (lib.sdpa_tree_fwd_workspace_size(ctypes.byref(t), ctypes.byref(c)) > 0) == (step == 0)
     r = _rope(pos_b=0)
     assert lib.sdpa_rope(ctypes.byref(r), FAKE, FAKE, FAKE, NULL, None) == 1      # (for k_out)
+
+
+def test_append_of_keys_alone_passes_the_checks_of_its_pointers():
+    import ctypes
+
+    from test_serve_abi import FAKE, NULL, _cache
+    lib = serve.load_serve_library()
+    c = _cache()
+    call = lambda k, v, T: lib.sdpa_cache_append(ctypes.byref(c), k, v, T, 128, 64, FAKE, None)
+    assert call(FAKE, NULL, 1 << 31) == 2                    # (refused for T, after them)
+    assert call(NULL, FAKE, 4) == call(NULL, NULL, 4) == call(FAKE, ctypes.c_void_p(0x10008), 4) == 1
