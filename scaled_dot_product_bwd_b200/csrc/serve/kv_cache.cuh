@@ -9,9 +9,9 @@
 //
 // Both kernels are bound by DRAM (append, e4m3: 2 bytes read and 1 written
 // per element; gather the reverse).  Measured: append of 32 k rows of 8 heads of
-// 128 as e4m3 41 us, 4.8 TB/s (73 % of a copy's rate; eight rows in flight per
-// thread instead of four 43 us; CTAs that stay and walk the rows with the next
-// rows' places read ahead 49 us); gather of 485 MB, two thirds of it written,
+// 128 as e4m3 42 us, 4.7 TB/s (71 % of a copy's rate; tried beside 41 us on
+// another day: eight rows in flight per thread instead of four 43 us, CTAs that
+// stay and walk the rows with the next rows' places read ahead 49 us); gather of 485 MB, two thirds of it written,
 // 104 us, 4.7 TB/s (a plain fill of this GPU's memory reaches 3.8 TB/s, at which
 // the written part alone takes 85 us); calls of a few rows 3 - 5 us, latency.
 // A row is spread over the lanes of a part
